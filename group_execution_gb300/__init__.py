@@ -6,7 +6,9 @@ A thin Python layer over libgroupexec.so (C ABI in include/groupexec.h):
 * ``Plan``   -- FuseOps-style grouping of a graph, one CUDA kernel per group
                 (``launch_group``) or per operator (``launch_unfused``);
 * ``TensorFusion`` -- pack many float32 gradients into one bf16 fusion buffer
-                and unpack them again, one kernel each.
+                and unpack them again, one kernel each;
+* ``TrainingOps`` -- layer norm, 8-bit activation checkpoints (``Checkpoint``)
+                and token log probabilities, with their gradients.
 
 PyTorch supplies device memory and streams only; every step runs in the
 library's kernels.  There is no CPU fallback.
@@ -19,7 +21,15 @@ from . import _lib
 from ._lib import FgError, OPCODES, EXEC_KINDS, FG_F32, FG_BF16  # noqa: F401
 
 __all__ = ["Graph", "Plan", "Partition", "TensorFusion", "FgError", "OPCODES", "graph_from_spec", "plan_threshold",
-           "merge_buckets", "simulate"]
+           "merge_buckets", "simulate", "TrainingOps", "Checkpoint", "checkpoint_layout"]
+
+
+def __getattr__(name):
+    # loaded on first use: the rest of the package imports without PyTorch
+    if name in ("TrainingOps", "Checkpoint", "checkpoint_layout"):
+        from . import training
+        return getattr(training, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def _i32a(xs):

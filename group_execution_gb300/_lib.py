@@ -91,6 +91,19 @@ SIGNATURES = {
     "tf_bucket_wait": (_I32, [_P, _I32, _P]),
     "tf_bucket_ready": (_I32, [_P, _I32, _P]),
     "tf_layout_destroy": (None, [_P]),
+    "ts_create": (_I32, [_I64, _P]),
+    "ts_sync_status": (_I32, [_P, _P]),
+    "ts_destroy": (None, [_P]),
+    "ts_layer_norm": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _F, _P, _I32, _I64, _P, _P, _P, _P]),
+    "ts_layer_norm_backward": (_I32, [_P, _P, _I32, _I64, _P, _I32, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I32, _I64,
+                                      _P, _P, _I32, _P]),
+    "ts_checkpoint_layout": (_I32, [_I64, _I64, _PI64, _PI64, _PI64]),
+    "ts_checkpoint_save": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P]),
+    "ts_checkpoint_load": (_I32, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "ts_activation_backward": (_I32, [_P, _I32, _P, _I32, _I64, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "ts_weight_grad": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I32, _I64, _I64, _P, _I64, _P, _I32, _P]),
+    "ts_token_logprobs": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _P]),
+    "ts_token_logprobs_backward": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P]),
 }
 
 _lock = threading.Lock()

@@ -21,8 +21,8 @@
  *     raw DEVICE pointers (float32 or bfloat16, row-major, contiguous) and a
  *     CUDA stream as `void*` (NULL = legacy default stream).  The library owns
  *     graphs, plans and layouts and the small device tables they hold; it
- *     allocates device memory only in fg_build_groups / tf_layout_create,
- *     never in a launch, and frees it in the matching *_destroy.
+ *     allocates device memory only in fg_build_groups / tf_layout_create /
+ *     ts_create, never in a launch, and frees it in the matching *_destroy.
  *   - Launches are asynchronous on the given stream.  Argument, shape and
  *     alignment errors are returned synchronously (tensors 16-byte aligned,
  *     fusion buffer 256-byte aligned).  CUDA launch errors map to FG_ECUDA.
@@ -527,6 +527,117 @@ fg_status tf_pack_buckets_observed(tf_layout* l, float scale, void* fusion_buf, 
                                    uint32_t seq_offset, int64_t wait_limit_ns, void* cuda_stream);
 
 void tf_layout_destroy(tf_layout* l);
+
+/* ---- training-step operators ------------------------------------------------
+ * What a training step runs between its operator groups and the packing of
+ * its gradients: layer norm, 8-bit activation checkpoints with the gradients
+ * that read them, and the log probabilities of a step's tokens.  The pages
+ * have no counterpart.
+ *
+ * Matrices are row major, FG_F32 or FG_BF16, with a row pitch in elements (ld
+ * >= columns) and any alignment to their element (rows that all start on 16
+ * bytes run faster); vectors and row statistics are dense float32.  All
+ * arithmetic and all sums are in float32; a bf16 output is rounded once.  No
+ * output may overlap an input except where stated.  rows = 0 computes empty
+ * sums; cols is at least 1.  Results do not depend on scheduling: no sum uses
+ * atomics.
+ *
+ * A ts_ops handle belongs to the device that is current in ts_create (calls
+ * with another current device return FG_EINVAL) and owns a workspace and a
+ * device error word.  Like a plan's, launches of one handle must be ordered:
+ * for concurrent streams, create one handle each.  Device memory is allocated
+ * in ts_create only. */
+typedef struct ts_ops ts_ops;
+
+/* workspace_bytes: 0 for the default (64 MiB), at least 1 MiB.  The workspace
+ * bounds how far a sum over rows is split, never what is computed; the
+ * gradients need 16 bytes a column of dy (FG_EUNSUPPORTED otherwise). */
+fg_status ts_create(int64_t workspace_bytes, ts_ops** out);
+
+/* Synchronises the stream, then reads and clears the handle's error word:
+ * FG_ETIMEOUT when a bounded wait (2 s) of a ts_weight_grad kernel expired;
+ * that call's dw is incomplete. */
+fg_status ts_sync_status(ts_ops* h, void* cuda_stream);
+
+void ts_destroy(ts_ops* h);
+
+/* Layer norm: y = gamma * (x - mean) * rstd + beta by row, with rstd =
+ * 1 / sqrt(var + eps) and var the mean squared distance from the mean.  gamma
+ * and beta [cols] may be NULL (1 and 0); mean and rstd [rows] may be NULL
+ * where the gradient is not wanted.  checkpoint, if not NULL, receives the
+ * normalised rows (x - mean) * rstd as an 8-bit checkpoint.  y may be x when
+ * dtype and pitch agree. */
+fg_status ts_layer_norm(ts_ops* h, const void* x, fg_dtype x_dtype, int64_t ldx, int64_t rows, int64_t cols,
+                        const float* gamma, const float* beta, float eps, void* y, fg_dtype y_dtype, int64_t ldy,
+                        float* mean, float* rstd, void* checkpoint, void* cuda_stream);
+
+/* Its gradient, from x (then mean is needed and dx has x's dtype) or from the
+ * checkpoint of the normalised rows (then x is NULL): dx = rstd * (u -
+ * mean(u) - n * mean(u * n)) with u = dy * gamma and n the normalised row;
+ * dgamma = column sums of dy * n and dbeta of dy, either may be NULL, added
+ * to what they hold when accumulate = 1.  dx may be dy when dtype and pitch
+ * agree. */
+fg_status ts_layer_norm_backward(ts_ops* h, const void* dy, fg_dtype dy_dtype, int64_t lddy, const void* x,
+                                 fg_dtype x_dtype, int64_t ldx, const void* checkpoint, int64_t rows, int64_t cols,
+                                 const float* gamma, const float* mean, const float* rstd, void* dx,
+                                 fg_dtype dx_dtype, int64_t lddx, float* dgamma, float* dbeta, int32_t accumulate,
+                                 void* cuda_stream);
+
+/* An 8-bit checkpoint of a [rows, cols] matrix is one 16-byte aligned buffer
+ * in the OCP microscaling layout with int8 elements: rows of `pitch` int8
+ * values (cols rounded up to 128, zeros past cols), then at scale_offset
+ * rows of pitch / 32 scale bytes.  Value c of a row is q[c] * 2^(E - 133),
+ * E = scale[c / 32], which is exact in bf16.  E is the exponent field of the
+ * block's largest magnitude, at least 7; q is rounded to nearest even and
+ * clamped to +-127.  A block that holds an infinity or a NaN has E = 255 and
+ * reads as NaN.  Host only; any output may be NULL. */
+fg_status ts_checkpoint_layout(int64_t rows, int64_t cols, int64_t* pitch, int64_t* scale_offset, int64_t* bytes);
+
+/* Saves x as a checkpoint; writes a checkpoint's values to y. */
+fg_status ts_checkpoint_save(ts_ops* h, const void* x, fg_dtype x_dtype, int64_t ldx, int64_t rows, int64_t cols,
+                             void* checkpoint, void* cuda_stream);
+fg_status ts_checkpoint_load(ts_ops* h, const void* checkpoint, int64_t rows, int64_t cols, void* y, fg_dtype y_dtype,
+                             int64_t ldy, void* cuda_stream);
+
+/* The gradient of an activation from the checkpoint of its OUTPUT a: dx = dy *
+ * f', with f' = (a > 0) for FG_OP_RELU, a (1 - a) for FG_OP_SIGMOID and
+ * 1 - a^2 for FG_OP_TANH.  A relu output below half a step is saved as 0 and
+ * passes no gradient.  dx may be dy when dtype and pitch agree. */
+fg_status ts_activation_backward(ts_ops* h, int32_t opcode, const void* dy, fg_dtype dy_dtype, int64_t lddy,
+                                 const void* checkpoint, int64_t rows, int64_t cols, void* dx, fg_dtype dx_dtype,
+                                 int64_t lddx, void* cuda_stream);
+
+/* A matmul's weight gradient from its saved input: dw [cols, n] float32 = X^T
+ * dy over the rows, dy [rows, n] bf16, X the checkpoint's values, or, with
+ * gamma and/or beta [cols], gamma * values + beta (the input of a matmul
+ * behind a layer norm).  db [n], if not NULL, receives dy's column sums (the
+ * bias gradient).  accumulate = 1 adds to what dw and db hold.  At most 2^20
+ * rows and columns of dw. */
+fg_status ts_weight_grad(ts_ops* h, const void* checkpoint, int64_t rows, int64_t cols, const float* gamma,
+                         const float* beta, const void* dy, fg_dtype dy_dtype, int64_t lddy, int64_t n, float* dw,
+                         int64_t lddw, float* db, int32_t accumulate, void* cuda_stream);
+
+/* One pass over rows of logits [rows, vocab]: lse = log sum exp, logprob =
+ * logits[tokens[r]] - lse, entropy of the distribution, and the k (0 to 32)
+ * largest logits in falling order as log probabilities with their columns
+ * (ties: lowest column first), top_* [rows, k].  Any output may be NULL
+ * (top_* only with k = 0; tokens only without logprob).  A token outside
+ * 0 .. vocab - 1 leaves its row unscored: logprob 0.  A -inf logit has
+ * probability 0; a row of nothing else has lse and log probabilities -inf and
+ * entropy 0.  A row with a NaN or +inf gives NaN; NaN logits rank first. */
+fg_status ts_token_logprobs(ts_ops* h, const void* logits, fg_dtype dtype, int64_t ld, int64_t rows, int64_t vocab,
+                            const int64_t* tokens, float* logprob, float* entropy, float* lse, int32_t k,
+                            float* top_logprob, int32_t* top_id, void* cuda_stream);
+
+/* Its gradient: dlogits = g_logprob * (onehot(token) - p) - g_entropy * p *
+ * (log p + entropy), p = exp(logits - lse), from the lse and entropy it wrote.
+ * g_entropy may be NULL (then entropy may be too).  An unscored row takes
+ * only the entropy's part; a row of -inf logits takes none.  dlogits may be
+ * logits when dtype and pitch agree. */
+fg_status ts_token_logprobs_backward(ts_ops* h, const void* logits, fg_dtype dtype, int64_t ld, int64_t rows,
+                                     int64_t vocab, const int64_t* tokens, const float* lse, const float* entropy,
+                                     const float* g_logprob, const float* g_entropy, void* dlogits, fg_dtype d_dtype,
+                                     int64_t ldd, void* cuda_stream);
 
 #ifdef __cplusplus
 }

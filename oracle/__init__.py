@@ -32,6 +32,8 @@ out from the passages they cite:
 * ``simulate``  -- the training-step simulator: ready queue, in-order
                    AllReduce channel, linear AllReduce time (DisCo,
                    Simulator and Profiler).
+* ``training``  -- layer norm, 8-bit activation checkpoints, token log
+                   probabilities and their gradients, in float64.
 
 Parity status: every function here is pinned by tests under ``tests/``
 (``-m "not gpu"``) against brute force, closed forms, worked examples from the
@@ -39,4 +41,4 @@ pages or library routines.  The composition of operators in ``execute`` is
 pinned against an independent element-by-element evaluator on small random
 DAGs; the full-size chains rely on that composition and the per-operator pins.
 """
-from . import kinds, postdom, partition, execute, pack, buckets, explicit, patterns, simulate  # noqa: F401
+from . import kinds, postdom, partition, execute, pack, buckets, explicit, patterns, simulate, training  # noqa: F401
