@@ -1,8 +1,46 @@
 // A matmul's weight gradient from its 8-bit saved input: dW = X^T dY over the
 // rows (tokens).  With an affine input X = gamma h + beta by column, h the
 // checkpoint,
-//   dW_cj = gamma_c sum_t h_tc dY_tj + beta_c db_j,   db_j = sum_t dY_tj.
+//   dW_cj = gamma_c sum_t h_tc dY_tj + beta_c db_j,   db_j = sum_t dY_tj,
+// so the product is of h alone and gamma and beta enter in the epilogue.
+//
+// The product runs on the 5th-generation tensor cores.  A checkpoint's values
+// are exact in bf16, so the products are exact and the sums are float32:
+// bf16 operands cost no accuracy.  Persistent CTA pairs walk 256 x 256 tiles
+// of dW (2-SM tcgen05.mma, cta_group::2), tokens 64 at a time; each CTA
+// stages half of the tile's columns of h and half of its columns of dY in a
+// ring of shared-memory slots, both MN-major, 128-byte swizzled.  Warps, in
+// each CTA:
+//   warp 0      TMA producer of its dY half (counted on the even CTA's slot
+//               barrier),
+//   warp 1      allocates TMEM (two accumulators) and, in the even CTA,
+//               issues the MMAs from one thread,
+//   warps 2-5   epilogue: a thread owns one row of the CTA's 128 x 256
+//               accumulator; it overlaps the next tile's MMAs,
+//   warp 6      fetches the checkpoint: int8 values by TMA, scale bytes by
+//               4-byte asynchronous copies, into a ring of its own,
+//   warps 7-14  two sets of four that take alternate slots: expand int8 to
+//               bf16, scale, and store the operand, swizzled.
+// A float32 accumulator that takes all 8192 tokens one MMA after the other is
+// 2.8e-6 off (2-norm): the tensor core truncates as it adds.  So a sum runs
+// over at most 2048 tokens; what it came to is added to a float32 partial in
+// the workspace, which the same thread of the same pair reads back (L2).
+//
+// Tiles past the last full round of pairs are cut along the tokens when that
+// balances the round: each piece writes its float32 partial to the workspace
+// and a second kernel adds the pieces in order.
+//
+// Rows of dY that TMA cannot read (a start or pitch off 16 bytes) are first
+// copied to the workspace at an aligned pitch, as many tokens at a time as
+// fit there.
+//
+// Every wait is bounded; on expiry the CTA records the error, drains its
+// copies, frees its TMEM and returns.
+#include <cuda.h>
+
 #include <algorithm>
+#include <atomic>
+#include <mutex>
 
 #include "launch.h"
 #include "ts_device.cuh"
@@ -10,60 +48,621 @@
 namespace fg {
 namespace {
 
-// The simplest form: a 32 x 32 tile of dW a block, 32 tokens at a time
-// through shared memory.
-__global__ void __launch_bounds__(256) ts_wgrad_kernel(const WgradArgs a, const float* colsum) {
-  __shared__ float xs[32][33], ys[32][33];
+constexpr int kTile = 256;                       // rows and columns of dW a pair's tile covers
+constexpr int kHalf = kTile / 2;                 // ... and one CTA stages of each operand
+constexpr int kKB = 64;                          // tokens a ring slot holds
+constexpr int kOperandBytes = kHalf * kKB * 2;   // 16 KB
+constexpr int kSlotBytes = 2 * kOperandBytes;
+constexpr int kSlots = 5;
+constexpr int kRawBytes = kKB * kHalf;           // a slot's checkpoint values, 8 KB
+constexpr int kRawScales = kKB * 4;              // and its scale bytes
+constexpr int kRaw = 6;
+constexpr int kExpandWarps = 8;                  // two sets of four
+constexpr int kThreads = (7 + kExpandWarps) * 32;
+constexpr int kSmem = kSlots * kSlotBytes + kRaw * (kRawBytes + kRawScales) + 1024;
+constexpr int kChain = 32;                       // token blocks one accumulation runs over
+constexpr int64_t kWaitNs = 2000000000LL;
+constexpr int64_t kPieceFloats = (int64_t)kTile * kTile;
+
+struct WgradKernel {
+  CUtensorMap dy, q;
+  const uint8_t* scale;
+  int64_t spitch;      // scale bytes a row
+  int rows, cols, n;
+  int tiles_n;         // tiles along n; tile t covers columns of h from (t / tiles_n) * kTile
+  int full, pieces;    // tiles taken whole, and pieces per later tile
+  int items;           // full + pieces * (tiles - full)
+  const float* gamma;
+  const float* beta;
+  const float* colsum;
+  float* dw;
+  int64_t lddw;
+  int accumulate;
+  float4* part;        // the cut tiles' pieces
+  float4* chain;       // each pair's running partial
+  int32_t* err;
+};
+
+struct Item {
+  int tile, piece, kb0, kb1;   // piece = -1: a whole tile
+};
+__device__ __forceinline__ Item item_of(const WgradKernel& P, int idx, int nkb) {
+  if (idx < P.full) return Item{idx, -1, 0, nkb};
+  const int q = idx - P.full, p = q % P.pieces;
+  if (P.pieces == 1) return Item{P.full + q, -1, 0, nkb};
+  return Item{P.full + q / P.pieces, q, (int)((int64_t)nkb * p / P.pieces), (int)((int64_t)nkb * (p + 1) / P.pieces)};
+}
+
+// What one accumulator takes of an item: token blocks [kb0, kb1).
+__device__ __forceinline__ int segment_end(const Item& w, int kb0) {
+  return w.kb1 - kb0 > kChain ? kb0 + kChain : w.kb1;
+}
+
+// Waits for the phase with the given parity, at most kWaitNs and only while
+// no thread of the CTA has given up.  Arrivals and data may come from the
+// pair's other CTA.
+__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait_cluster(bar, parity))
+    if (*abort_flag || (int64_t)(global_ns() - t0) > kWaitNs) return false;
+  return true;
+}
+// Four int8 values -> two bf16 pairs, times a power of two, exactly: with
+// byte b under 0x43 (a bf16 of exponent 2^7), 0x4300 | (b & 127) is 128 + (b &
+// 127) and 0x4300 | (b & 128) is 128 or 256, and their difference is b as a
+// signed number.
+__device__ __forceinline__ void expand4(uint32_t w, __nv_bfloat162 step, uint32_t& lo, uint32_t& hi) {
+  const uint32_t a = __byte_perm(w, 0x43434343u, 0x4140), b = __byte_perm(w, 0x43434343u, 0x4342);
+  const uint32_t am = a & 0xff7fff7fu, as = a & 0xff80ff80u, bm = b & 0xff7fff7fu, bs = b & 0xff80ff80u;
+  const __nv_bfloat162 l = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&am),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&as)), step);
+  const __nv_bfloat162 h = __hmul2(__hsub2(*reinterpret_cast<const __nv_bfloat162*>(&bm),
+                                           *reinterpret_cast<const __nv_bfloat162*>(&bs)), step);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ __nv_bfloat162 bf16_step(uint32_t e) {
+  const uint32_t h = e < 255 ? (max(e, 7u) - 6) << 7 : 0x7fc0u, w = h | h << 16;
+  return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+// Stores eight values of one row of dw from column j (vec: 8, 4 or 1 floats
+// at a time), scaled, shifted and accumulated as asked.
+__device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j, float g, float b, int vec,
+                                        float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] *= g;
+  if (b != 0.f || P.beta) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < P.n) v[i] += b * P.colsum[j + i];
+  }
+  float* d = row + j;
+  if (vec == 8 && j + 8 <= P.n) {
+    if (P.accumulate) {
+      float o[8];
+      load8(d, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = o[i] + v[i];
+    }
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else if (vec >= 4 && j + 8 <= P.n) {
+    if (P.accumulate) {
+      float o[8];
+      load8(d, o);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = o[i] + v[i];
+    }
+    store8(d, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (j + i < P.n) d[i] = P.accumulate ? d[i] + v[i] : v[i];
+  }
+}
+__device__ __forceinline__ int store_width(const WgradKernel& P) {
+  const uint64_t p = reinterpret_cast<uint64_t>(P.dw);
+  return p % 32 == 0 && P.lddw % 8 == 0 ? 8 : p % 16 == 0 && P.lddw % 4 == 0 ? 4 : 1;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ts_wgrad_kernel(const __grid_constant__ WgradKernel P) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 2 * kRaw + 5];
+  __shared__ int abort_flag, issued, raw_issued;
+  __shared__ uint32_t tmem_slot;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
+                 tempty0 = tfull0 + 16, done_bar = tempty0 + 16, rfull0 = done_bar + 8,
+                 rempty0 = rfull0 + 8 * kRaw;
+  uint8_t* raw = ring + kSlots * kSlotBytes;
+  uint8_t* raw_scale = raw + kRaw * kRawBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)cluster_ctarank();
+  const bool leader = h == 0;
+  const uint16_t pair_mask = 3u;
+  const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int nkb = (P.rows + kKB - 1) / kKB;
+  if (threadIdx.x == 0) {
+    abort_flag = issued = raw_issued = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(full0 + 8 * s, 1 + kExpandWarps);   // the even CTA's expect_tx, a set of four in each CTA
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int s = 0; s < kRaw; ++s) {
+      mbar_init(rfull0 + 8 * s, 1 + 32);   // the TMA's bytes, every lane's scale copies
+      mbar_init(rempty0 + 8 * s, kExpandWarps / 2);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 8);   // the epilogue warps of the pair
+    }
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
   pdl_launch_dependents();
   pdl_wait();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int c0 = blockIdx.x * 32, j0 = blockIdx.y * 32;
-  float acc[4] = {};
-  for (int64_t t0 = 0; t0 < a.rows; t0 += 32) {
-    for (int i = ty; i < 32; i += 8) {
-      const int64_t t = t0 + i;
-      const int c = c0 + tx, j = j0 + tx;
-      xs[i][tx] = t < a.rows && c < a.cols
-                      ? (float)a.x.q[t * a.x.pitch + c] * ckpt_step(a.x.scale[(t * a.x.pitch + c) / kCkptBlock])
-                      : 0.f;
-      ys[i][tx] = t < a.rows && j < a.n
-                      ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.dy.p)[t * a.dy.ld + j])
-                      : 0.f;
-    }
-    __syncthreads();
+
+  if (warp == 0) {
+    // ---- dY producer ----
+    if (lane == 0) {
+      tma_prefetch(&P.dy);
+      const uint64_t keep = l2_evict_last();
+      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + kOperandBytes;
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int x = pair; x < P.items && ok; x += npair) {
+        const Item w = item_of(P, x, nkb);
+        const int n0 = w.tile % P.tiles_n * kTile + h * kHalf;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (it >= kSlots && !wait_pair(empty0 + 8 * s, ph ^ 1, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (leader) mbar_expect_tx(full0 + 8 * s, 2 * kOperandBytes);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      for (int i = 0; i < 32; ++i) acc[k] += xs[i][ty + 8 * k] * ys[i][tx];
-    __syncthreads();
-  }
-  const int j = j0 + tx;
+          for (int g = 0; g < kHalf / 64; ++g)
+            tma_load_2d_pair(dst0 + s * kSlotBytes + g * 8192, &P.dy, n0 + 64 * g, kb * kKB, cbar0 + 8 * s, keep);
+          ++it;
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      issued = it;
+      if (!ok) {
+        abort_flag = 1;
+        set_error(P.err, DEVERR_TIMEOUT);
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    if (lane == 0 && leader) {
+      const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 1, 1);
+      // MN-major: atoms of 64 columns x 8 tokens, 64-column groups 8 KB apart
+      const uint32_t base = smem_u32(ring);
+      const uint64_t ad0 = smem_desc_sw128(base, 8192, 1024), bd0 = smem_desc_sw128(base + kOperandBytes, 8192, 1024);
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int x = pair; x < P.items && ok; x += npair) {
+        const Item w = item_of(P, x, nkb);
+        for (int s0 = w.kb0; s0 < w.kb1 && ok; ++i) {
+          const int s1 = segment_end(w, s0), b = i & 1;
+          if (i >= 2 && !wait_pair(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          for (int kb = s0; kb < s1; ++kb) {
+            if (!wait_pair(full0 + 8 * s, ph, &abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t so = (uint32_t)(s * kSlotBytes) >> 4;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int c = c0 + ty + 8 * k;
-    if (c < a.cols && j < a.n) {
-      float v = acc[k];
-      if (a.gamma) v *= a.gamma[c];
-      if (a.beta) v += a.beta[c] * colsum[j];
-      float* d = a.dw + (int64_t)c * a.lddw + j;
-      *d = a.accumulate ? *d + v : v;
+            for (int kk = 0; kk < kKB / 16; ++kk)
+              tc_mma_bf16<2>(tmem + b * kTile, ad0 + so + kk * (2048 >> 4), bd0 + so + kk * (2048 >> 4), idesc,
+                             kb != s0 || kk != 0);
+            tc_commit_mask(empty0 + 8 * s, pair_mask);
+            if (++s == kSlots) {
+              s = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok) tc_commit_mask(tfull0 + 8 * b, pair_mask);
+          s0 = s1;
+        }
+      }
+      if (!ok) {
+        abort_flag = 1;
+        set_error(P.err, DEVERR_TIMEOUT);
+      }
+      // every MMA issued has completed before either CTA may free TMEM
+      tc_commit_mask(done_bar, pair_mask);
+      mbar_wait(done_bar, 0, kDrainLimitNs);
+    }
+  } else if (warp < 6) {
+    // ---- epilogue ----
+    const int q = warp & 3;   // the TMEM lane quarter this warp may access
+    const int r = q * 32 + lane;
+    const int vec = store_width(P);
+    // partials: [64 column quads][128 rows][4], so that a warp's 16-byte
+    // accesses cover 512 contiguous bytes
+    float4* chain = P.chain + (int64_t)(pair * 2 + h) * (kPieceFloats / 8) + r;
+    int i = 0;
+    bool ok = true;
+    for (int x = pair; x < P.items && ok; x += npair) {
+      const Item w = item_of(P, x, nkb);
+      const int c = w.tile / P.tiles_n * kTile + h * kHalf + r, n0 = w.tile % P.tiles_n * kTile;
+      const float g = P.gamma && c < P.cols ? P.gamma[c] : 1.f, be = P.beta && c < P.cols ? P.beta[c] : 0.f;
+      float* row = P.dw + (int64_t)c * P.lddw;
+      float4* piece = w.piece < 0 ? nullptr : P.part + (int64_t)(w.piece * 2 + h) * (kPieceFloats / 8) + r;
+      for (int s0 = w.kb0; s0 < w.kb1; ++i) {
+        const int s1 = segment_end(w, s0), b = i & 1;
+        ok = __all_sync(0xffffffffu, wait_pair(tfull0 + 8 * b, (i >> 1) & 1, &abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t acc0 = tmem + ((uint32_t)(q * 32) << 16) + b * kTile;
+        const bool first = s0 == w.kb0, last = s1 == w.kb1;
+        float4* dst = last ? piece : chain;
+#pragma unroll 1
+        for (int j = 0; j < kTile; j += 32) {
+          if (n0 + j >= P.n) break;
+          float4 o[8];
+          if (!first) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) o[k] = __ldcg(chain + (j / 4 + k) * kHalf);
+          }
+          float v[32];
+          tmem_ld32(acc0 + j, v);
+          if (!first) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              v[4 * k] += o[k].x;
+              v[4 * k + 1] += o[k].y;
+              v[4 * k + 2] += o[k].z;
+              v[4 * k + 3] += o[k].w;
+            }
+          }
+          if (dst) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              dst[(j / 4 + k) * kHalf] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          } else if (c < P.cols) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float e[8];
+#pragma unroll
+              for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
+              finish8(P, row, n0 + j + 8 * k, g, be, vec, e);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+        s0 = s1;
+      }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      set_error(P.err, DEVERR_TIMEOUT);
+    }
+  } else if (warp == 6) {
+    // ---- checkpoint fetch ----
+    const uint64_t keep = l2_evict_last();
+    int it = 0, s = 0;
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int x = pair; x < P.items && ok; x += npair) {
+      const Item w = item_of(P, x, nkb);
+      const int m0 = w.tile / P.tiles_n * kTile + h * kHalf;
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (it >= kRaw) {
+          ok = __all_sync(0xffffffffu, wait_pair(rempty0 + 8 * s, ph ^ 1, &abort_flag));
+          if (!ok) break;
+        }
+        const uint32_t bar = rfull0 + 8 * s;
+        if (lane == 0) {
+          mbar_expect_tx(bar, kRawBytes);
+          tma_load_2d_hint(smem_u32(raw + s * kRawBytes), &P.q, m0, kb * kKB, bar, keep);
+        }
+#pragma unroll
+        for (int u = 0; u < kKB / 32; ++u) {
+          // rows and columns outside the checkpoint: zero bytes, no access
+          const int k = lane + 32 * u, row = kb * kKB + k;
+          const bool in = row < P.rows && m0 / kCkptBlock < P.spitch;
+          const uint8_t* src = P.scale + (in ? (int64_t)row * P.spitch + m0 / kCkptBlock : 0);
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
+                           smem_u32(raw_scale + s * kRawScales + k * 4)),
+                       "l"(src), "r"(in ? 4 : 0)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        ++it;
+        if (++s == kRaw) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (lane == 0) {
+      raw_issued = it;
+      if (!ok) {
+        abort_flag = 1;
+        set_error(P.err, DEVERR_TIMEOUT);
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ---- expansion ----
+    // a slot's 64 tokens x 128 columns: thread t of a set takes tokens t / 8
+    // + 16 u, columns (t % 8) * 16 .. + 15
+    const int set = (warp - 7) >> 2, t = threadIdx.x - (7 + 4 * set) * 32, kr = t >> 3, jc = t & 7;
+    const uint32_t written0 = cluster_addr(full0, 0);
+    // the slot addresses of a thread's two 16-byte halves; lanes 4-7 of every
+    // eight store them in the other order, so that eight lanes cover all banks
+    const uint32_t g = (uint32_t)(jc >> 2) * 8192 + (uint32_t)kr * 128, first = (uint32_t)(jc >> 2);
+    const uint32_t c0 = (uint32_t)((jc & 3) * 2);
+    const uint32_t off_a = g + (((c0 + first) ^ (kr & 7)) << 4), off_b = g + (((c0 + (first ^ 1)) ^ (kr & 7)) << 4);
+    int it = 0;
+    bool ok = true;
+    for (int x = pair; x < P.items && ok; x += npair) {
+      const Item w = item_of(P, x, nkb);
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        if ((it & 1) != set) continue;
+        const int rs = it % kRaw, s = it % kSlots;
+        ok = __all_sync(0xffffffffu, wait_pair(rfull0 + 8 * rs, (it / kRaw) & 1, &abort_flag));
+        if (!ok) break;
+        uint4 v[4];
+        uint32_t e[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[u] = *reinterpret_cast<const uint4*>(raw + rs * kRawBytes + (kr + 16 * u) * kHalf + jc * 16);
+          e[u] = raw_scale[rs * kRawScales + (kr + 16 * u) * 4 + (jc >> 1)];
+        }
+        if (it >= kSlots) {
+          ok = __all_sync(0xffffffffu, wait_pair(empty0 + 8 * s, ((it / kSlots) & 1) ^ 1, &abort_flag));
+          if (!ok) break;
+        }
+        uint8_t* dst = ring + s * kSlotBytes;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const __nv_bfloat162 step = bf16_step(e[u]);
+          uint4 lo, hi;
+          expand4(v[u].x, step, lo.x, lo.y);
+          expand4(v[u].y, step, lo.z, lo.w);
+          expand4(v[u].z, step, hi.x, hi.y);
+          expand4(v[u].w, step, hi.z, hi.w);
+          *reinterpret_cast<uint4*>(dst + off_a + u * 16 * 128) = first ? hi : lo;
+          *reinterpret_cast<uint4*>(dst + off_b + u * 16 * 128) = first ? lo : hi;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(rempty0 + 8 * rs);
+          mbar_arrive_cluster(written0 + 8 * s);
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      set_error(P.err, DEVERR_TIMEOUT);
     }
   }
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0)
+    for (int k = raw_issued - kRaw < 0 ? 0 : raw_issued - kRaw; k < raw_issued; ++k)
+      mbar_wait(rfull0 + 8 * (k % kRaw), (k / kRaw) & 1, kDrainLimitNs);
+  if (abort_flag && leader && threadIdx.x == 0) {
+    // dY's copies in flight complete on the even CTA's barriers; the slots
+    // they fill may lack arrivals, so each wait may run to its limit
+    for (int k = issued - kSlots < 0 ? 0 : issued - kSlots; k < issued; ++k)
+      mbar_wait(full0 + 8 * (k % kSlots), (k / kSlots) & 1, kDrainLimitNs);
+  }
+  // no CTA leaves while its peer may still write to its shared memory or
+  // issue MMAs into its TMEM
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, 512);
+}
+
+// The cut tiles: a thread adds the pieces of one row's eight columns in order.
+__global__ void __launch_bounds__(256) ts_wgrad_finish_kernel(const __grid_constant__ WgradKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tile = P.full + blockIdx.x / 32, b = blockIdx.x % 32;   // 32 blocks a tile: 8 columns of all 256 rows each
+  const int h = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
+  const int c = tile / P.tiles_n * kTile + threadIdx.x, j = tile % P.tiles_n * kTile + b * 8;
+  if (c >= P.cols || j >= P.n) return;
+  float v[8] = {};
+  for (int p = 0; p < P.pieces; ++p) {
+    const float4* o =
+        P.part + (int64_t)((blockIdx.x / 32 * P.pieces + p) * 2 + h) * (kPieceFloats / 8) + b * 2 * kHalf + r;
+    const float4 x = __ldcg(o), y = __ldcg(o + kHalf);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+  finish8(P, P.dw + (int64_t)c * P.lddw, j, P.gamma ? P.gamma[c] : 1.f, P.beta ? P.beta[c] : 0.f, store_width(P), v);
+}
+
+// dy's rows at an aligned pitch.
+__global__ void __launch_bounds__(256) ts_repack_kernel(const __nv_bfloat16* src, int64_t ld, int64_t rows, int n,
+                                                        __nv_bfloat16* dst, int64_t pitch) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < n; j += (int64_t)gridDim.x * 256)
+      dst[r * pitch + j] = src[r * ld + j];
+}
+
+// dW of no tokens: beta's part is 0 too.
+__global__ void __launch_bounds__(256) ts_zero_kernel(float* dw, int64_t lddw, int cols, int n) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int c = blockIdx.y; c < cols; c += gridDim.y)
+    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < n; j += (int64_t)gridDim.x * 256)
+      dw[c * lddw + j] = 0.f;
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  return fn;
+}
+
+// The pairs that run at once on the device; also opts in to the shared memory.
+cudaError_t resident_pairs(int device, int* out) {
+  static std::atomic<int> cached[64];
+  int n = device < 64 ? cached[device].load(std::memory_order_acquire) : 0;
+  if (!n) {
+    cudaError_t e = cudaFuncSetAttribute(ts_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = pdl_config(2, kThreads, kSmem, nullptr);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&n, ts_wgrad_kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    if (device < 64) cached[device].store(n, std::memory_order_release);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+// The product over `rows` tokens of dy rows that TMA can read.
+cudaError_t product(const ts_ops& h, WgradKernel& P, const TsCkpt& x, const TsMat& dy, int64_t rows, uint8_t* ws,
+                    int64_t ws_bytes, cudaStream_t st) {
+  EncodeFn enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {(cuuint64_t)P.n, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)dy.ld * 2};
+  const cuuint32_t box[2] = {64, kKB}, es[2] = {1, 1};
+  if (enc(&P.dy, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(dy.p), dims, strides, box, es,
+          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  int pairs = 0;
+  cudaError_t e = resident_pairs(h.device, &pairs);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t qdims[2] = {(cuuint64_t)x.pitch, (cuuint64_t)rows}, qstrides[1] = {(cuuint64_t)x.pitch};
+  const cuuint32_t qbox[2] = {kHalf, kKB};
+  if (enc(&P.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.q, qdims, qstrides, qbox, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
+      CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  P.scale = x.scale;
+  P.spitch = x.pitch / kCkptBlock;
+  P.rows = (int)rows;
+  P.tiles_n = (P.n + kTile - 1) / kTile;
+  const int tiles = (P.cols + kTile - 1) / kTile * P.tiles_n, nkb = (int)((rows + kKB - 1) / kKB);
+  // partials of long sums, one a pair (a small workspace runs fewer pairs)
+  const int64_t slots = ws_bytes / (kPieceFloats * 4);
+  if (nkb > kChain) pairs = (int)std::min<int64_t>(pairs, std::max<int64_t>(slots, 1));
+  P.full = tiles / pairs * pairs;
+  const int rem = tiles - P.full;
+  P.pieces = 1;
+  if (rem) {
+    const int64_t room = (slots - (nkb > kChain ? pairs : 0)) / rem;
+    P.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({pairs / rem, nkb / 8, room}));
+  }
+  P.items = P.full + P.pieces * rem;
+  P.chain = reinterpret_cast<float4*>(ws);
+  P.part = P.chain + (nkb > kChain ? pairs : 0) * (kPieceFloats / 4);
+  cudaLaunchConfig_t cfg = pdl_config(2 * std::min(pairs, P.items), kThreads, kSmem, st);
+  cudaLaunchAttribute at[1];
+  pdl_attr(cfg, at);
+  e = cudaLaunchKernelEx(&cfg, ts_wgrad_kernel, P);
+  if (e != cudaSuccess || P.pieces == 1) return e;
+  cudaLaunchConfig_t fin = pdl_config(rem * 32, 256, 0, st);
+  pdl_attr(fin, at);
+  return cudaLaunchKernelEx(&fin, ts_wgrad_finish_kernel, P);
 }
 
 }  // namespace
 
 cudaError_t launch_weight_grad(const ts_ops& h, const WgradArgs& a, cudaStream_t st) {
+  cudaLaunchAttribute at[1];
+  cudaError_t e;
   // dy's column sums: this call's own at the workspace's end, for beta
-  float* colsum = a.beta ? reinterpret_cast<float*>(h.ws + h.ws_bytes) - (a.n + 3) / 4 * 4 : nullptr;
+  const int64_t keep = a.beta ? ((int64_t)a.n * 4 + 255) / 256 * 256 : 0;
+  int64_t room = h.ws_bytes - keep;
+  float* colsum = keep ? reinterpret_cast<float*>(h.ws + room) : nullptr;
   if (colsum || a.db) {
-    cudaError_t e = launch_column_sums(h, a.dy, a.rows, a.n, colsum, a.db, a.accumulate, st);
+    e = launch_column_sums(h, a.dy, a.rows, a.n, colsum, a.db, a.accumulate, st);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = pdl_config(1, 256, 0, st);
-  cfg.gridDim = dim3((a.cols + 31) / 32, (a.n + 31) / 32);
-  cudaLaunchAttribute at[1];
-  pdl_attr(cfg, at);
-  return cudaLaunchKernelEx(&cfg, ts_wgrad_kernel, a, (const float*)colsum);
+  if (a.rows == 0) {
+    if (a.accumulate) return cudaSuccess;
+    cudaLaunchConfig_t cfg = pdl_config(1, 256, 0, st);
+    cfg.gridDim = dim3((a.n + 255) / 256, std::min(a.cols, 1024));
+    pdl_attr(cfg, at);
+    return cudaLaunchKernelEx(&cfg, ts_zero_kernel, a.dw, a.lddw, a.cols, a.n);
+  }
+  WgradKernel P = {};
+  P.cols = a.cols;
+  P.n = a.n;
+  P.gamma = a.gamma;
+  P.beta = a.beta;
+  P.colsum = colsum;
+  P.dw = a.dw;
+  P.lddw = a.lddw;
+  P.accumulate = a.accumulate;
+  P.err = h.err;
+  if (rows_aligned(a.dy)) return product(h, P, a.x, a.dy, a.rows, h.ws, room, st);
+  // an aligned copy of dy in at most half of the workspace, the partials in
+  // the rest
+  TsMat dy;
+  dy.p = h.ws;
+  dy.bf16 = 1;
+  dy.ld = (a.n + 7) / 8 * 8;
+  const int64_t most = std::max<int64_t>(1, room / 2 / (dy.ld * 2));
+  for (int64_t t = 0; t < a.rows; t += most) {
+    const int64_t rows = std::min(most, a.rows - t);
+    cudaLaunchConfig_t cfg = pdl_config(1, 256, 0, st);
+    cfg.gridDim = dim3((a.n + 1023) / 1024, (unsigned)std::min<int64_t>(rows, 1024));
+    pdl_attr(cfg, at);
+    e = cudaLaunchKernelEx(&cfg, ts_repack_kernel,
+                           static_cast<const __nv_bfloat16*>(a.dy.p) + t * a.dy.ld, a.dy.ld, rows, a.n,
+                           reinterpret_cast<__nv_bfloat16*>(h.ws), dy.ld);
+    if (e != cudaSuccess) return e;
+    TsCkpt x = a.x;
+    x.q += t * x.pitch;
+    x.scale += t * (x.pitch / kCkptBlock);
+    const int64_t used = (rows * dy.ld * 2 + 255) / 256 * 256;
+    e = product(h, P, x, dy, rows, h.ws + used, room - used, st);
+    if (e != cudaSuccess) return e;
+    P.accumulate = 1;   // the later tokens add to the first ones'
+    P.beta = nullptr;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace fg
