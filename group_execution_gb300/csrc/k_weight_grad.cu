@@ -57,7 +57,8 @@ constexpr int kSlots = 5;
 constexpr int kRawBytes = kKB * kHalf;           // a slot's checkpoint values, 8 KB
 constexpr int kRawScales = kKB * 4;              // and its scale bytes
 constexpr int kRaw = 6;
-constexpr int kExpandWarps = 8;                  // two sets of four
+constexpr int kSets = 2;                         // sets of four expanding warps, which take turns by slot
+constexpr int kExpandWarps = 4 * kSets;
 constexpr int kThreads = (7 + kExpandWarps) * 32;
 constexpr int kSmem = kSlots * kSlotBytes + kRaw * (kRawBytes + kRawScales) + 1024;
 constexpr int kChain = 32;                       // token blocks one accumulation runs over
@@ -189,12 +190,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = issued = raw_issued = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(full0 + 8 * s, 1 + kExpandWarps);   // the even CTA's expect_tx, a set of four in each CTA
+      mbar_init(full0 + 8 * s, 1 + 8);   // the even CTA's expect_tx, a set of four in each CTA
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(rfull0 + 8 * s, 1 + 32);   // the TMA's bytes, every lane's scale copies
-      mbar_init(rempty0 + 8 * s, kExpandWarps / 2);
+      mbar_init(rempty0 + 8 * s, 4);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
@@ -423,7 +424,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int x = pair; x < P.items && ok; x += npair) {
       const Item w = item_of(P, x, nkb);
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        if ((it & 1) != set) continue;
+        if (it % kSets != set) continue;
         const int rs = it % kRaw, s = it % kSlots;
         ok = __all_sync(0xffffffffu, wait_pair(rfull0 + 8 * rs, (it / kRaw) & 1, &abort_flag));
         if (!ok) break;
