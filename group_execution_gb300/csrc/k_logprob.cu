@@ -122,102 +122,144 @@ struct Chunk<__nv_bfloat16> {
   }
 };
 
-constexpr int kLpThreads = 512, kLpWarps = kLpThreads / 32;
 constexpr int kCandidates = 1024;
 constexpr int kMaxTop = 32, kMaxCluster = 8;
 
+// W warps share a row.
+template <int W>
 struct LpShared {
-  unsigned long long cand[kCandidates];
+  unsigned long long cand[W == 1 ? 288 : kCandidates];
   unsigned long long top[kMaxTop];
-  // what the cluster's CTAs leave with its first one
-  unsigned long long tops[kMaxCluster * kMaxTop];
+  // lists of the row's warps, and what the cluster's CTAs leave with its
+  // first one
+  unsigned long long lists[W == 1 ? 1 : W * 32];
+  unsigned long long tops[W == 1 ? 1 : kMaxCluster * kMaxTop];
   Softmax part[kMaxCluster];
-  Softmax warp[kLpWarps];
-  uint32_t bound[kLpWarps];
-  float ref[kLpWarps];
+  Softmax warp[W];
+  uint32_t bound[W];
+  uint32_t ref[W];
   int count;
 };
+template <int W>
+__device__ __forceinline__ void row_sync() {
+  if (W == 1)
+    __syncwarp();
+  else
+    __syncthreads();
+}
 
+// A logit, or a chunk by its largest, with its (first) column: larger logits
+// first, then lower columns.  Never 0.
 __device__ __forceinline__ unsigned long long composite(float v, int c) {
   return (unsigned long long)order_key(v) << 32 | (0xffffffffu - (uint32_t)c);
 }
-__device__ __forceinline__ void offer(LpShared& sh, float v, int c, unsigned long long tau) {
-  const unsigned long long k = composite(v, c);
-  if (k >= tau) {
-    const int i = atomicAdd(&sh.count, 1);
-    if (i < kCandidates) sh.cand[i] = k;
+__device__ __forceinline__ int composite_col(unsigned long long k) { return (int)(0xffffffffu - (uint32_t)k); }
+
+// The larger (keep_max) or smaller of this lane's entry and lane ^ o's.
+__device__ __forceinline__ unsigned long long exchange(unsigned long long v, int o, bool keep_max) {
+  const unsigned long long w = __shfl_xor_sync(0xffffffffu, v, o);
+  return (w > v) == keep_max ? w : v;
+}
+// 32 entries in falling order across the lanes (a bitonic network).
+__device__ __forceinline__ unsigned long long sort32(unsigned long long v, int lane) {
+#pragma unroll
+  for (int k = 2; k <= 32; k *= 2)
+#pragma unroll
+    for (int o = k / 2; o > 0; o /= 2) v = exchange(v, o, ((lane & o) == 0) == ((lane & k) == 0 || k == 32));
+  return v;
+}
+// The 32 largest, in falling order, of two lists in falling order.
+__device__ __forceinline__ unsigned long long merge32(unsigned long long a, unsigned long long b, int lane) {
+  const unsigned long long r = __shfl_sync(0xffffffffu, b, 31 - lane);
+  a = max(a, r);
+#pragma unroll
+  for (int o = 16; o > 0; o /= 2) a = exchange(a, o, (lane & o) == 0);
+  return a;
+}
+// The 32 largest of n composites in falling order, one to a lane of every
+// warp that calls (0 where there are fewer): warp w of W sorts every W-th
+// batch of 32, then the warps' lists are merged pairwise through `lists`.
+// All W warps call it; the result is warp 0's.
+template <int W>
+__device__ __forceinline__ unsigned long long largest32(const unsigned long long* in, int n, unsigned long long* lists,
+                                                        int warp, int lane) {
+  unsigned long long v = 0;
+  for (int i = warp * 32; i < n; i += W * 32) {
+    const unsigned long long s = sort32(i + lane < n ? in[i + lane] : 0, lane);
+    v = i == warp * 32 ? s : merge32(v, s, lane);
   }
+  int lists_left = min(W, (n + 31) / 32);
+  while (lists_left > 1) {
+    const int half = (lists_left + 1) / 2;
+    if (warp >= half && warp < lists_left) lists[warp * 32 + lane] = v;
+    __syncthreads();
+    if (warp + half < lists_left) v = merge32(v, lists[(warp + half) * 32 + lane], lane);
+    lists_left = half;
+  }
+  return v;
 }
 
-// The k largest of n composites, in order, into out (0 where there are fewer):
-// a composite's place is the number of larger ones (all are distinct, but for
-// the zeros that stand for none).
-__device__ void select_top(const unsigned long long* in, int n, unsigned long long* out, int k) {
-  for (int i = threadIdx.x; i < k; i += kLpThreads) out[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
-    const unsigned long long v = in[i];
-    if (!v) continue;
-    int place = 0;
-    for (int j = 0; j < n; ++j) place += in[j] > v;
-    if (place < k) out[place] = v;
-  }
-  __syncthreads();
-}
-
-// One row, or one of a cluster's equal segments of a row, a CTA.  One pass:
+// One row, or one of a cluster's equal segments of a row, to W warps.  One
+// pass:
 //
 // Each thread first loads U chunks of eight logits.  Their maximum over the
-// CTA is the reference of every thread's sums; a thread moves its own only
-// when a chunk exceeds it by 2^5, which keeps the exponentials in range
-// without a running maximum per logit.  From the same chunks comes a lower
-// bound of the k-th largest logit: every warp takes the r-th largest of its
-// lanes' maxima, and the q-th largest of these, q r >= k, has at least k
-// logits at or above it.  Chunks below the bound, nearly all, cost one
-// comparison; logits at or above it go to a list in shared memory, from which
-// the k largest are picked at the end.  Should the list overflow (logits in
-// rising order, or many equal ones), its own k-th largest is the next bound
-// and the row is read again for the list alone; the bound rises every time.
-template <class T, int U>
-__global__ void __launch_bounds__(kLpThreads, 2) ts_logprob_kernel(const LogprobArgs a) {
-  __shared__ LpShared sh;
+// row's threads is the reference of every thread's sums; a thread moves its
+// own only when a chunk exceeds it by 2^5, which keeps the exponentials in
+// range without a running maximum per logit.  From the same chunks comes a
+// lower bound of the k-th largest logit: every warp takes the r-th largest of
+// its lanes' maxima, and the q-th largest of these, q r >= k, has at least k
+// logits at or above it.  A chunk below the bound costs one comparison; one
+// at or above it is noted in shared memory by its maximum and column.  The k
+// largest logits lie in the k chunks with the largest maxima (ties by
+// column), so at the end those are picked from the list, read again (L2) and
+// their logits picked from.  Should the list overflow (logits in rising
+// order), its own k-th largest is the next bound and the row is read again
+// for the list alone; the bound rises every time.
+template <class T, int U, int W>
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, W == 1 ? 8 : 4) ts_logprob_kernel(const LogprobArgs a) {
+  constexpr int kRows = W == 1 ? 4 : 1, kN = W * 32;   // rows a block, threads a row
+  __shared__ LpShared<W> shared[kRows];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t ncl;
-  asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ncl));
-  const uint32_t rank = ncl > 1 ? cluster_ctarank() : 0;
-  if (ncl > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-  const int64_t row = blockIdx.x / ncl;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, tid = W == 1 ? lane : threadIdx.x;
+  LpShared<W>& sh = shared[W == 1 ? threadIdx.x >> 5 : 0];
+  uint32_t ncl = 1, rank = 0;
+  if (W > 1) {
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ncl));
+    if (ncl > 1) {
+      rank = cluster_ctarank();
+      asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    }
+  }
+  const int64_t row = W == 1 ? (int64_t)blockIdx.x * kRows + (threadIdx.x >> 5) : blockIdx.x / ncl;
+  if (row >= a.rows) return;   // (a whole warp of the last block, W = 1)
   const T* x = static_cast<const T*>(a.logits.p) + row * a.logits.ld;
-  // this CTA's logits, [begin, end), as loose ones before a 16-byte boundary,
-  // whole chunks from it on, and loose ones after them
+  // these threads' logits, [begin, end), as loose ones before a 16-byte
+  // boundary, whole chunks from it on, and loose ones after them
   const int begin = (int)((int64_t)a.vocab * rank / ncl), end = (int)((int64_t)a.vocab * (rank + 1) / ncl);
   const int off = (int)(reinterpret_cast<uintptr_t>(x + begin) % 16 / sizeof(T));
   const int head = min(end - begin, off ? (int)(16 / sizeof(T)) - off : 0);
   const int first = begin + head, chunks = (end - first) / 8, tail = first + chunks * 8;
-  const int loose = head + (end - tail);   // at most 14
-  const int my_loose = (int)threadIdx.x < loose ? (int)threadIdx.x < head ? begin + (int)threadIdx.x
-                                                                          : tail + (int)threadIdx.x - head
-                                                : -1;
+  const int my_loose = tid < head ? begin + tid : tail + tid - head < end ? tail + tid - head : -1;   // at most 14
+  const T* body = x + first + tid * 8;   // this thread's first chunk; the next are kN chunks apart
   float tok_logit = 0.f;
   int64_t tok = -1;
-  if (threadIdx.x == 0 && rank == 0 && a.logprob) {
+  if (tid == 0 && rank == 0 && a.logprob) {
     tok = a.tokens[row];
     if (tok >= 0 && tok < a.vocab) tok_logit = to_f32(x[tok]);
   }
-  if (threadIdx.x == 0) sh.count = 0;
+  if (tid == 0) sh.count = 0;
 
   Chunk<T> c[U];
   float loose_v = -INFINITY, seed = -INFINITY;
   if (my_loose >= 0) loose_v = to_f32(x[my_loose]);
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (threadIdx.x + u * kLpThreads < chunks) c[u].load(x + first + (threadIdx.x + u * kLpThreads) * 8);
+    if (tid + u * kN < chunks) c[u].load(body + u * kN * 8);
   uint32_t lane_key = 0;   // 0: no logit
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (threadIdx.x + u * kLpThreads < chunks) {
+    if (tid + u * kN < chunks) {
       const float m = c[u].top();
       seed = fmaxf(seed, m);
       lane_key = max(lane_key, order_key(m));
@@ -226,35 +268,37 @@ __global__ void __launch_bounds__(kLpThreads, 2) ts_logprob_kernel(const Logprob
     seed = fmaxf(seed, loose_v);
     lane_key = max(lane_key, order_key(loose_v));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) seed = fmaxf(seed, __shfl_xor_sync(0xffffffffu, seed, o));
-  const int r = (2 * a.k + kLpWarps - 1) / kLpWarps;
-  const int q = a.k ? (a.k + r - 1) / r : 0;
-  uint32_t nth = 0;
+  const uint32_t seed_key = __reduce_max_sync(0xffffffffu, order_key(seed));   // (fmaxf passed over any NaN)
+  const int r = W == 1 ? a.k : (2 * a.k + W - 1) / W;
+  const int q = W == 1 ? 0 : a.k ? (a.k + r - 1) / r : 0;
+  uint32_t bound = 0, ref_key = seed_key;
   for (int i = 0; i < r; ++i) {
-    nth = __reduce_max_sync(0xffffffffu, lane_key);
-    if (lane == __ffs(__ballot_sync(0xffffffffu, lane_key == nth)) - 1) lane_key = 0;
+    bound = __reduce_max_sync(0xffffffffu, lane_key);
+    if (lane == __ffs(__ballot_sync(0xffffffffu, lane_key == bound)) - 1) lane_key = 0;
   }
-  if (lane == 0) {
-    sh.ref[warp] = seed;
-    sh.bound[warp] = nth;
+  if (W > 1) {
+    if (lane == 0) {
+      sh.ref[warp] = seed_key;
+      sh.bound[warp] = bound;
+    }
+    __syncthreads();
+    ref_key = __reduce_max_sync(0xffffffffu, lane < W ? sh.ref[lane] : 0u);
+    uint32_t key = lane < W ? sh.bound[lane] : 0;
+    bound = 0;
+    for (int i = 0; i < q; ++i) {
+      bound = __reduce_max_sync(0xffffffffu, key);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, key == bound)) - 1) key = 0;
+    }
+  } else {
+    __syncwarp();
   }
-  __syncthreads();
-  seed = lane < kLpWarps ? sh.ref[lane] : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) seed = fmaxf(seed, __shfl_xor_sync(0xffffffffu, seed, o));
-  uint32_t key = lane < kLpWarps ? sh.bound[lane] : 0, bound = 0;
-  for (int i = 0; i < q; ++i) {
-    bound = __reduce_max_sync(0xffffffffu, key);
-    if (lane == __ffs(__ballot_sync(0xffffffffu, key == bound)) - 1) key = 0;
-  }
-  // the bound as a float: a chunk whose largest logit is below it has no
-  // candidate (a NaN compares as not below)
-  unsigned long long tau = a.k ? (unsigned long long)bound << 32 : ~0ull;
-  const float tau_f = !a.k      ? INFINITY
-                      : !bound  ? -INFINITY
-                                : __uint_as_float(bound & 0x80000000u ? bound & 0x7fffffffu : ~bound);
+  auto key_value = [](uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k); };
+  seed = key_value(ref_key);
+  // a chunk whose largest logit is below the bound has no candidate (a NaN
+  // compares as not below)
   const bool want = a.k > 0;
+  unsigned long long tau = (unsigned long long)bound << 32;
+  const float tau_f = !want ? INFINITY : !bound ? -INFINITY : key_value(bound);
 
   Softmax acc{seed, 0.f, 0.f};
   uint64_t s2 = 0, t2 = 0;
@@ -274,148 +318,192 @@ __global__ void __launch_bounds__(kLpThreads, 2) ts_logprob_kernel(const Logprob
       t2 = fma2(e2, pack2f(d0, d1), t2);
     }
   };
-  auto raise = [&](float m) {
+  auto settle = [&]() {
     float sa, sb, ta, tb;
     unpack2f(s2, sa, sb);
     unpack2f(t2, ta, tb);
     acc.s = sa + sb;
     acc.t = ta + tb;
+  };
+  auto raise = [&](float m) {
+    settle();
     move_reference(acc, m);
     s2 = pack2f(acc.s, 0.f);
     t2 = pack2f(acc.t, 0.f);
     minus_m = -m;
     limit = m + 32.f;
   };
-  auto take = [&](const Chunk<T>& ch, int i) {
+  auto note = [&](float m, int col) {
+    const unsigned long long k = composite(m, col);
+    if (k >= tau) {
+      const int i = atomicAdd(&sh.count, 1);
+      if (i < (int)(sizeof(sh.cand) / 8)) sh.cand[i] = k;
+    }
+  };
+  int col = first + tid * 8;   // the column of c[0]
+  auto take = [&](const Chunk<T>& ch, int at) {
     const float m = ch.top();
     float v[8];
     ch.get(v);
     if (m > limit) raise(m);
     sums(v);
-    if (want && !(m < tau_f)) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) offer(sh, v[j], first + i * 8 + j, tau);
+    if (!(m < tau_f)) {
+      if (want) note(m, at);
     }
   };
   if (my_loose >= 0) {
     float v[8] = {loose_v, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
     if (loose_v > limit) raise(loose_v);
     sums(v);
-    if (want) offer(sh, loose_v, my_loose, tau);
+    if (want) note(loose_v, my_loose);
   }
-  for (int i0 = threadIdx.x; i0 < chunks; i0 += U * kLpThreads) {
-    // the next chunks are in flight while these are worked on
+  // whole rounds of U chunks a thread, the next round's loads in flight
+  // while one is worked on, and the rest
+  const int rounds = chunks / (U * kN);
+  for (int i = 0; i < rounds; ++i) {
     Chunk<T> n[U];
+    body += U * kN * 8;
+    if (i + 1 < rounds) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + (u + U) * kLpThreads;
-      if (i < chunks) n[u].load(x + first + (int64_t)i * 8);
+      for (int u = 0; u < U; ++u) n[u].load(body + u * kN * 8);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (rounds * U * kN + tid + u * kN < chunks) n[u].load(body + u * kN * 8);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * kLpThreads < chunks) take(c[u], i0 + u * kLpThreads);
+    for (int u = 0; u < U; ++u) take(c[u], col + u * kN * 8);
+    col += U * kN * 8;
 #pragma unroll
     for (int u = 0; u < U; ++u) c[u] = n[u];
   }
-  {
-    float sa, sb, ta, tb;
-    unpack2f(s2, sa, sb);
-    unpack2f(t2, ta, tb);
-    acc.s = sa + sb;
-    acc.t = ta + tb;
-  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const Softmax p{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
-                    __shfl_xor_sync(0xffffffffu, acc.t, o)};
-    acc = merge(acc, p);
+  for (int u = 0; u < U; ++u)
+    if (rounds * U * kN + tid + u * kN < chunks) take(c[u], col + u * kN * 8);
+
+  settle();
+  int one;
+  __match_all_sync(0xffffffffu, __float_as_uint(acc.m), &one);
+  if (one) {   // no lane moved its reference
+    acc.s = warp_sum(acc.s);
+    acc.t = warp_sum(acc.t);
+  } else {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Softmax p{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
+                      __shfl_xor_sync(0xffffffffu, acc.t, o)};
+      acc = merge(acc, p);
+    }
   }
-  if (lane == 0) sh.warp[warp] = acc;
-  __syncthreads();
+  if (W > 1 && lane == 0) sh.warp[warp] = acc;
+  row_sync<W>();
+  unsigned long long mine = 0;   // the lane-th largest, in the row's first warp
   if (want) {
+    constexpr int kRoom = (int)(sizeof(sh.cand) / 8);
     int n = sh.count;
-    while (n > kCandidates) {
-      select_top(sh.cand, kCandidates, sh.top, a.k);
+    while (W > 1 && n > kRoom) {
+      mine = largest32<W>(sh.cand, kRoom, sh.lists, warp, lane);
+      if (warp == 0) sh.top[lane] = mine;
+      row_sync<W>();
       tau = sh.top[a.k - 1];
-      if (threadIdx.x == 0) sh.count = 0;
-      __syncthreads();
-      for (int i = threadIdx.x; i < chunks; i += kLpThreads) {
-        float v[8];
+      if (tid == 0) sh.count = 0;
+      row_sync<W>();
+      for (int i = tid; i < chunks; i += kN) {
         Chunk<T> ch;
         ch.load(x + first + (int64_t)i * 8);
-        ch.get(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) offer(sh, v[j], first + i * 8 + j, tau);
+        note(ch.top(), first + i * 8);
       }
-      if (my_loose >= 0) offer(sh, loose_v, my_loose, tau);
-      __syncthreads();
+      if (my_loose >= 0) note(loose_v, my_loose);
+      row_sync<W>();
       n = sh.count;
     }
-    select_top(sh.cand, n, sh.top, a.k);
+    // the k chunks, then their logits
+    mine = largest32<W>(sh.cand, n, sh.lists, warp, lane);
+    if (warp == 0) sh.top[lane] = mine;
+    row_sync<W>();
+    if (tid == 0) sh.count = 0;
+    row_sync<W>();
+    const uint32_t least = (uint32_t)(sh.top[a.k - 1] >> 32);
+    for (int i = tid; i < a.k * 8; i += kN) {
+      const unsigned long long e = sh.top[i / 8];
+      if (!e) continue;
+      const int at = composite_col(e), j = i % 8;
+      if (j && (at < first || at >= tail)) continue;   // a loose one
+      const unsigned long long k = composite(to_f32(x[at + j]), at + j);
+      if ((uint32_t)(k >> 32) >= least) sh.cand[atomicAdd(&sh.count, 1)] = k;   // 256 at most
+    }
+    row_sync<W>();
+    mine = largest32<W>(sh.cand, sh.count, sh.lists, warp, lane);
   }
-  if (warp == 0) {
+  if (warp) {
+    if (W > 1 && ncl > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      cluster_sync();
+    }
+    return;
+  }
+  // the row's first warp finishes
+  if (W > 1) {
     acc = sh.warp[0];
-    for (int w = 1; w < kLpWarps; ++w) acc = merge(acc, sh.warp[w]);
+    for (int w = 1; w < W; ++w) acc = merge(acc, sh.warp[w]);
   }
-  const unsigned long long* top = sh.top;
-  if (ncl > 1) {
+  __syncwarp();
+  if (W > 1 && ncl > 1) {
     // the first CTA (which has started) gathers the segments' sums and lists
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (warp == 0) {
-      const uint32_t dst = cluster_addr(smem_u32(&sh.part[rank]), 0);
-      if (lane == 0)
-        asm volatile("st.shared::cluster.f32 [%0], %1;\n st.shared::cluster.f32 [%0 + 4], %2;\n"
-                     " st.shared::cluster.f32 [%0 + 8], %3;" ::"r"(dst),
-                     "f"(acc.m), "f"(acc.s), "f"(acc.t)
-                     : "memory");
-      if (lane < a.k)
-        asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(
-                         cluster_addr(smem_u32(&sh.tops[rank * a.k + lane]), 0)),
-                     "l"(sh.top[lane])
-                     : "memory");
-    }
+    const uint32_t dst = cluster_addr(smem_u32(&sh.part[rank]), 0);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.f32 [%0], %1;\n st.shared::cluster.f32 [%0 + 4], %2;\n"
+                   " st.shared::cluster.f32 [%0 + 8], %3;" ::"r"(dst),
+                   "f"(acc.m), "f"(acc.s), "f"(acc.t)
+                   : "memory");
+    if (lane < a.k)
+      asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(cluster_addr(smem_u32(&sh.tops[rank * a.k + lane]), 0)),
+                   "l"(mine)
+                   : "memory");
     cluster_sync();   // releases the stores, acquires them in the first CTA
     if (rank) return;
-    if (warp == 0) {
-      acc = sh.part[0];
-      for (uint32_t w = 1; w < ncl; ++w) acc = merge(acc, sh.part[w]);
-    }
-    if (want) select_top(sh.tops, (int)ncl * a.k, sh.top, a.k);
+    acc = sh.part[0];
+    for (uint32_t w = 1; w < ncl; ++w) acc = merge(acc, sh.part[w]);
+    for (uint32_t w = 1; w < ncl && want; ++w) mine = merge32(mine, lane < a.k ? sh.tops[w * a.k + lane] : 0, lane);
   }
-  if (warp == 0) {
-    const bool none = acc.s == 0.f;
-    const float ln = logf(acc.s), lse = none ? -INFINITY : acc.m + ln;
-    if (lane == 0) {
-      if (a.lse) a.lse[row] = lse;
-      if (a.entropy) a.entropy[row] = none ? 0.f : ln - kLn2 * (acc.t / acc.s);
-      if (a.logprob)
-        a.logprob[row] = tok < 0 || tok >= a.vocab ? 0.f : none ? -INFINITY : tok_logit - lse;
-    }
-    if (lane < a.k) {
-      const unsigned long long k = top[lane];
-      const int id = (int)(0xffffffffu - (uint32_t)k);
-      a.top_id[row * a.k + lane] = id;
-      a.top_logprob[row * a.k + lane] = none ? -INFINITY : to_f32(x[id]) - lse;
-    }
+  const bool none = acc.s == 0.f;
+  const float ln = logf(acc.s), lse = none ? -INFINITY : acc.m + ln;
+  if (lane == 0) {
+    if (a.lse) a.lse[row] = lse;
+    if (a.entropy) a.entropy[row] = none ? 0.f : ln - kLn2 * (acc.t / acc.s);
+    if (a.logprob) a.logprob[row] = tok < 0 || tok >= a.vocab ? 0.f : none ? -INFINITY : tok_logit - lse;
+  }
+  if (lane < a.k) {
+    a.top_id[row * a.k + lane] = composite_col(mine);
+    a.top_logprob[row * a.k + lane] = none ? -INFINITY : to_f32(x[composite_col(mine)]) - lse;
   }
 }
 
-// Segments a row: as many as keep about two CTAs on every SM, each of at
-// least two chunks a thread.
+constexpr int kWarpRow = 2048;   // columns up to which one warp takes a row (its list holds every chunk)
+
+// Segments a row: enough for about two blocks on every SM, of two chunks a
+// thread at least.
 template <class T, int U>
 cudaError_t logprob_rows(const ts_ops& h, const LogprobArgs& a, cudaStream_t st) {
-  int ncl = 1;
-  while (ncl < kMaxCluster && a.rows * ncl * 2 <= 2 * (int64_t)h.nsm && a.vocab / (ncl * 2) >= kLpThreads * 8) ncl *= 2;
-  cudaLaunchConfig_t cfg = pdl_config((int)(a.rows * ncl), kLpThreads, 0, st);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  if (a.vocab <= kWarpRow) {
+    cudaLaunchConfig_t cfg = pdl_config((int)((a.rows + 3) / 4), 128, 0, st);
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, 1>, a);
+  }
+  int ncl = 1;
+  while (ncl < kMaxCluster && a.rows * ncl * 2 <= 2 * (int64_t)h.nsm && a.vocab / (ncl * 2) >= 256 * 16) ncl *= 2;
+  cudaLaunchConfig_t cfg = pdl_config((int)(a.rows * ncl), 256, 0, st);
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim.x = ncl;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U>, a);
+  return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, 8>, a);
 }
 
 template <class TX, class TD, bool VEC>
