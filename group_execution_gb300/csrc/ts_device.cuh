@@ -53,6 +53,37 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
                                             bf16x2(v[6], v[7]));
 }
 
+// Two float32 values in one register pair: one instruction works on both.
+using F2 = uint64_t;
+__device__ __forceinline__ F2 pack2f(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2f(F2 v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float sum2(F2 v) {
+  float a, b;
+  unpack2f(v, a, b);
+  return a + b;
+}
+
 // A warp works on groups of 256 columns of one row, eight values a lane.  VEC
 // (every row of every operand starts on 16 bytes): a lane's eight columns are
 // consecutive and move in 16-byte accesses.  Otherwise value j of a lane is
@@ -92,6 +123,57 @@ __device__ __forceinline__ void store_group(T* p, int c0, int cols, int lane, co
   }
 }
 
+// A group of a row as it lies in memory, fetched some time before it is used.
+// Columns at or past `cols` are zeros.
+template <class T, bool VEC>
+struct RawGroup;
+template <class T>
+struct RawGroup<T, false> {
+  T e[8];
+  __device__ __forceinline__ void load(const T* p, int c0, int cols, int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + j * 32 + lane;
+      e[j] = c < cols ? p[c] : from_f32<T>(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = to_f32(e[j]);
+  }
+};
+template <class T>
+struct RawGroup<T, true> {
+  static constexpr int kQuads = sizeof(T) / 2;   // 16-byte quads of eight values
+  uint4 q[kQuads];
+  __device__ __forceinline__ void load(const T* p, int c0, int cols, int lane) {
+    const int c = c0 + lane * 8;
+    if (c + 8 <= cols) {
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) q[i] = reinterpret_cast<const uint4*>(p + c)[i];
+    } else {
+      __align__(16) T e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = c + j < cols ? p[c + j] : from_f32<T>(0.f);
+#pragma unroll
+      for (int i = 0; i < kQuads; ++i) q[i] = reinterpret_cast<const uint4*>(e)[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (sizeof(T) == 4) {
+      const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[kQuads - 1].x, q[kQuads - 1].y, q[kQuads - 1].z, q[kQuads - 1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(u[j]);
+    } else {
+      const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(u[j] << 16);
+        v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+      }
+    }
+  }
+};
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -102,8 +184,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 // A block's scale byte E is the exponent field of its largest magnitude, at
 // least 7 so that the step 2^(E - 133) is a normal float; 255 marks a block
 // that holds an infinity or a NaN.
-__device__ __forceinline__ float ckpt_step(int e) {
-  return e < 255 ? __uint_as_float((uint32_t)(e - 6) << 23) : __uint_as_float(0x7fc00000u);
+__device__ __forceinline__ float ckpt_step(uint32_t e) {
+  return e < 255 ? __uint_as_float((e - 6) << 23) : __uint_as_float(0x7fc00000u);
 }
 // 1 / step, or 0 where the block is marked (its values are then stored as 0).
 __device__ __forceinline__ float ckpt_inv_step(int e) {
@@ -177,5 +259,45 @@ __device__ __forceinline__ void ckpt_load_group(const TsCkpt& c, int64_t r, int 
     }
   }
 }
+
+// A group of a checkpoint row, fetched some time before it is used.
+template <bool VEC>
+struct RawCkpt;
+template <>
+struct RawCkpt<true> {
+  uint2 q;
+  uint32_t e;
+  __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
+    const int col = c0 + lane * 8;
+    q = make_uint2(0, 0);
+    e = 7;
+    if (col < c.pitch) {
+      q = *reinterpret_cast<const uint2*>(c.q + r * c.pitch + col);
+      e = c.scale[r * (c.pitch / kCkptBlock) + col / kCkptBlock];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const float step = ckpt_step(e);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3))) * step;
+  }
+};
+template <>
+struct RawCkpt<false> {
+  int q[8];
+  uint32_t e[8];
+  __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int col = c0 + j * 32 + lane;
+      q[j] = col < c.pitch ? c.q[r * c.pitch + col] : 0;
+      e[j] = col < c.pitch ? c.scale[r * (c.pitch / kCkptBlock) + col / kCkptBlock] : 7u;
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)q[j] * ckpt_step(e[j]);
+  }
+};
 
 }  // namespace fg
