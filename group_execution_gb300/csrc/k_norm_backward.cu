@@ -16,36 +16,45 @@
 namespace fg {
 namespace {
 
-// Where the normalised row h comes from: x, or the checkpoint.
+// Where the normalised row h comes from: x, or the checkpoint.  An object is a
+// cursor on a row; Raw holds a group of it as it lies in memory.
 template <class TX>
 struct FromX {
   using Dx = TX;
+  static constexpr bool kCkpt = false;
+  const TX* row;
+  __device__ __forceinline__ FromX(const NormArgs& a, int64_t r) : row(static_cast<const TX*>(a.x.p) + r * a.x.ld) {}
+  __device__ __forceinline__ void advance(const NormArgs& a, int64_t rows) { row += rows * a.x.ld; }
   template <bool VEC>
   struct Raw {
     static constexpr int kRegs = VEC ? (int)sizeof(TX) * 2 : 8;
     RawGroup<TX, VEC> x;
-    __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int c0, int lane) {
-      x.load(static_cast<const TX*>(a.x.p) + row * a.x.ld, c0, a.cols, lane);
+    __device__ __forceinline__ void load(const NormArgs& a, const FromX& s, int c0, int lane) {
+      x.load(s.row, c0, a.cols, lane);
     }
-    __device__ __forceinline__ void get(float mean, float rstd, float (&h)[8]) const {
-      x.get(h);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[j] = (h[j] - mean) * rstd;
-    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { x.get(v); }   // x itself
   };
   __device__ __forceinline__ static float mean(const NormArgs& a, int64_t row) { return a.mean[row]; }
 };
 template <class TDX>
 struct FromCkpt {
   using Dx = TDX;
+  static constexpr bool kCkpt = true;
+  TsCkpt row;   // a view of this one row
+  __device__ __forceinline__ FromCkpt(const NormArgs& a, int64_t r) : row(a.ckpt) { move(r); }
+  __device__ __forceinline__ void move(int64_t rows) {
+    row.q += rows * row.pitch;
+    row.scale += rows * (row.pitch / kCkptBlock);
+  }
+  __device__ __forceinline__ void advance(const NormArgs&, int64_t rows) { move(rows); }
   template <bool VEC>
   struct Raw {
-    static constexpr int kRegs = VEC ? 3 : 16;
+    static constexpr int kRegs = VEC ? 3 : 10;
     RawCkpt<VEC> c;
-    __device__ __forceinline__ void load(const NormArgs& a, int64_t row, int c0, int lane) {
-      c.load(a.ckpt, row, c0, lane);
+    __device__ __forceinline__ void load(const NormArgs&, const FromCkpt& s, int c0, int lane) {
+      c.load(s.row, 0, c0, lane);
     }
-    __device__ __forceinline__ void get(float, float, float (&h)[8]) const { c.get(h); }
+    __device__ __forceinline__ void get(float (&v)[8]) const { c.get(v); }   // h
   };
   __device__ __forceinline__ static float mean(const NormArgs&, int64_t) { return 0.f; }
 };
@@ -53,8 +62,12 @@ template <class Src, bool VEC>
 __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, int lane, float mean, float rstd,
                                        float (&h)[8]) {
   typename Src::template Raw<VEC> r;
-  r.load(a, row, c0, lane);
-  r.get(mean, rstd, h);
+  r.load(a, Src(a, row), c0, lane);
+  r.get(h);
+  if (!Src::kCkpt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = (h[j] - mean) * rstd;
+  }
 }
 
 // dx alone: one block a row, any length.
@@ -148,9 +161,7 @@ __global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float*
       for (int j = 0; j < 8; ++j) sb[j] += v[j];
       if constexpr (kH) {
         float h[8];
-        typename Src::template Raw<VEC> raw;
-        raw.load(a, rr, c0, lane);
-        raw.get(Src::mean(a, rr), a.rstd[rr], h);
+        load_h<Src, VEC>(a, rr, c0, lane, Src::mean(a, rr), a.rstd[rr], h);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sg[j] += v[j] * h[j];
       }
@@ -175,18 +186,46 @@ __global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float*
   }
 }
 
+// Two values a row, of K = 1 or 2 rows, summed over a warp: each step halves
+// what a lane still carries, so five or six shuffles do it.  Lanes 0 .. 16 / K
+// - 1 end with the sum of the first value, the next 16 / K with the second,
+// and so on.
+template <int K>
+__device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
+  float v;
+  if constexpr (K == 2) {
+    const bool hi = lane & 16, mid = lane & 8;
+    float x = hi ? s[2] : s[0], y = hi ? s[3] : s[1];
+    x += __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[2], 16);
+    y += __shfl_xor_sync(0xffffffffu, hi ? s[1] : s[3], 16);
+    v = mid ? y : x;
+    v += __shfl_xor_sync(0xffffffffu, mid ? x : y, 8);
+  } else {
+    const bool hi = lane & 16;
+    v = hi ? s[1] : s[0];
+    v += __shfl_xor_sync(0xffffffffu, hi ? s[0] : s[1], 16);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
 // Rows of at most 256 * G * W columns, W = 1, 2, 4, 8 or 16: dx and the
 // partial column sums in one pass.  A block of 16 warps has 16 / W row slots,
-// W warps a slot, G groups of 256 columns a warp.  A slot works on R rows at
-// once (one barrier and one chain of shuffles for all of them) and walks its
-// rows with the next D in flight in registers (one block an SM: with two, 64
+// W warps a slot, G groups of 256 columns a warp.  A slot works on K rows at
+// once (one barrier and one chain of shuffles for both) and walks its rows
+// with the next K D in flight in registers (one block an SM: with two, 64
 // registers a thread do not hold this).  A thread meets the same columns in
 // every row, so gamma (G = 1) and both column sums stay in its registers; at
 // the end the block adds its slots in order and writes one partial.
-template <class TDY, class Src, bool VEC, int G, int D, int R>
+//
+// Bound by instruction issue before memory in bf16 (eight columns a lane and
+// row: two loads, one store and about 100 other instructions), so pairs of
+// float32 operations go in one instruction and addresses advance by addition.
+template <class TDY, class Src, bool VEC, int G, int D, int K>
 __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs a, int W, float* part) {
-  static_assert(D % R == 0, "whole sets of rows in flight");
-  __shared__ float red[2][2 * R][16];
+  __shared__ float red[2][16][4];   // [warp][value]
   __shared__ float sums[G == 1 ? 2 * 16 * kGroupCols : 1];   // the slots' column sums (G = 1, W < 16)
   pdl_launch_dependents();
   pdl_wait();
@@ -201,52 +240,68 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
   };
   load_gamma(0);
   const float n = 1.f / (float)a.cols;
-  const int64_t step = (int64_t)gridDim.x * slots;
-  int64_t row = (int64_t)blockIdx.x * slots + slot;
-  RawGroup<TDY, VEC> dy[D][G];
-  typename Src::template Raw<VEC> x[D][G];
-  float mean[D], rstd[D];
-  auto fetch = [&](int d, int64_t r) {
-    if (r >= a.rows) return;
+  const int rows = (int)a.rows, step = gridDim.x * slots, first = blockIdx.x * slots + slot;
+  RawGroup<TDY, VEC> dy[D][K][G];
+  typename Src::template Raw<VEC> x[D][K][G];
+  float mean[D][K], rstd[D][K];
+  // the row that is fetched next
+  int at = first;
+  const TDY* dyp = static_cast<const TDY*>(a.dy.p) + (int64_t)first * a.dy.ld;
+  Src src(a, first);
+  const int64_t dy_step = (int64_t)step * a.dy.ld;
+  auto fetch = [&](int d, int k) {
+    if (at < rows) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-      const int c0 = (g * W + warp) * kGroupCols;
-      dy[d][g].load(static_cast<const TDY*>(a.dy.p) + r * a.dy.ld, c0, a.cols, lane);
-      x[d][g].load(a, r, c0, lane);
+      for (int g = 0; g < G; ++g) {
+        const int c0 = (g * W + warp) * kGroupCols;
+        dy[d][k][g].load(dyp, c0, a.cols, lane);
+        x[d][k][g].load(a, src, c0, lane);
+      }
+      mean[d][k] = Src::mean(a, at);
+      rstd[d][k] = a.rstd[at];
     }
-    mean[d] = Src::mean(a, r);
-    rstd[d] = a.rstd[r];
+    at += step;
+    dyp += dy_step;
+    src.advance(a, step);
   };
 #pragma unroll
-  for (int d = 0; d < D; ++d) fetch(d, row + d * step);
+  for (int d = 0; d < D; ++d)
+#pragma unroll
+    for (int k = 0; k < K; ++k) fetch(d, k);
   int buf = 0;
-  while (row < a.rows) {
+  typename Src::Dx* dx = static_cast<typename Src::Dx*>(a.dx.p) + (int64_t)first * a.dx.ld;
+  const int64_t dx_step = (int64_t)step * a.dx.ld;
+  for (int row = first; row < rows;) {
 #pragma unroll
-    for (int d = 0; d < D; d += R) {
-      if (row >= a.rows) break;
-      F2 u[R][G][4], h[R][G][4];
-      float rs[R], s[2 * R];
+    for (int d = 0; d < D; ++d) {
+      if (row >= rows) break;
+      const bool two = K == 2 && row + step < rows;
+      F2 u[K][G][4], h[K][G][4];
+      float rs[K], s[2 * K];
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
+      for (int k = 0; k < K; ++k) {
         F2 s1 = 0, s2 = 0;
         rs[k] = 0.f;
-        if (k == 0 || row + k * step < a.rows) {
-          rs[k] = rstd[d + k];
+        if (k == 0 || two) {
+          rs[k] = rstd[d][k];
+          const F2 scale = pack2f(rs[k], rs[k]), shift = pack2f(-mean[d][k], -mean[d][k]);
 #pragma unroll
           for (int g = 0; g < G; ++g) {
             float du[8], dh[8];
-            dy[d + k][g].get(du);
-            x[d + k][g].get(mean[d + k], rs[k], dh);
+            dy[d][k][g].get(du);
+            x[d][k][g].get(dh);
             if (G > 1) load_gamma(g);   // (from L1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const F2 v = pack2f(du[2 * j], du[2 * j + 1]);
-              h[k][g][j] = pack2f(dh[2 * j], dh[2 * j + 1]);
+              F2 hh = pack2f(dh[2 * j], dh[2 * j + 1]);
+              if (!Src::kCkpt) hh = mul2(add2(hh, shift), scale);
+              h[k][g][j] = hh;
               sb[g][j] = add2(sb[g][j], v);
-              sg[g][j] = fma2(v, h[k][g][j], sg[g][j]);
+              sg[g][j] = fma2(v, hh, sg[g][j]);
               u[k][g][j] = mul2(v, gamma[j]);
               s1 = add2(s1, u[k][g][j]);
-              s2 = fma2(u[k][g][j], h[k][g][j], s2);
+              s2 = fma2(u[k][g][j], hh, s2);
             }
           }
         }
@@ -254,46 +309,42 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
         s[2 * k + 1] = sum2(s2);
       }
 #pragma unroll
-      for (int k = 0; k < R; ++k) fetch(d + k, row + (D + k) * step);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-        for (int k = 0; k < 2 * R; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+      for (int k = 0; k < K; ++k) fetch(d, k);
+      constexpr int kLanes = 16 / K;   // that share a value
+      float v = warp_sums<K>(s, lane);
       if (W > 1) {
-        if (lane == 0) {
-#pragma unroll
-          for (int k = 0; k < 2 * R; ++k) red[buf][k][slot * W + warp] = s[k];
-        }
+        if (lane % kLanes == 0) red[buf][slot * W + warp][lane / kLanes] = v;
         named_bar_sync(1 + slot, W * 32);
-        // lanes 0-15 add the rows' first sums, 16-31 the second ones, in a
-        // fixed tree
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-          float v = (lane & 15) < W ? red[buf][2 * k + (lane >> 4)][slot * W + (lane & 15)] : 0.f;
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          s[2 * k] = __shfl_sync(0xffffffffu, v, 0);
-          s[2 * k + 1] = __shfl_sync(0xffffffffu, v, 16);
+        // the lanes that share a value add the warps', K each, in a fixed tree
+        const int w = (lane % kLanes) * K;
+        v = 0.f;
+        if (w < W) {
+          v = red[buf][slot * W + w][lane / kLanes];
+          if (K == 2) v += red[buf][slot * W + w + 1][lane / kLanes];
         }
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         buf ^= 1;   // (the next sums go to the other half, so one barrier is enough)
       }
+      v *= n;
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (k && row >= a.rows) break;
+      for (int k = 0; k < K; ++k) {
+        const float m1 = -rs[k] * __shfl_sync(0xffffffffu, v, 2 * kLanes * k);
+        const float m2 = -rs[k] * __shfl_sync(0xffffffffu, v, 2 * kLanes * k + kLanes);
+        if (k && !two) break;
         // dx = r u - r m1 - h r m2
-        const float m1 = -rs[k] * (s[2 * k] * n), m2 = -rs[k] * (s[2 * k + 1] * n);
-        const F2 rr = pack2f(rs[k], rs[k]), mm1 = pack2f(m1, m1), mm2 = pack2f(m2, m2);
+        const F2 rr = pack2f(rs[k], rs[k]), a1 = pack2f(m1, m1), a2 = pack2f(m2, m2);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           float o[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            unpack2f(fma2(h[k][g][j], mm2, fma2(u[k][g][j], rr, mm1)), o[2 * j], o[2 * j + 1]);
-          store_group<VEC>(static_cast<typename Src::Dx*>(a.dx.p) + row * a.dx.ld, (g * W + warp) * kGroupCols, a.cols,
-                           lane, o);
+            unpack2f(fma2(h[k][g][j], a2, fma2(u[k][g][j], rr, a1)), o[2 * j], o[2 * j + 1]);
+          store_group<VEC>(dx, (g * W + warp) * kGroupCols, a.cols, lane, o);
         }
-        row += step;
+        dx += dx_step;
       }
+      row += K * step;
     }
   }
   if (!part) return;
@@ -386,7 +437,7 @@ cudaError_t columns(const ts_ops& h, const NormArgs& a, float* fresh, cudaStream
   return finish_columns(part, parts, a.cols, a.dbeta, a.dgamma, a.accumulate, fresh, st);
 }
 
-template <class TDY, class Src, bool VEC, int G, int D, int R>
+template <class TDY, class Src, bool VEC, int G, int D, int K>
 cudaError_t backward_fused(const ts_ops& h, const NormArgs& a, int W, cudaStream_t st) {
   // one block an SM, a partial a block
   const int slots = 16 / W;
@@ -396,20 +447,20 @@ cudaError_t backward_fused(const ts_ops& h, const NormArgs& a, int W, cudaStream
   cudaLaunchConfig_t cfg = pdl_config((int)grid, 512, 0, st);
   cudaLaunchAttribute at[1];
   pdl_attr(cfg, at);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, ts_norm_backward_kernel<TDY, Src, VEC, G, D, R>, a, W, part);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ts_norm_backward_kernel<TDY, Src, VEC, G, D, K>, a, W, part);
   if (e != cudaSuccess || !part) return e;
   return finish_columns(part, (int)grid, a.cols, a.dbeta, a.dgamma, a.accumulate, nullptr, st);
 }
 
 template <class TDY, class Src, bool VEC>
 cudaError_t backward_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
-  // rows in flight: what about 32 registers hold
+  // pairs of rows in flight: what about 32 registers hold
   constexpr int kRegs = (VEC ? (int)sizeof(TDY) * 2 : 8) + Src::template Raw<VEC>::kRegs;
-  constexpr int D = kRegs <= 8 ? 4 : kRegs <= 16 ? 2 : 1, R = D > 1 ? 2 : 1;
+  constexpr int D = 1;
   if (a.rows > 0 && a.cols <= 16 * kGroupCols) {
     int W = 1;
     while (W * kGroupCols < a.cols) W *= 2;
-    return backward_fused<TDY, Src, VEC, 1, D, R>(h, a, W, st);
+    return backward_fused<TDY, Src, VEC, 1, D, 2>(h, a, W, st);
   }
   if (a.rows > 0 && a.cols <= 32 * kGroupCols) return backward_fused<TDY, Src, VEC, 2, 1, 1>(h, a, 16, st);
   if (a.rows > 0) {

@@ -55,6 +55,10 @@ inline TsCkpt ckpt_view(void* buf, int64_t rows, int64_t cols) {
   return c;
 }
 
+// Opts a kernel in to `bytes` of dynamic shared memory (once per kernel and
+// device for the largest size asked for so far).
+cudaError_t opt_in_smem(const void* kernel, int bytes);
+
 struct NormArgs {
   TsMat x, dy;
   TsOut y, dx;

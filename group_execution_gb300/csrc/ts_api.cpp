@@ -2,9 +2,12 @@
 // checks, the handle with its workspace and error word, and the launches.
 #include <cuda_runtime.h>
 
+#include <map>
 #include <memory>
+#include <mutex>
 #include <new>
 #include <string>
+#include <utility>
 
 #include "groupexec.h"
 #include "launch.h"
@@ -62,6 +65,22 @@ TsOut out(void* p, int dtype, int64_t ld) { return TsOut{p, dtype == FG_BF16, ld
 
 }  // namespace
 
+namespace fg {
+cudaError_t opt_in_smem(const void* kernel, int bytes) {
+  static std::mutex mu;
+  static std::map<std::pair<int, const void*>, int> done;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> g(mu);
+  int& have = done[{dev, kernel}];
+  if (have >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) have = bytes;
+  return e;
+}
+}  // namespace fg
+
 #define TS_TRY(x) \
   if (fg_status s_ = (x)) return s_
 
@@ -111,7 +130,7 @@ fg_status ts_sync_status(ts_ops* h, void* stream) {
   if (flag == 0) return FG_OK;
   e = cudaMemset(h->err, 0, sizeof(int32_t));
   if (e != cudaSuccess) return cuda_err(e, "clearing the device error word");
-  if (flag == DEVERR_TIMEOUT) return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad expired");
+  if (flag == DEVERR_TIMEOUT) return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad or ts_layer_norm_backward expired");
   return err(FG_EDEVICE, "device error word " + std::to_string(flag));
 }
 

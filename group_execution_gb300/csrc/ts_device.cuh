@@ -284,19 +284,23 @@ struct RawCkpt<true> {
 };
 template <>
 struct RawCkpt<false> {
-  int q[8];
-  uint32_t e[8];
+  int8_t q[8];
+  uint32_t e[2];   // the group's eight scale bytes (a row's are a multiple of 4)
   __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int col = c0 + j * 32 + lane;
-      q[j] = col < c.pitch ? c.q[r * c.pitch + col] : 0;
-      e[j] = col < c.pitch ? c.scale[r * (c.pitch / kCkptBlock) + col / kCkptBlock] : 7u;
+      q[j] = col < c.pitch ? c.q[r * c.pitch + col] : (int8_t)0;
     }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      e[i] = c0 + i * 128 < c.pitch
+                 ? *reinterpret_cast<const uint32_t*>(c.scale + r * (c.pitch / kCkptBlock) + c0 / kCkptBlock + 4 * i)
+                 : 0x07070707u;
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)q[j] * ckpt_step(e[j]);
+    for (int j = 0; j < 8; ++j) v[j] = (float)q[j] * ckpt_step((e[j / 4] >> (8 * (j & 3))) & 0xffu);
   }
 };
 
