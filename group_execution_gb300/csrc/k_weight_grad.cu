@@ -7,20 +7,28 @@
 // The product runs on the 5th-generation tensor cores.  A checkpoint's values
 // are exact in bf16, so the products are exact and the sums are float32:
 // bf16 operands cost no accuracy.  Persistent CTA pairs walk 256 x 256 tiles
-// of dW (2-SM tcgen05.mma, cta_group::2), tokens 64 at a time; each CTA
+// of dW (2-SM tcgen05.mma, cta_group::2), tokens 128 at a time; each CTA
 // stages half of the tile's columns of h and half of its columns of dY in a
 // ring of shared-memory slots, both MN-major, 128-byte swizzled.  Warps, in
 // each CTA:
-//   warp 0      TMA producer of its dY half (counted on the even CTA's slot
-//               barrier),
+//   warp 0      TMA producer of its dY half (two lanes, 64 columns each;
+//               counted on the even CTA's slot barrier),
 //   warp 1      allocates TMEM (two accumulators) and, in the even CTA,
 //               issues the MMAs from one thread,
-//   warps 2-5   epilogue: a thread owns one row of the CTA's 128 x 256
-//               accumulator; it overlaps the next tile's MMAs,
-//   warp 6      fetches the checkpoint: int8 values by TMA, scale bytes by
+//   warps 2, 3  fetch the checkpoint: int8 values by TMA, scale bytes by
 //               4-byte asynchronous copies, into a ring of its own,
-//   warps 7-14  two sets of four that take alternate slots: expand int8 to
-//               bf16, scale, and store the operand, swizzled.
+//   warps 4-7   epilogue: a thread owns one row of the CTA's 128 x 256
+//               accumulator; it overlaps the next tile's MMAs,
+//   warps 8-23  four sets of four, a quarter of every slot's tokens each:
+//               expand int8 to bf16, scale, and store the operand, swizzled.
+// Measured at 8192 x 4096 x 4096, in cycles of the issuing warp: a wait, the
+// MMAs and the commit of a slot cost about 600 beside the MMAs themselves, so
+// slots hold 128 tokens; an arrival that releases to the cluster about 2000
+// (626 us a call), so arrivals release to the CTA, after the proxy fence.
+// With the expanded operand in tensor memory (256 x 192 tiles) there is room
+// for four slots of 64 tokens only, fewer than the way from an MMA's end over
+// the expanding warps to the next MMA is long: 252 us.
+//
 // A float32 accumulator that takes all 8192 tokens one MMA after the other is
 // 2.8e-6 off (2-norm): the tensor core truncates as it adds.  So a sum runs
 // over at most 2048 tokens; what it came to is added to a float32 partial in
@@ -50,18 +58,21 @@ namespace {
 
 constexpr int kTile = 256;                       // rows and columns of dW a pair's tile covers
 constexpr int kHalf = kTile / 2;                 // ... and one CTA stages of each operand
-constexpr int kKB = 64;                          // tokens a ring slot holds
-constexpr int kOperandBytes = kHalf * kKB * 2;   // 16 KB
+constexpr int kKB = 128;                         // tokens of a ring slot
+constexpr int kGroupBytes = kKB * 128;           // 64 columns of either operand
+constexpr int kOperandBytes = 2 * kGroupBytes;   // 32 KB
 constexpr int kSlotBytes = 2 * kOperandBytes;
-constexpr int kSlots = 5;
-constexpr int kRawBytes = kKB * kHalf;           // a slot's checkpoint values, 8 KB
-constexpr int kRawScales = kKB * 4;              // and its scale bytes
-constexpr int kRaw = 6;
-constexpr int kSets = 2;                         // sets of four expanding warps, which take turns by slot
+constexpr int kSlots = 3;
+constexpr int kRawTokens = 64;                   // tokens of a slot of the checkpoint's own ring
+constexpr int kRawBytes = kRawTokens * kHalf;    // its values, 8 KB
+constexpr int kRawScales = kRawTokens * 4;       // and its scale bytes
+constexpr int kRaw = 4;
+constexpr int kSets = 4;                         // sets of four expanding warps, a quarter of a slot's tokens each
+constexpr int kSetTokens = kKB / kSets;
 constexpr int kExpandWarps = 4 * kSets;
-constexpr int kThreads = (7 + kExpandWarps) * 32;
+constexpr int kThreads = (8 + kExpandWarps) * 32;
 constexpr int kSmem = kSlots * kSlotBytes + kRaw * (kRawBytes + kRawScales) + 1024;
-constexpr int kChain = 32;                       // token blocks one accumulation runs over
+constexpr int kChain = 16;                       // blocks of kKB tokens one accumulation runs over
 constexpr int64_t kWaitNs = 2000000000LL;
 constexpr int64_t kPieceFloats = (int64_t)kTile * kTile;
 
@@ -100,12 +111,11 @@ __device__ __forceinline__ int segment_end(const Item& w, int kb0) {
 }
 
 // Waits for the phase with the given parity, at most kWaitNs and only while
-// no thread of the CTA has given up.  Arrivals and data may come from the
-// pair's other CTA.
-__device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
+// no thread of the CTA has given up.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
-  while (!mbar_try_wait_cluster(bar, parity))
+  while (!mbar_try_wait(bar, parity))
     if (*abort_flag || (int64_t)(global_ns() - t0) > kWaitNs) return false;
   return true;
 }
@@ -126,6 +136,20 @@ __device__ __forceinline__ void expand4(uint32_t w, __nv_bfloat162 step, uint32_
 __device__ __forceinline__ __nv_bfloat162 bf16_step(uint32_t e) {
   const uint32_t h = e < 255 ? (max(e, 7u) - 6) << 7 : 0x7fc0u, w = h | h << 16;
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+// 16 consecutive f32 columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // Stores eight values of one row of dw from column j (vec: 8, 4 or 1 floats
@@ -172,15 +196,15 @@ __device__ __forceinline__ int store_width(const WgradKernel& P) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_wgrad_kernel(const __grid_constant__ WgradKernel P) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 2 * kRaw + 5];
-  __shared__ int abort_flag, issued, raw_issued;
+  __shared__ __align__(8) uint64_t bar_mem[2 * (kSlots + kRaw) + 5];
+  __shared__ int abort_flag, issued, raw_issued[2];
   __shared__ uint32_t tmem_slot;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
-                 tempty0 = tfull0 + 16, done_bar = tempty0 + 16, rfull0 = done_bar + 8,
-                 rempty0 = rfull0 + 8 * kRaw;
   uint8_t* raw = ring + kSlots * kSlotBytes;
   uint8_t* raw_scale = raw + kRaw * kRawBytes;
+  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, rfull0 = empty0 + 8 * kSlots,
+                 rempty0 = rfull0 + 8 * kRaw, tfull0 = rempty0 + 8 * kRaw, tempty0 = tfull0 + 16,
+                 done_bar = tempty0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = (int)cluster_ctarank();
   const bool leader = h == 0;
@@ -188,14 +212,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
   const int nkb = (P.rows + kKB - 1) / kKB;
   if (threadIdx.x == 0) {
-    abort_flag = issued = raw_issued = 0;
+    abort_flag = issued = raw_issued[0] = raw_issued[1] = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(full0 + 8 * s, 1 + 8);   // the even CTA's expect_tx, a set of four in each CTA
+      mbar_init(full0 + 8 * s, 1 + 2 * kExpandWarps);   // the even CTA's expect_tx, the pair's expanding warps
       mbar_init(empty0 + 8 * s, 1);
     }
     for (int s = 0; s < kRaw; ++s) {
       mbar_init(rfull0 + 8 * s, 1 + 32);   // the TMA's bytes, every lane's scale copies
-      mbar_init(rempty0 + 8 * s, 4);
+      mbar_init(rempty0 + 8 * s, kExpandWarps * kRawTokens / kKB);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
@@ -214,26 +238,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   pdl_wait();
 
   if (warp == 0) {
-    // ---- dY producer ----
-    if (lane == 0) {
+    // ---- dY producer: lane 0 the first 64 columns, lane 1 the rest ----
+    if (lane < 2) {
+      const int g = lane;
       tma_prefetch(&P.dy);
       const uint64_t keep = l2_evict_last();
-      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + kOperandBytes;
+      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + kOperandBytes + g * kGroupBytes;
       int it = 0, s = 0;
       uint32_t ph = 0;
       bool ok = true;
       for (int x = pair; x < P.items && ok; x += npair) {
         const Item w = item_of(P, x, nkb);
-        const int n0 = w.tile % P.tiles_n * kTile + h * kHalf;
+        const int n0 = w.tile % P.tiles_n * kTile + h * kHalf + g * 64;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (it >= kSlots && !wait_pair(empty0 + 8 * s, ph ^ 1, &abort_flag)) {
+          if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, &abort_flag)) {
             ok = false;
             break;
           }
-          if (leader) mbar_expect_tx(full0 + 8 * s, 2 * kOperandBytes);
-#pragma unroll
-          for (int g = 0; g < kHalf / 64; ++g)
-            tma_load_2d_pair(dst0 + s * kSlotBytes + g * 8192, &P.dy, n0 + 64 * g, kb * kKB, cbar0 + 8 * s, keep);
+          if (leader && g == 0) mbar_expect_tx(full0 + 8 * s, 2 * kOperandBytes);
+          tma_load_2d_pair(dst0 + s * kSlotBytes, &P.dy, n0, kb * kKB, cbar0 + 8 * s, keep);
           ++it;
           if (++s == kSlots) {
             s = 0;
@@ -241,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      issued = it;
+      if (g == 0) issued = it;
       if (!ok) {
         abort_flag = 1;
         set_error(P.err, DEVERR_TIMEOUT);
@@ -251,9 +274,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---- MMA issuer ----
     if (lane == 0 && leader) {
       const uint32_t idesc = idesc_bf16_f32(kTile, kTile, 1, 1);
-      // MN-major: atoms of 64 columns x 8 tokens, 64-column groups 8 KB apart
+      // MN-major: atoms of 64 columns x 8 tokens, groups of 64 columns 16 KB apart
       const uint32_t base = smem_u32(ring);
-      const uint64_t ad0 = smem_desc_sw128(base, 8192, 1024), bd0 = smem_desc_sw128(base + kOperandBytes, 8192, 1024);
+      const uint64_t ad0 = smem_desc_sw128(base, kGroupBytes, 1024),
+                     bd0 = smem_desc_sw128(base + kOperandBytes, kGroupBytes, 1024);
       int s = 0, i = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -261,13 +285,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Item w = item_of(P, x, nkb);
         for (int s0 = w.kb0; s0 < w.kb1 && ok; ++i) {
           const int s1 = segment_end(w, s0), b = i & 1;
-          if (i >= 2 && !wait_pair(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, &abort_flag)) {
+          if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, &abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           for (int kb = s0; kb < s1; ++kb) {
-            if (!wait_pair(full0 + 8 * s, ph, &abort_flag)) {
+            if (!wait_bar(full0 + 8 * s, ph, &abort_flag)) {
               ok = false;
               break;
             }
@@ -295,7 +319,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_commit_mask(done_bar, pair_mask);
       mbar_wait(done_bar, 0, kDrainLimitNs);
     }
-  } else if (warp < 6) {
+  } else if (warp >= 4 && warp < 8) {
     // ---- epilogue ----
     const int q = warp & 3;   // the TMEM lane quarter this warp may access
     const int r = q * 32 + lane;
@@ -313,38 +337,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float4* piece = w.piece < 0 ? nullptr : P.part + (int64_t)(w.piece * 2 + h) * (kPieceFloats / 8) + r;
       for (int s0 = w.kb0; s0 < w.kb1; ++i) {
         const int s1 = segment_end(w, s0), b = i & 1;
-        ok = __all_sync(0xffffffffu, wait_pair(tfull0 + 8 * b, (i >> 1) & 1, &abort_flag));
+        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, &abort_flag));
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc0 = tmem + ((uint32_t)(q * 32) << 16) + b * kTile;
         const bool first = s0 == w.kb0, last = s1 == w.kb1;
         float4* dst = last ? piece : chain;
+        // the partial's next chunk is fetched (from L2) before one is used
+        float4 o[4];
+        auto fetch = [&](int j) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[k] = __ldcg(chain + (j / 4 + k) * kHalf);
+        };
+        if (!first) fetch(0);
 #pragma unroll 1
-        for (int j = 0; j < kTile; j += 32) {
+        for (int j = 0; j < kTile; j += 16) {
           if (n0 + j >= P.n) break;
-          float4 o[8];
+          float v[16];
+          tmem_ld16(acc0 + j, v);
           if (!first) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) o[k] = __ldcg(chain + (j / 4 + k) * kHalf);
-          }
-          float v[32];
-          tmem_ld32(acc0 + j, v);
-          if (!first) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < 4; ++k) {
               v[4 * k] += o[k].x;
               v[4 * k + 1] += o[k].y;
               v[4 * k + 2] += o[k].z;
               v[4 * k + 3] += o[k].w;
             }
+            if (j + 16 < kTile) fetch(j + 16);
           }
           if (dst) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < 4; ++k)
               dst[(j / 4 + k) * kHalf] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
           } else if (c < P.cols) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2; ++k) {
               float e[8];
 #pragma unroll
               for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
@@ -362,29 +389,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       abort_flag = 1;
       set_error(P.err, DEVERR_TIMEOUT);
     }
-  } else if (warp == 6) {
-    // ---- checkpoint fetch ----
+  } else if (warp == 2 || warp == 3) {
+    // ---- checkpoint fetch: alternate slots (one warp takes 780 cycles a slot) ----
+    const int mine = warp & 1;
     const uint64_t keep = l2_evict_last();
-    int it = 0, s = 0;
-    uint32_t ph = 0;
+    int it = 0;
     bool ok = true;
     for (int x = pair; x < P.items && ok; x += npair) {
       const Item w = item_of(P, x, nkb);
       const int m0 = w.tile / P.tiles_n * kTile + h * kHalf;
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+      for (int t0 = w.kb0 * kKB; t0 < w.kb1 * kKB; t0 += kRawTokens, ++it) {
+        if ((it & 1) != mine) continue;
+        const int s = it % kRaw;
         if (it >= kRaw) {
-          ok = __all_sync(0xffffffffu, wait_pair(rempty0 + 8 * s, ph ^ 1, &abort_flag));
+          ok = __all_sync(0xffffffffu, wait_bar(rempty0 + 8 * s, ((it / kRaw) & 1) ^ 1, &abort_flag));
           if (!ok) break;
         }
         const uint32_t bar = rfull0 + 8 * s;
         if (lane == 0) {
           mbar_expect_tx(bar, kRawBytes);
-          tma_load_2d_hint(smem_u32(raw + s * kRawBytes), &P.q, m0, kb * kKB, bar, keep);
+          tma_load_2d_hint(smem_u32(raw + s * kRawBytes), &P.q, m0, t0, bar, keep);
         }
 #pragma unroll
-        for (int u = 0; u < kKB / 32; ++u) {
+        for (int u = 0; u < kRawTokens / 32; ++u) {
           // rows and columns outside the checkpoint: zero bytes, no access
-          const int k = lane + 32 * u, row = kb * kKB + k;
+          const int k = lane + 32 * u, row = t0 + k;
           const bool in = row < P.rows && m0 / kCkptBlock < P.spitch;
           const uint8_t* src = P.scale + (in ? (int64_t)row * P.spitch + m0 / kCkptBlock : 0);
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
@@ -393,15 +422,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        : "memory");
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-        ++it;
-        if (++s == kRaw) {
-          s = 0;
-          ph ^= 1;
-        }
       }
     }
     if (lane == 0) {
-      raw_issued = it;
+      raw_issued[mine] = it;
       if (!ok) {
         abort_flag = 1;
         set_error(P.err, DEVERR_TIMEOUT);
@@ -410,52 +434,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ---- expansion ----
-    // a slot's 64 tokens x 128 columns: thread t of a set takes tokens t / 8
-    // + 16 u, columns (t % 8) * 16 .. + 15
-    const int set = (warp - 7) >> 2, t = threadIdx.x - (7 + 4 * set) * 32, kr = t >> 3, jc = t & 7;
+    // a set's 32 tokens x 128 columns: thread t takes tokens t / 8 + 16 u,
+    // columns (t % 8) * 16 .. + 15
+    const int set = (warp - 8) >> 2, t = threadIdx.x & 127, kr = t >> 3, jc = t & 7;
     const uint32_t written0 = cluster_addr(full0, 0);
     // the slot addresses of a thread's two 16-byte halves; lanes 4-7 of every
     // eight store them in the other order, so that eight lanes cover all banks
-    const uint32_t g = (uint32_t)(jc >> 2) * 8192 + (uint32_t)kr * 128, first = (uint32_t)(jc >> 2);
-    const uint32_t c0 = (uint32_t)((jc & 3) * 2);
+    const uint32_t g = (uint32_t)(jc >> 2) * kGroupBytes + (uint32_t)(set * kSetTokens + kr) * 128;
+    const uint32_t first = (uint32_t)(jc >> 2), c0 = (uint32_t)((jc & 3) * 2);
     const uint32_t off_a = g + (((c0 + first) ^ (kr & 7)) << 4), off_b = g + (((c0 + (first ^ 1)) ^ (kr & 7)) << 4);
-    int it = 0;
+    constexpr int kPerRaw = kRawTokens / kSetTokens;   // sets that share a raw slot
+    const int raw_row = set % kPerRaw * kSetTokens + kr;
+    constexpr int kU = kSetTokens / 16;
+    int blk = 0;
     bool ok = true;
     for (int x = pair; x < P.items && ok; x += npair) {
       const Item w = item_of(P, x, nkb);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        if (it % kSets != set) continue;
-        const int rs = it % kRaw, s = it % kSlots;
-        ok = __all_sync(0xffffffffu, wait_pair(rfull0 + 8 * rs, (it / kRaw) & 1, &abort_flag));
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
+        const int it = blk * (kKB / kRawTokens) + set / kPerRaw, rs = it % kRaw, s = blk % kSlots;
+        ok = __all_sync(0xffffffffu, wait_bar(rfull0 + 8 * rs, (it / kRaw) & 1, &abort_flag));
         if (!ok) break;
-        uint4 v[4];
-        uint32_t e[4];
+        uint4 v[kU];
+        uint32_t e[kU];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          v[u] = *reinterpret_cast<const uint4*>(raw + rs * kRawBytes + (kr + 16 * u) * kHalf + jc * 16);
-          e[u] = raw_scale[rs * kRawScales + (kr + 16 * u) * 4 + (jc >> 1)];
+        for (int u = 0; u < kU; ++u) {
+          v[u] = *reinterpret_cast<const uint4*>(raw + rs * kRawBytes + (raw_row + 16 * u) * kHalf + jc * 16);
+          e[u] = raw_scale[rs * kRawScales + (raw_row + 16 * u) * 4 + (jc >> 1)];
         }
-        if (it >= kSlots) {
-          ok = __all_sync(0xffffffffu, wait_pair(empty0 + 8 * s, ((it / kSlots) & 1) ^ 1, &abort_flag));
+        uint4 lo[kU], hi[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const __nv_bfloat162 step = bf16_step(e[u]);
+          expand4(v[u].x, step, lo[u].x, lo[u].y);
+          expand4(v[u].y, step, lo[u].z, lo[u].w);
+          expand4(v[u].z, step, hi[u].x, hi[u].y);
+          expand4(v[u].w, step, hi[u].z, hi[u].w);
+        }
+        if (blk >= kSlots) {
+          ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ((blk / kSlots) & 1) ^ 1, &abort_flag));
           if (!ok) break;
         }
         uint8_t* dst = ring + s * kSlotBytes;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const __nv_bfloat162 step = bf16_step(e[u]);
-          uint4 lo, hi;
-          expand4(v[u].x, step, lo.x, lo.y);
-          expand4(v[u].y, step, lo.z, lo.w);
-          expand4(v[u].z, step, hi.x, hi.y);
-          expand4(v[u].w, step, hi.z, hi.w);
-          *reinterpret_cast<uint4*>(dst + off_a + u * 16 * 128) = first ? hi : lo;
-          *reinterpret_cast<uint4*>(dst + off_b + u * 16 * 128) = first ? lo : hi;
+        for (int u = 0; u < kU; ++u) {
+          *reinterpret_cast<uint4*>(dst + off_a + u * 16 * 128) = first ? hi[u] : lo[u];
+          *reinterpret_cast<uint4*>(dst + off_b + u * 16 * 128) = first ? lo[u] : hi[u];
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(rempty0 + 8 * rs);
           mbar_arrive_cluster(written0 + 8 * s);
+          // (not before the values read have been used: an arrival overtakes
+          // the loads before it, and the slot was refilled under them)
+          mbar_arrive(rempty0 + 8 * rs);
         }
       }
     }
@@ -466,9 +497,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (abort_flag && threadIdx.x == 0)
-    for (int k = raw_issued - kRaw < 0 ? 0 : raw_issued - kRaw; k < raw_issued; ++k)
-      mbar_wait(rfull0 + 8 * (k % kRaw), (k / kRaw) & 1, kDrainLimitNs);
+  if (abort_flag && threadIdx.x < 2)
+    for (int n = raw_issued[threadIdx.x], k = n - kRaw < 0 ? 0 : n - kRaw; k < n; ++k)
+      if ((k & 1) == (int)threadIdx.x) mbar_wait(rfull0 + 8 * (k % kRaw), (k / kRaw) & 1, kDrainLimitNs);
   if (abort_flag && leader && threadIdx.x == 0) {
     // dY's copies in flight complete on the even CTA's barriers; the slots
     // they fill may lack arrivals, so each wait may run to its limit
@@ -574,7 +605,7 @@ cudaError_t product(const ts_ops& h, WgradKernel& P, const TsCkpt& x, const TsMa
   cudaError_t e = resident_pairs(h.device, &pairs);
   if (e != cudaSuccess) return e;
   const cuuint64_t qdims[2] = {(cuuint64_t)x.pitch, (cuuint64_t)rows}, qstrides[1] = {(cuuint64_t)x.pitch};
-  const cuuint32_t qbox[2] = {kHalf, kKB};
+  const cuuint32_t qbox[2] = {kHalf, kRawTokens};
   if (enc(&P.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.q, qdims, qstrides, qbox, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
           CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
       CUDA_SUCCESS)
@@ -592,7 +623,7 @@ cudaError_t product(const ts_ops& h, WgradKernel& P, const TsCkpt& x, const TsMa
   P.pieces = 1;
   if (rem) {
     const int64_t room = (slots - (nkb > kChain ? pairs : 0)) / rem;
-    P.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({pairs / rem, nkb / 8, room}));
+    P.pieces = (int)std::max<int64_t>(1, std::min<int64_t>({pairs / rem, nkb / 4, room}));
   }
   P.items = P.full + P.pieces * rem;
   P.chain = reinterpret_cast<float4*>(ws);

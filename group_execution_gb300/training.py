@@ -49,10 +49,10 @@ def _array(name, t, shape, dtype=torch.float32):
     return t.data_ptr()
 
 
-def _stream(stream):
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+# The current stream's handle; making a torch.cuda.Stream object to ask takes
+# longer (2.9 us) than all checks of a call.
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def checkpoint_layout(rows, cols):
@@ -90,6 +90,7 @@ class TrainingOps:
         self.lib = _lib.load()
         self.h = C.c_void_p()
         _lib.check(self.lib.ts_create(workspace_bytes, C.byref(self.h)))
+        self.device = torch.cuda.current_device()
 
     def __del__(self):
         h = getattr(self, "h", None)
@@ -97,10 +98,15 @@ class TrainingOps:
             self.lib.ts_destroy(h)
             self.h = None
 
+    def _stream(self, stream):
+        if stream is None:
+            return _current(self.device)
+        return stream if isinstance(stream, int) else stream.cuda_stream
+
     def sync(self, stream=None):
         """Waits for the stream; raises FgError (FG_ETIMEOUT) if a kernel
         recorded an expired wait."""
-        _lib.check(self.lib.ts_sync_status(self.h, _stream(stream)))
+        _lib.check(self.lib.ts_sync_status(self.h, self._stream(stream)))
 
     def layer_norm(self, x, gamma, beta, y, mean, rstd, eps=1e-5, ckpt=None, stream=None):
         """y = gamma (x - mean) rstd + beta by row; gamma, beta, mean, rstd may
@@ -111,7 +117,7 @@ class TrainingOps:
         _lib.check(self.lib.ts_layer_norm(
             self.h, px, tx, ldx, rows, cols, _array("gamma", gamma, (cols,)), _array("beta", beta, (cols,)), eps, py, ty,
             ldy, _array("mean", mean, (rows,)), _array("rstd", rstd, (rows,)), _saved(ckpt, rows, cols),
-            _stream(stream)))
+            self._stream(stream)))
 
     def layer_norm_backward(self, dy, x, gamma, mean, rstd, dx, dgamma, dbeta, accumulate=False, stream=None):
         """The gradient, from x, or from the Checkpoint of the normalised rows
@@ -127,17 +133,17 @@ class TrainingOps:
         _lib.check(self.lib.ts_layer_norm_backward(
             self.h, pdy, tdy, lddy, px, tx, ldx, pc, rows, cols, _array("gamma", gamma, (cols,)),
             _array("mean", mean, (rows,)), _array("rstd", rstd, (rows,)), pdx, tdx, lddx,
-            _array("dgamma", dgamma, (cols,)), _array("dbeta", dbeta, (cols,)), accumulate, _stream(stream)))
+            _array("dgamma", dgamma, (cols,)), _array("dbeta", dbeta, (cols,)), accumulate, self._stream(stream)))
 
     def checkpoint_save(self, x, ckpt, stream=None):
         """x in 8 bits into ckpt."""
         px, tx, ldx = _matrix("x", x, ckpt.rows, ckpt.cols)
-        _lib.check(self.lib.ts_checkpoint_save(self.h, px, tx, ldx, ckpt.rows, ckpt.cols, ckpt.ptr, _stream(stream)))
+        _lib.check(self.lib.ts_checkpoint_save(self.h, px, tx, ldx, ckpt.rows, ckpt.cols, ckpt.ptr, self._stream(stream)))
 
     def checkpoint_load(self, ckpt, y, stream=None):
         """ckpt's values into y."""
         py, ty, ldy = _matrix("y", y, ckpt.rows, ckpt.cols)
-        _lib.check(self.lib.ts_checkpoint_load(self.h, ckpt.ptr, ckpt.rows, ckpt.cols, py, ty, ldy, _stream(stream)))
+        _lib.check(self.lib.ts_checkpoint_load(self.h, ckpt.ptr, ckpt.rows, ckpt.cols, py, ty, ldy, self._stream(stream)))
 
     def activation_backward(self, op, dy, ckpt, dx, stream=None):
         """dx = dy f'(x) for op "relu", "sigmoid" or "tanh", from the
@@ -145,7 +151,7 @@ class TrainingOps:
         pdy, tdy, lddy = _matrix("dy", dy, ckpt.rows, ckpt.cols)
         pdx, tdx, lddx = _matrix("dx", dx, ckpt.rows, ckpt.cols)
         _lib.check(self.lib.ts_activation_backward(self.h, OPCODES[op], pdy, tdy, lddy, ckpt.ptr, ckpt.rows, ckpt.cols,
-                                                   pdx, tdx, lddx, _stream(stream)))
+                                                   pdx, tdx, lddx, self._stream(stream)))
 
     def weight_grad(self, ckpt, dy, dw, db=None, gamma=None, beta=None, accumulate=False, stream=None):
         """dw = X^T dy, X the checkpoint's values, or gamma * values + beta by
@@ -158,7 +164,7 @@ class TrainingOps:
         _lib.check(self.lib.ts_weight_grad(
             self.h, ckpt.ptr, ckpt.rows, ckpt.cols, _array("gamma", gamma, (ckpt.cols,)),
             _array("beta", beta, (ckpt.cols,)), pdy, tdy, lddy, n, pdw, lddw, _array("db", db, (n,)), accumulate,
-            _stream(stream)))
+            self._stream(stream)))
 
     def token_logprobs(self, logits, tokens, logprob, entropy, lse, top_logprob=None, top_id=None, stream=None):
         """Log probabilities of tokens (int64), the entropy and log-sum-exp of
@@ -173,7 +179,7 @@ class TrainingOps:
             self.h, p, t, ld, rows, vocab, _array("tokens", tokens, (rows,), torch.int64),
             _array("logprob", logprob, (rows,)), _array("entropy", entropy, (rows,)), _array("lse", lse, (rows,)), k,
             _array("top_logprob", top_logprob, (rows, k)), _array("top_id", top_id, (rows, k), torch.int32),
-            _stream(stream)))
+            self._stream(stream)))
 
     def token_logprobs_backward(self, logits, tokens, lse, entropy, g_logprob, g_entropy, dlogits, stream=None):
         """dlogits from the gradients of logprob and (may be None) entropy."""
@@ -183,7 +189,7 @@ class TrainingOps:
         _lib.check(self.lib.ts_token_logprobs_backward(
             self.h, p, t, ld, rows, vocab, _array("tokens", tokens, (rows,), torch.int64), _array("lse", lse, (rows,)),
             _array("entropy", entropy, (rows,)), _array("g_logprob", g_logprob, (rows,)),
-            _array("g_entropy", g_entropy, (rows,)), pd, td, ldd, _stream(stream)))
+            _array("g_entropy", g_entropy, (rows,)), pd, td, ldd, self._stream(stream)))
 
 
 def _saved(ckpt, rows, cols):
