@@ -15,19 +15,22 @@
 //               counted on the even CTA's slot barrier),
 //   warp 1      allocates TMEM (two accumulators) and, in the even CTA,
 //               issues the MMAs from one thread,
-//   warps 2, 3  fetch the checkpoint: int8 values by TMA, scale bytes by
-//               4-byte asynchronous copies, into a ring of its own,
-//   warps 4-7   epilogue: a thread owns one row of the CTA's 128 x 256
-//               accumulator; it overlaps the next tile's MMAs,
-//   warps 8-23  four sets of four, a quarter of every slot's tokens each:
-//               expand int8 to bf16, scale, and store the operand, swizzled.
-// Measured at 8192 x 4096 x 4096, in cycles of the issuing warp: a wait, the
-// MMAs and the commit of a slot cost about 600 beside the MMAs themselves, so
-// slots hold 128 tokens; an arrival that releases to the cluster about 2000
-// (626 us a call), so arrivals release to the CTA, after the proxy fence.
-// With the expanded operand in tensor memory (256 x 192 tiles) there is room
-// for four slots of 64 tokens only, fewer than the way from an MMA's end over
-// the expanding warps to the next MMA is long: 252 us.
+//   warps 4-11  epilogue: a thread owns half of one row of the CTA's 128 x
+//               256 accumulator; it overlaps the next tile's MMAs,
+//   warps 12-27 the checkpoint: two groups of eight that take turns by slot,
+//               64 tokens to each half: 16-byte loads of int8 values, a slot
+//               ahead, expanded to bf16, scaled and stored swizzled.
+// At 8192 x 4096 x 4096 this runs at 1350 TFLOP/s (70 % of the burst rate of
+// a plain bf16 product, 79 % of its sustained rate): the expansion's stores,
+// the copies' writes and the MMA's reads fill the 1024 cycles of
+// shared memory that a slot's MMAs take.  What was measured on the way (us a
+// call, and cycles of the issuing warp): a slot's wait, commit and first MMA
+// cost about 600 cycles beside the MMAs, so slots hold 128 tokens; an arrival
+// that releases to the cluster costs about 2000 (626 us), so arrivals release
+// to the CTA, after the proxy fence; the bytes through a shared-memory ring of
+// their own 226 us; the expanded operand in tensor memory (256 x 192 tiles)
+// leaves room for four slots of 64 tokens, fewer than the way from an MMA's end
+// over the expanding warps to the next MMA is long, 252 us.
 //
 // A float32 accumulator that takes all 8192 tokens one MMA after the other is
 // 2.8e-6 off (2-norm): the tensor core truncates as it adds.  So a sum runs
@@ -63,23 +66,19 @@ constexpr int kGroupBytes = kKB * 128;           // 64 columns of either operand
 constexpr int kOperandBytes = 2 * kGroupBytes;   // 32 KB
 constexpr int kSlotBytes = 2 * kOperandBytes;
 constexpr int kSlots = 3;
-constexpr int kRawTokens = 64;                   // tokens of a slot of the checkpoint's own ring
-constexpr int kRawBytes = kRawTokens * kHalf;    // its values, 8 KB
-constexpr int kRawScales = kRawTokens * 4;       // and its scale bytes
-constexpr int kRaw = 4;
-constexpr int kSets = 4;                         // sets of four expanding warps, a quarter of a slot's tokens each
-constexpr int kSetTokens = kKB / kSets;
+constexpr int kGroups = 2;                       // groups of expanding warps, which take turns by slot
+constexpr int kSets = 2 * kGroups;               // two sets of four warps a group, half a slot's tokens each
+constexpr int kSetTokens = kKB / 2;
 constexpr int kExpandWarps = 4 * kSets;
-constexpr int kThreads = (8 + kExpandWarps) * 32;
-constexpr int kSmem = kSlots * kSlotBytes + kRaw * (kRawBytes + kRawScales) + 1024;
+constexpr int kThreads = (12 + kExpandWarps) * 32;
+constexpr int kSmem = kSlots * kSlotBytes + 1024;
 constexpr int kChain = 16;                       // blocks of kKB tokens one accumulation runs over
 constexpr int64_t kWaitNs = 2000000000LL;
 constexpr int64_t kPieceFloats = (int64_t)kTile * kTile;
 
 struct WgradKernel {
-  CUtensorMap dy, q;
-  const uint8_t* scale;
-  int64_t spitch;      // scale bytes a row
+  CUtensorMap dy;
+  TsCkpt x;
   int rows, cols, n;
   int tiles_n;         // tiles along n; tile t covers columns of h from (t / tiles_n) * kTile
   int full, pieces;    // tiles taken whole, and pieces per later tile
@@ -158,10 +157,16 @@ __device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j,
                                         float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= g;
-  if (b != 0.f || P.beta) {
+  if (P.beta) {
+    float s[8];
+    if (j + 8 <= P.n) {   // (16-byte aligned: j is a multiple of 8)
+      load8(P.colsum + j, s);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (j + i < P.n) v[i] += b * P.colsum[j + i];
+      for (int i = 0; i < 8; ++i) s[i] = j + i < P.n ? P.colsum[j + i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += b * s[i];
   }
   float* d = row + j;
   if (vec == 8 && j + 8 <= P.n) {
@@ -196,15 +201,12 @@ __device__ __forceinline__ int store_width(const WgradKernel& P) {
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_wgrad_kernel(const __grid_constant__ WgradKernel P) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_mem[2 * (kSlots + kRaw) + 5];
-  __shared__ int abort_flag, issued, raw_issued[2];
+  __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 5];
+  __shared__ int abort_flag, issued;
   __shared__ uint32_t tmem_slot;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* raw = ring + kSlots * kSlotBytes;
-  uint8_t* raw_scale = raw + kRaw * kRawBytes;
-  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, rfull0 = empty0 + 8 * kSlots,
-                 rempty0 = rfull0 + 8 * kRaw, tfull0 = rempty0 + 8 * kRaw, tempty0 = tfull0 + 16,
-                 done_bar = tempty0 + 16;
+  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
+                 tempty0 = tfull0 + 16, done_bar = tempty0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = (int)cluster_ctarank();
   const bool leader = h == 0;
@@ -212,18 +214,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
   const int nkb = (P.rows + kKB - 1) / kKB;
   if (threadIdx.x == 0) {
-    abort_flag = issued = raw_issued[0] = raw_issued[1] = 0;
+    abort_flag = issued = 0;
     for (int s = 0; s < kSlots; ++s) {
-      mbar_init(full0 + 8 * s, 1 + 2 * kExpandWarps);   // the even CTA's expect_tx, the pair's expanding warps
+      mbar_init(full0 + 8 * s, 1 + 2 * 8);   // the even CTA's expect_tx, a group of eight warps in each CTA
       mbar_init(empty0 + 8 * s, 1);
-    }
-    for (int s = 0; s < kRaw; ++s) {
-      mbar_init(rfull0 + 8 * s, 1 + 32);   // the TMA's bytes, every lane's scale copies
-      mbar_init(rempty0 + 8 * s, kExpandWarps * kRawTokens / kKB);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(tfull0 + 8 * b, 1);
-      mbar_init(tempty0 + 8 * b, 8);   // the epilogue warps of the pair
+      mbar_init(tempty0 + 8 * b, 16);   // the epilogue warps of the pair
     }
     mbar_init(done_bar, 1);
     fence_mbar_init();
@@ -319,7 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_commit_mask(done_bar, pair_mask);
       mbar_wait(done_bar, 0, kDrainLimitNs);
     }
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < 12) {
     // ---- epilogue ----
     const int q = warp & 3;   // the TMEM lane quarter this warp may access
     const int r = q * 32 + lane;
@@ -349,9 +347,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[k] = __ldcg(chain + (j / 4 + k) * kHalf);
         };
-        if (!first) fetch(0);
+        const int j0 = warp >= 8 ? kTile / 2 : 0, j1 = j0 + kTile / 2;   // two warps to a lane quarter, half the columns each
+        if (!first) fetch(j0);
 #pragma unroll 1
-        for (int j = 0; j < kTile; j += 16) {
+        for (int j = j0; j < j1; j += 16) {
           if (n0 + j >= P.n) break;
           float v[16];
           tmem_ld16(acc0 + j, v);
@@ -363,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[4 * k + 2] += o[k].z;
               v[4 * k + 3] += o[k].w;
             }
-            if (j + 16 < kTile) fetch(j + 16);
+            if (j + 16 < j1) fetch(j + 16);
           }
           if (dst) {
 #pragma unroll
@@ -389,106 +388,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       abort_flag = 1;
       set_error(P.err, DEVERR_TIMEOUT);
     }
-  } else if (warp == 2 || warp == 3) {
-    // ---- checkpoint fetch: alternate slots (one warp takes 780 cycles a slot) ----
-    const int mine = warp & 1;
-    const uint64_t keep = l2_evict_last();
-    int it = 0;
-    bool ok = true;
-    for (int x = pair; x < P.items && ok; x += npair) {
-      const Item w = item_of(P, x, nkb);
-      const int m0 = w.tile / P.tiles_n * kTile + h * kHalf;
-      for (int t0 = w.kb0 * kKB; t0 < w.kb1 * kKB; t0 += kRawTokens, ++it) {
-        if ((it & 1) != mine) continue;
-        const int s = it % kRaw;
-        if (it >= kRaw) {
-          ok = __all_sync(0xffffffffu, wait_bar(rempty0 + 8 * s, ((it / kRaw) & 1) ^ 1, &abort_flag));
-          if (!ok) break;
-        }
-        const uint32_t bar = rfull0 + 8 * s;
-        if (lane == 0) {
-          mbar_expect_tx(bar, kRawBytes);
-          tma_load_2d_hint(smem_u32(raw + s * kRawBytes), &P.q, m0, t0, bar, keep);
-        }
-#pragma unroll
-        for (int u = 0; u < kRawTokens / 32; ++u) {
-          // rows and columns outside the checkpoint: zero bytes, no access
-          const int k = lane + 32 * u, row = t0 + k;
-          const bool in = row < P.rows && m0 / kCkptBlock < P.spitch;
-          const uint8_t* src = P.scale + (in ? (int64_t)row * P.spitch + m0 / kCkptBlock : 0);
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                           smem_u32(raw_scale + s * kRawScales + k * 4)),
-                       "l"(src), "r"(in ? 4 : 0)
-                       : "memory");
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-      }
-    }
-    if (lane == 0) {
-      raw_issued[mine] = it;
-      if (!ok) {
-        abort_flag = 1;
-        set_error(P.err, DEVERR_TIMEOUT);
-      }
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else {
+  } else if (warp >= 12) {
     // ---- expansion ----
-    // a set's 32 tokens x 128 columns: thread t takes tokens t / 8 + 16 u,
-    // columns (t % 8) * 16 .. + 15
-    const int set = (warp - 8) >> 2, t = threadIdx.x & 127, kr = t >> 3, jc = t & 7;
+    // a set's 64 tokens x 128 columns of every kGroups-th slot: thread t takes
+    // tokens t / 8 + 16 u, columns (t % 8) * 16 .. + 15 (a warp's loads cover
+    // four whole 128-byte lines)
+    const int set = (warp - 12) >> 2, group = set >> 1, t = threadIdx.x & 127, jc = t & 7;
+    const int tr = (set & 1) * kSetTokens + (t >> 3);   // this thread's first token of a slot
     const uint32_t written0 = cluster_addr(full0, 0);
     // the slot addresses of a thread's two 16-byte halves; lanes 4-7 of every
     // eight store them in the other order, so that eight lanes cover all banks
-    const uint32_t g = (uint32_t)(jc >> 2) * kGroupBytes + (uint32_t)(set * kSetTokens + kr) * 128;
+    const uint32_t g = (uint32_t)(jc >> 2) * kGroupBytes + (uint32_t)tr * 128;
     const uint32_t first = (uint32_t)(jc >> 2), c0 = (uint32_t)((jc & 3) * 2);
-    const uint32_t off_a = g + (((c0 + first) ^ (kr & 7)) << 4), off_b = g + (((c0 + (first ^ 1)) ^ (kr & 7)) << 4);
-    constexpr int kPerRaw = kRawTokens / kSetTokens;   // sets that share a raw slot
-    const int raw_row = set % kPerRaw * kSetTokens + kr;
+    const uint32_t off_a = g + (((c0 + first) ^ (tr & 7)) << 4), off_b = g + (((c0 + (first ^ 1)) ^ (tr & 7)) << 4);
     constexpr int kU = kSetTokens / 16;
-    int blk = 0;
-    bool ok = true;
-    for (int x = pair; x < P.items && ok; x += npair) {
-      const Item w = item_of(P, x, nkb);
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++blk) {
-        const int it = blk * (kKB / kRawTokens) + set / kPerRaw, rs = it % kRaw, s = blk % kSlots;
-        ok = __all_sync(0xffffffffu, wait_bar(rfull0 + 8 * rs, (it / kRaw) & 1, &abort_flag));
-        if (!ok) break;
-        uint4 v[kU];
-        uint32_t e[kU];
+    const int64_t spitch = P.x.pitch / kCkptBlock;
+    // the load cursor: item, block, and the blocks left to the group's next
+    int lx = pair, lkb = 0, lend = 0, lm0 = 0;
+    auto open_item = [&]() {
+      const Item w = item_of(P, lx, nkb);
+      lkb = w.kb0;
+      lend = w.kb1;
+      lm0 = w.tile / P.tiles_n * kTile + h * kHalf;
+    };
+    auto skip = [&](int n) {   // n blocks on
+      while (lx < P.items && n >= lend - lkb) {
+        n -= lend - lkb;
+        lx += npair;
+        if (lx < P.items) open_item();
+      }
+      lkb += n;
+    };
+    uint4 v[kU];
+    uint32_t e[kU];
+    auto load = [&]() {
+      const int row = lkb * kKB + tr, col = lm0 + jc * 16;
+      const int8_t* q = P.x.q + (int64_t)row * P.x.pitch + col;
+      const uint8_t* sc = P.x.scale + (int64_t)row * spitch + col / kCkptBlock;
 #pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          v[u] = *reinterpret_cast<const uint4*>(raw + rs * kRawBytes + (raw_row + 16 * u) * kHalf + jc * 16);
-          e[u] = raw_scale[rs * kRawScales + (raw_row + 16 * u) * 4 + (jc >> 1)];
-        }
-        uint4 lo[kU], hi[kU];
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          const __nv_bfloat162 step = bf16_step(e[u]);
-          expand4(v[u].x, step, lo[u].x, lo[u].y);
-          expand4(v[u].y, step, lo[u].z, lo[u].w);
-          expand4(v[u].z, step, hi[u].x, hi[u].y);
-          expand4(v[u].w, step, hi[u].z, hi[u].w);
-        }
-        if (blk >= kSlots) {
-          ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ((blk / kSlots) & 1) ^ 1, &abort_flag));
-          if (!ok) break;
-        }
-        uint8_t* dst = ring + s * kSlotBytes;
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          *reinterpret_cast<uint4*>(dst + off_a + u * 16 * 128) = first ? hi[u] : lo[u];
-          *reinterpret_cast<uint4*>(dst + off_b + u * 16 * 128) = first ? lo[u] : hi[u];
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_cluster(written0 + 8 * s);
-          // (not before the values read have been used: an arrival overtakes
-          // the loads before it, and the slot was refilled under them)
-          mbar_arrive(rempty0 + 8 * rs);
+      for (int u = 0; u < kU; ++u) {
+        v[u] = make_uint4(0, 0, 0, 0);
+        e[u] = 7;
+        if (row + 16 * u < P.rows && col < P.x.pitch) {
+          v[u] = *reinterpret_cast<const uint4*>(q + 16 * u * P.x.pitch);
+          e[u] = sc[16 * u * spitch];
         }
       }
+    };
+    bool ok = true;
+    if (lx < P.items) open_item();
+    skip(group);
+    if (lx < P.items) load();
+    for (int blk = group; lx < P.items; blk += kGroups) {
+      const int s = blk % kSlots;
+      if (blk >= kSlots) {
+        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ((blk / kSlots) & 1) ^ 1, &abort_flag));
+        if (!ok) break;
+      }
+      uint8_t* dst = ring + s * kSlotBytes;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const __nv_bfloat162 step = bf16_step(e[u]);
+        uint4 lo, hi;
+        expand4(v[u].x, step, lo.x, lo.y);
+        expand4(v[u].y, step, lo.z, lo.w);
+        expand4(v[u].z, step, hi.x, hi.y);
+        expand4(v[u].w, step, hi.z, hi.w);
+        *reinterpret_cast<uint4*>(dst + off_a + u * 16 * 128) = first ? hi : lo;
+        *reinterpret_cast<uint4*>(dst + off_b + u * 16 * 128) = first ? lo : hi;
+      }
+      skip(kGroups);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(written0 + 8 * s);
+      if (lx < P.items) load();   // the next slot's bytes arrive while the tensor core is on the ones before it
     }
     if (!ok && lane == 0) {
       abort_flag = 1;
@@ -497,9 +470,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (abort_flag && threadIdx.x < 2)
-    for (int n = raw_issued[threadIdx.x], k = n - kRaw < 0 ? 0 : n - kRaw; k < n; ++k)
-      if ((k & 1) == (int)threadIdx.x) mbar_wait(rfull0 + 8 * (k % kRaw), (k / kRaw) & 1, kDrainLimitNs);
   if (abort_flag && leader && threadIdx.x == 0) {
     // dY's copies in flight complete on the even CTA's barriers; the slots
     // they fill may lack arrivals, so each wait may run to its limit
@@ -604,14 +574,7 @@ cudaError_t product(const ts_ops& h, WgradKernel& P, const TsCkpt& x, const TsMa
   int pairs = 0;
   cudaError_t e = resident_pairs(h.device, &pairs);
   if (e != cudaSuccess) return e;
-  const cuuint64_t qdims[2] = {(cuuint64_t)x.pitch, (cuuint64_t)rows}, qstrides[1] = {(cuuint64_t)x.pitch};
-  const cuuint32_t qbox[2] = {kHalf, kRawTokens};
-  if (enc(&P.q, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x.q, qdims, qstrides, qbox, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-          CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) !=
-      CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  P.scale = x.scale;
-  P.spitch = x.pitch / kCkptBlock;
+  P.x = x;
   P.rows = (int)rows;
   P.tiles_n = (P.n + kTile - 1) / kTile;
   const int tiles = (P.cols + kTile - 1) / kTile * P.tiles_n, nkb = (int)((rows + kKB - 1) / kKB);
