@@ -482,47 +482,122 @@ cudaError_t logprob_rows(const ts_ops& h, const LogprobArgs& a, cudaStream_t st)
   return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, 8>, a);
 }
 
+// One row's constants: dlogits = p (a - w log p) plus g at the token.
+struct RowGrad {
+  float lse, a, w, g;
+  int tok;      // -1: the row is not scored
+  bool zero;    // nothing to add up
+  __device__ __forceinline__ RowGrad(const LogprobArgs& p, int64_t row) {
+    lse = p.lse[row];
+    const int64_t t = p.tokens[row];
+    tok = t >= 0 && t < p.vocab ? (int)t : -1;
+    g = tok >= 0 ? p.g_logprob[row] : 0.f;
+    w = p.g_entropy ? p.g_entropy[row] : 0.f;
+    zero = lse == -INFINITY || (tok < 0 && w == 0.f);
+    a = -g;
+    if (w != 0.f) a -= w * p.entropy[row];
+  }
+  // Eight logits from column c on.
+  __device__ __forceinline__ void apply(float (&v)[8]) const {
+    const F2 m2 = pack2f(-lse, -lse), l2 = pack2f(kLog2e, kLog2e), a2 = pack2f(a, a), w2 = pack2f(-w, -w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const F2 d = add2(pack2f(v[2 * i], v[2 * i + 1]), m2);
+      float d0, d1;
+      unpack2f(mul2(d, l2), d0, d1);
+      const F2 e = pack2f(ex2(d0), ex2(d1));
+      F2 o = a2;
+      if (w != 0.f) {
+        unpack2f(d, d0, d1);   // (where p is 0 the product must be too)
+        o = fma2(w2, pack2f(max_nan(d0, -200.f), max_nan(d1, -200.f)), a2);
+      }
+      unpack2f(mul2(e, o), v[2 * i], v[2 * i + 1]);
+    }
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.f;
+    }
+  }
+};
+
+// VEC: logits and gradient lie alike against 16-byte boundaries (the same
+// type and pitch, or rows that start on one): a row's aligned chunks of eight
+// are one lane's each, what is left at its ends single lanes'.  A warp takes
+// kLpGroups consecutive groups of 32 chunks of a row, loaded together.
+constexpr int kLpGroups = 2;
+
 template <class TX, class TD, bool VEC>
-__global__ void __launch_bounds__(256) ts_logprob_backward_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(256) ts_logprob_backward_kernel(const LogprobArgs a, int per_row) {
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31;
-  const int per_row = (a.vocab + kGroupCols - 1) / kGroupCols;
-  const int64_t total = a.rows * per_row, step = (int64_t)gridDim.x * 8;
-  for (int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); i < total; i += step) {
-    const int64_t row = i / per_row;
-    const int c0 = (int)(i - row * per_row) * kGroupCols;
-    const TX* x = static_cast<const TX*>(a.logits.p) + row * a.logits.ld;
-    TD* d = static_cast<TD*>(a.dlogits.p) + row * a.dlogits.ld;
-    const float lse = a.lse[row];
-    const int64_t tok = a.tokens[row];
-    const bool scored = tok >= 0 && tok < a.vocab;
-    const float g = scored ? a.g_logprob[row] : 0.f;
-    const float w = a.g_entropy ? a.g_entropy[row] : 0.f, h = a.g_entropy ? a.entropy[row] : 0.f;
-    float v[8];
-    load_group<VEC>(x, c0, a.vocab, lane, v);
+  const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t row = i / per_row;
+  if (row >= a.rows) return;
+  const int g0 = (int)(i - row * per_row) * kLpGroups;
+  const TX* x = static_cast<const TX*>(a.logits.p) + row * a.logits.ld;
+  TD* d = static_cast<TD*>(a.dlogits.p) + row * a.dlogits.ld;
+  int first = 0, whole = a.vocab / kGroupCols * 32;   // the first whole chunk's column, and their number
+  if (VEC) {
+    const int off = (int)(reinterpret_cast<uintptr_t>(x) % 16 / sizeof(TX));
+    first = min(a.vocab, off ? (int)(16 / sizeof(TX)) - off : 0);
+    whole = (a.vocab - first) / 8;
+  }
+  float v[kLpGroups][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float lp = v[j] - lse;
-      const float p = lse == -INFINITY ? 0.f : expf(lp);
-      float o = scored ? -g * p : 0.f;
-      if (w != 0.f) o -= w * p * (fmaxf(lp, -200.f) + h);
-      if (c0 + group_col<VEC>(lane, j) == tok && lse != -INFINITY) o += g;
-      v[j] = o;
+  for (int u = 0; u < kLpGroups; ++u) {
+    if (VEC) {
+      const int c = (g0 + u) * 32 + lane;
+      if (c < whole) load8(x + first + c * 8, v[u]);
+    } else {
+      load_group<false>(x, (g0 + u) * kGroupCols, a.vocab, lane, v[u]);
     }
-    store_group<VEC>(d, c0, a.vocab, lane, v);
+  }
+  const RowGrad r(a, row);
+#pragma unroll
+  for (int u = 0; u < kLpGroups; ++u) {
+    r.apply(v[u]);
+    if (VEC) {
+      const int c = (g0 + u) * 32 + lane, col = first + c * 8;
+      if (c >= whole) continue;
+      if (!r.zero && (unsigned)(r.tok - col) < 8u) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (col + j == r.tok) v[u][j] += r.g;
+      }
+      store8(d + col, v[u]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!r.zero && (g0 + u) * kGroupCols + j * 32 + lane == r.tok) v[u][j] += r.g;
+      store_group<false>(d, (g0 + u) * kGroupCols, a.vocab, lane, v[u]);
+    }
+  }
+  if (VEC && g0 == 0) {
+    // the ends of the row, at most 14 logits
+    const int tail = first + whole * 8, c = lane < first ? lane : tail + lane - first;
+    if (c < a.vocab) {
+      float e[8] = {to_f32(x[c]), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      r.apply(e);
+      d[c] = from_f32<TD>(!r.zero && c == r.tok ? e[0] + r.g : e[0]);
+    }
   }
 }
 
 template <class TX, class TD>
-cudaError_t backward_types(const ts_ops& h, const LogprobArgs& a, cudaStream_t st) {
-  const int64_t groups = a.rows * ((a.vocab + kGroupCols - 1) / kGroupCols);
-  cudaLaunchConfig_t cfg = pdl_config((int)std::min<int64_t>((groups + 7) / 8, (int64_t)h.nsm * 8), 256, 0, st);
+cudaError_t backward_types(const LogprobArgs& a, cudaStream_t st) {
+  const auto off = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16; };
+  const bool alike = sizeof(TX) == sizeof(TD) && off(a.logits.p) == off(a.dlogits.p) &&
+                     a.logits.ld * (int64_t)sizeof(TX) % 16 == a.dlogits.ld * (int64_t)sizeof(TD) % 16;
+  const bool vec = alike || (rows_aligned(a.logits) && rows_aligned(a.dlogits));
+  const int per_row = (a.vocab + kGroupCols * kLpGroups - 1) / (kGroupCols * kLpGroups);
+  const int64_t blocks = (a.rows * per_row + 7) / 8;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = pdl_config((int)blocks, 256, 0, st);
   cudaLaunchAttribute at[1];
   pdl_attr(cfg, at);
-  return rows_aligned(a.logits) && rows_aligned(a.dlogits)
-             ? cudaLaunchKernelEx(&cfg, ts_logprob_backward_kernel<TX, TD, true>, a)
-             : cudaLaunchKernelEx(&cfg, ts_logprob_backward_kernel<TX, TD, false>, a);
+  return vec ? cudaLaunchKernelEx(&cfg, ts_logprob_backward_kernel<TX, TD, true>, a, per_row)
+             : cudaLaunchKernelEx(&cfg, ts_logprob_backward_kernel<TX, TD, false>, a, per_row);
 }
 
 }  // namespace
@@ -531,10 +606,10 @@ cudaError_t launch_token_logprobs(const ts_ops& h, const LogprobArgs& a, cudaStr
   return a.logits.bf16 ? logprob_rows<__nv_bfloat16, 4>(h, a, st) : logprob_rows<float, 2>(h, a, st);
 }
 
-cudaError_t launch_token_logprobs_backward(const ts_ops& h, const LogprobArgs& a, cudaStream_t st) {
+cudaError_t launch_token_logprobs_backward(const ts_ops&, const LogprobArgs& a, cudaStream_t st) {
   using B = __nv_bfloat16;
-  if (a.logits.bf16) return a.dlogits.bf16 ? backward_types<B, B>(h, a, st) : backward_types<B, float>(h, a, st);
-  return a.dlogits.bf16 ? backward_types<float, B>(h, a, st) : backward_types<float, float>(h, a, st);
+  if (a.logits.bf16) return a.dlogits.bf16 ? backward_types<B, B>(a, st) : backward_types<B, float>(a, st);
+  return a.dlogits.bf16 ? backward_types<float, B>(a, st) : backward_types<float, float>(a, st);
 }
 
 }  // namespace fg

@@ -208,8 +208,9 @@ __device__ __forceinline__ void ckpt_store_group(const TsCkpt& c, int64_t r, int
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const unsigned quad = 0xfu << (threadIdx.x & 28);   // (half warps may be in different rows)
+    m = max(m, __shfl_xor_sync(quad, m, 1));
+    m = max(m, __shfl_xor_sync(quad, m, 2));
     const int e = max((int)(m >> 23), 7);
     const float inv = ckpt_inv_step(e);
     uint32_t w[2] = {0, 0};
