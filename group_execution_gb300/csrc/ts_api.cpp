@@ -23,8 +23,9 @@ fg_status cuda_err(cudaError_t e, const char* what) {
 }
 fg_status done(cudaError_t e, const char* what) { return e == cudaSuccess ? FG_OK : cuda_err(e, what); }
 
-// Rows and columns index with 32 bits inside a kernel (offsets are 64-bit).
-constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 1024;
+// Rows and columns index with 32 bits inside a kernel, some rows past the last
+// one among them (offsets are 64-bit).
+constexpr int64_t kMaxExtent = (int64_t(1) << 31) - 65536;
 
 fg_status check_handle(const ts_ops* h) {
   if (!h) return err(FG_EINVAL, "null handle");

@@ -539,8 +539,8 @@ void tf_layout_destroy(tf_layout* l);
  * bytes run faster); vectors and row statistics are dense float32.  All
  * arithmetic and all sums are in float32; a bf16 output is rounded once.  No
  * output may overlap an input except where stated.  rows = 0 computes empty
- * sums; cols is at least 1.  Results do not depend on scheduling: no sum uses
- * atomics.
+ * sums; cols is at least 1; extents are at most 2^31 - 65536.  Results do not
+ * depend on scheduling: no sum uses atomics.
  *
  * A ts_ops handle belongs to the device that is current in ts_create (calls
  * with another current device return FG_EINVAL) and owns a workspace and a

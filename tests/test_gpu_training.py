@@ -555,3 +555,42 @@ def test_refusals(ops):
     assert lib.ts_checkpoint_save(h, p, 0, 64, 4, 64, C.c_void_p(ck.ptr + 8), None) == E
     assert lib.ts_weight_grad(h, ck.ptr, 4, 64, None, None, p, 1, 64, 1 << 21, p, 1 << 21, None, 0, None) in (S, U)
     ops.sync()
+
+
+# ---- the operators together --------------------------------------------------------
+
+
+def test_training_step_example():
+    from examples import training_step as T
+    m = T.Model(tokens=200, width=96, hidden=160, vocab=328, seed=3)
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((200, 96), generator=gen, device="cuda")
+    t = torch.randint(0, 328, (200,), generator=gen, device="cuda")
+    loss = m.step(x, t)
+    m.ops.sync()
+    # the same step in 64 bits, rounded where the step rounds: the matmuls'
+    # operands to bf16, the saved activations to 8 bits
+    gamma, beta, w1, b1, w2 = (host(p) for p in m.params)
+    w1, w2 = rounded(w1, BF16), rounded(w2, BF16)
+    y, _, rstd, h = OT.layer_norm(host(x), gamma, beta)
+    saved_norm = OT.checkpoint_decode(OT.checkpoint_encode(h), 200, 96)
+    acts = np.maximum(rounded(y, BF16) @ w1 + b1, 0)
+    saved_acts = OT.checkpoint_decode(OT.checkpoint_encode(acts), 200, 160)
+    logits, tokens = saved_acts @ w2, t.cpu().numpy()
+    want_loss = -OT.token_logprobs(logits, tokens)[0].mean()
+    dlogits = rounded(OT.token_logprobs_backward(logits, tokens, np.full(200, -1.0 / 200)), BF16)
+    dw2 = OT.weight_grad(saved_acts, dlogits)[0]
+    dhidden = rounded(OT.activation_backward("relu", dlogits @ w2.T, saved_acts), BF16)
+    dw1, db1 = OT.weight_grad(saved_norm, dhidden, gamma, beta)
+    dx, dgamma, dbeta = OT.layer_norm_backward(dhidden @ w1.T, saved_norm, rstd, gamma)
+    assert abs(loss.item() - want_loss) < 1e-4 * want_loss
+    # a value that lies on the edge of its rounding may go the other way, 2^-8
+    # of itself in bf16: were it all of them, that is what the results are off
+    for got, want in zip(m.grads + [m.dx], [dgamma, dbeta, dw1, db1, dw2, dx]):
+        assert np.linalg.norm(host(got) - want) <= 2.0 ** -8 * np.linalg.norm(want)
+
+
+def test_training_example_learns():
+    from examples import training_step as T
+    losses = T.main(steps=12)
+    assert losses[-1] < 0.9 * losses[0] and all(b < a for a, b in zip(losses, losses[1:]))
