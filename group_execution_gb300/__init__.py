@@ -28,7 +28,8 @@ def __getattr__(name):
     # loaded on first use: the rest of the package imports without PyTorch
     if name in ("TrainingOps", "Checkpoint", "checkpoint_layout"):
         from . import training
-        return getattr(training, name)
+        value = globals()[name] = getattr(training, name)
+        return value
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -26,7 +26,7 @@ def _matrix(name, t, rows, cols):
         raise FgError(FG_EINVAL, f"{name}: must be float32 or bfloat16")
     if not t.is_cuda:
         raise FgError(FG_EINVAL, f"{name}: must be a CUDA tensor")
-    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+    if t.shape != (rows, cols):
         raise FgError(FG_ESHAPE, f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
     ld, inner = t.stride()
     if inner != 1 and cols > 1:
@@ -40,7 +40,7 @@ def _array(name, t, shape, dtype=torch.float32):
     """Pointer of a dense array argument (None passes through)."""
     if t is None:
         return None
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda:
         raise FgError(FG_EINVAL, f"{name}: must be a CUDA tensor of {dtype}")
     if t.shape != shape:
         raise FgError(FG_ESHAPE, f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
