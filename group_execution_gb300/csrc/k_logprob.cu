@@ -191,8 +191,8 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
 // their logits picked from.  Should the list overflow (logits in rising
 // order), its own k-th largest is the next bound and the row is read again
 // for the list alone; the bound rises every time.
-template <class T, int U, int W>
-__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, W == 1 ? 8 : 4) ts_logprob_kernel(const LogprobArgs a) {
+template <class T, int U, int W, int BLOCKS>
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kernel(const LogprobArgs a) {
   constexpr int kRows = W == 1 ? 4 : 1, kN = W * 32;   // rows a block, threads a row
   __shared__ LpShared<W> shared[kRows];
   pdl_launch_dependents();
@@ -456,30 +456,44 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, W == 1 ? 8 : 4) ts_logp
   }
 }
 
-constexpr int kWarpRow = 2048;   // columns up to which one warp takes a row (its list holds every chunk)
+// Which rows get how many warps, measured at k = 8:
+// - up to 2048 columns one (its list holds every chunk): 16384 x 2000 bf16
+//   takes 30 us, with four warps a row 77;
+// - with at most four rows a SM eight, and the row cut into segments for a
+//   cluster's CTAs while that leaves two blocks on every SM and two chunks a
+//   thread: 600 x 50000 bf16 takes 18 us, with the four warps below 23;
+// - else up to 16384 columns four, whose many short rows hide each other's
+//   barriers: 4096 x 4000 bf16 takes 24 us, with eight 37, 4096 x 16000 f32 54
+//   against 61;
+// - beyond, eight at five blocks a SM rather than four, with a few registers
+//   spilled: 2048 x 65536 f32 (k = 20) takes 95 us against 100, with four
+//   warps 151.
+constexpr int kWarpRow = 2048, kQuarterRow = 16384;
 
-// Segments a row: enough for about two blocks on every SM, of two chunks a
-// thread at least.
-template <class T, int U>
-cudaError_t logprob_rows(const ts_ops& h, const LogprobArgs& a, cudaStream_t st) {
+template <class T, int U, int W, int BLOCKS>
+cudaError_t logprob_launch(const LogprobArgs& a, int64_t blocks, int cluster, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = pdl_config((int)blocks, W == 1 ? 128 : W * 32, 0, st);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  if (a.vocab <= kWarpRow) {
-    cudaLaunchConfig_t cfg = pdl_config((int)((a.rows + 3) / 4), 128, 0, st);
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, 1>, a);
-  }
-  int ncl = 1;
-  while (ncl < kMaxCluster && a.rows * ncl * 2 <= 2 * (int64_t)h.nsm && a.vocab / (ncl * 2) >= 256 * 16) ncl *= 2;
-  cudaLaunchConfig_t cfg = pdl_config((int)(a.rows * ncl), 256, 0, st);
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = ncl;
+  at[1].val.clusterDim.x = cluster;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, 8>, a);
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, ts_logprob_kernel<T, U, W, BLOCKS>, a);
+}
+
+template <class T, int U>
+cudaError_t logprob_rows(const ts_ops& h, const LogprobArgs& a, cudaStream_t st) {
+  if (a.vocab <= kWarpRow) return logprob_launch<T, U, 1, 8>(a, (a.rows + 3) / 4, 1, st);
+  if (a.rows <= 4 * (int64_t)h.nsm) {
+    int ncl = 1;
+    while (ncl < kMaxCluster && a.rows * ncl * 2 <= 2 * (int64_t)h.nsm && a.vocab / (ncl * 2) >= 256 * 16) ncl *= 2;
+    return logprob_launch<T, U, 8, 4>(a, a.rows * ncl, ncl, st);
+  }
+  if (a.vocab <= kQuarterRow) return logprob_launch<T, U, 4, 8>(a, a.rows, 1, st);
+  return logprob_launch<T, U, 8, 5>(a, a.rows, 1, st);
 }
 
 // One row's constants: dlogits = p (a - w log p) plus g at the token.

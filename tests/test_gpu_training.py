@@ -406,6 +406,15 @@ def test_token_logprobs(ops, rows, vocab, dtype, pad, kind, k):
         assert (np.abs(g[ok] - tlp[ok]) <= (2.0 ** -22 * (big + 16) * 4)[ok]).all()
 
 
+# more rows than the SMs' blocks at one time: other numbers of warps to a row
+@pytest.mark.parametrize("k", [0, 32])
+@pytest.mark.parametrize("kind", ["normal", "ties", "masked", "awkward"])
+@pytest.mark.parametrize("dtype, pad", [(F32, 3), (BF16, 7)])
+@pytest.mark.parametrize("vocab", [2051, 16384, 16391])
+def test_token_logprobs_many_rows(ops, vocab, dtype, pad, kind, k):
+    test_token_logprobs(ops, 650, vocab, dtype, pad, kind, k)
+
+
 @pytest.mark.parametrize("entropy", [False, True])
 @pytest.mark.parametrize("kind", ["normal", "masked"])
 @pytest.mark.parametrize("xt, dt", TYPES)
