@@ -4,8 +4,11 @@
 //
 // A checkpoint's values are exact in bf16 (8 bits of significand) and the
 // step's division is exact, so rounding to the nearest step is the only
-// rounding on the way.  Each kernel is one pass; device memory bounds them (92 to
-// 97 % of its copy rate at 8192 x 4096, 65 % for saving bf16).
+// rounding on the way.  Each kernel is one pass, bound by device memory: at 8192
+// x 4096 saving f32 takes 27 us (93 % of the copy rate), bf16 22 (67 %: the
+// blocks' maxima and roundings are instructions a column, whatever its type),
+// loading to bf16 16 (91 %), to f32 32 (77 %), relu's derivative in bf16 27
+// (92 %).
 #include <algorithm>
 
 #include "launch.h"

@@ -4,7 +4,11 @@
 // with h optionally saved as an 8-bit checkpoint in the same pass.
 //
 // Two passes over values that stay in registers: the variance is taken about
-// the mean that was found, so it neither cancels nor goes negative.
+// the mean that was found, so it neither cancels nor goes negative.  Bound by
+// memory where rows are wide types, else by the two reductions a row between
+// its loads and its stores: 8192 x 4096 takes 53 us in f32 (74 % of the copy
+// rate), 33 in bf16 (60 %), 44 from f32 to bf16 with the checkpoint (79 %);
+// 64 x 1024 f32 3.7, of which a launch is 2 to 3.
 #include <algorithm>
 #include <atomic>
 
@@ -118,7 +122,8 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8
 }
 
 // Rows too long for registers: one block a row, which reads it three times
-// (the later two from L2).
+// (the later two from L2).  1024 x 32768 bf16 takes 68 us, where one reading
+// and the store at the copy rate take 20.
 template <class TX, class TY, bool VEC>
 __global__ void __launch_bounds__(1024) ts_norm_long_kernel(const NormArgs a) {
   __shared__ float red[2][32];
@@ -195,6 +200,8 @@ cudaError_t norm_walk(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
 template <class TX, class TY, bool VEC>
 cudaError_t norm_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
   const int groups = (a.cols + kGroupCols - 1) / kGroupCols;
+  // a warp to a row while four groups hold it (no barrier), then the fewest
+  // warps whose registers do
   if (groups <= 4) return norm_walk<TX, TY, VEC, 1, 4>(h, a, st);
   if (groups <= 16) return norm_walk<TX, TY, VEC, 8, 2>(h, a, st);
   if (groups <= 32) return norm_walk<TX, TY, VEC, 16, 2>(h, a, st);

@@ -27,7 +27,6 @@ struct FromX {
   __device__ __forceinline__ void advance(const NormArgs& a, int64_t rows) { row += rows * a.x.ld; }
   template <bool VEC>
   struct Raw {
-    static constexpr int kRegs = VEC ? (int)sizeof(TX) * 2 : 8;
     RawGroup<TX, VEC> x;
     __device__ __forceinline__ void load(const NormArgs& a, const FromX& s, int c0, int lane) {
       x.load(s.row, c0, a.cols, lane);
@@ -49,7 +48,6 @@ struct FromCkpt {
   __device__ __forceinline__ void advance(const NormArgs&, int64_t rows) { move(rows); }
   template <bool VEC>
   struct Raw {
-    static constexpr int kRegs = VEC ? 3 : 10;
     RawCkpt<VEC> c;
     __device__ __forceinline__ void load(const NormArgs&, const FromCkpt& s, int c0, int lane) {
       c.load(s.row, 0, c0, lane);
@@ -70,7 +68,11 @@ __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, i
   }
 }
 
-// dx alone: one block a row, any length.
+// dx alone: one block a row, any length.  With the column sums' kernel below,
+// which reads the operands again, it takes the rows beyond 8192 columns, which
+// the registers of one block do not hold with the next rows in flight: 2048 x
+// 16384 bf16 99 us (30 % of the copy rate).  (A ring of rows in shared memory
+// took 87 there and was slower at all shorter rows.)
 template <class TDY, class Src, bool VEC>
 __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
   __shared__ float red[2][8];
@@ -223,6 +225,10 @@ __device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
 // Bound by instruction issue before memory in bf16 (eight columns a lane and
 // row: two loads, one store and about 100 other instructions), so pairs of
 // float32 operations go in one instruction and addresses advance by addition.
+// 8192 x 4096 takes 47 us in bf16 (63 % of the copy rate), 46 from the
+// checkpoint, 70 in f32 (85 %); G = 2 at 4096 x 8192 bf16 takes 54.  1021 x
+// 5003 f32 from the checkpoint, whose rows start at odd elements and come
+// by single ones, takes 24 us (29 %).  About 4 us of each is the kernel that adds the partials.
 template <class TDY, class Src, bool VEC, int G, int D, int K>
 __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs a, int W, float* part) {
   __shared__ float red[2][16][4];   // [warp][value]
@@ -454,13 +460,12 @@ cudaError_t backward_fused(const ts_ops& h, const NormArgs& a, int W, cudaStream
 
 template <class TDY, class Src, bool VEC>
 cudaError_t backward_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
-  // pairs of rows in flight: what about 32 registers hold
-  constexpr int kRegs = (VEC ? (int)sizeof(TDY) * 2 : 8) + Src::template Raw<VEC>::kRegs;
-  constexpr int D = 1;
+  // Up to 4096 columns the next pair of rows in flight; 8192 x 4096 bf16 took
+  // 52 us by single rows.
   if (a.rows > 0 && a.cols <= 16 * kGroupCols) {
     int W = 1;
     while (W * kGroupCols < a.cols) W *= 2;
-    return backward_fused<TDY, Src, VEC, 1, D, 2>(h, a, W, st);
+    return backward_fused<TDY, Src, VEC, 1, 1, 2>(h, a, W, st);
   }
   if (a.rows > 0 && a.cols <= 32 * kGroupCols) return backward_fused<TDY, Src, VEC, 2, 1, 1>(h, a, 16, st);
   if (a.rows > 0) {
