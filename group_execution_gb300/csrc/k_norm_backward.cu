@@ -8,6 +8,7 @@
 // workspace, then a second kernel adds the partials in block order.  The
 // result depends on the sizes alone, not on scheduling.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "launch.h"
@@ -15,6 +16,12 @@
 
 namespace fg {
 namespace {
+
+// A row of a block of 1024 threads, on its way to L2.
+__device__ __forceinline__ void prefetch_row(const void* p, int bytes) {
+  for (int i = threadIdx.x * 128; i < bytes; i += 1024 * 128)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(p) + i));
+}
 
 // Where the normalised row h comes from: x, or the checkpoint.  An object is a
 // cursor on a row; Raw holds a group of it as it lies in memory.
@@ -34,6 +41,9 @@ struct FromX {
     __device__ __forceinline__ void get(float (&v)[8]) const { x.get(v); }   // x itself
   };
   __device__ __forceinline__ static float mean(const NormArgs& a, int64_t row) { return a.mean[row]; }
+  __device__ __forceinline__ static void prefetch(const NormArgs& a, int64_t row) {
+    prefetch_row(static_cast<const TX*>(a.x.p) + row * a.x.ld, a.cols * (int)sizeof(TX));
+  }
 };
 template <class TDX>
 struct FromCkpt {
@@ -55,6 +65,10 @@ struct FromCkpt {
     __device__ __forceinline__ void get(float (&v)[8]) const { c.get(v); }   // h
   };
   __device__ __forceinline__ static float mean(const NormArgs&, int64_t) { return 0.f; }
+  __device__ __forceinline__ static void prefetch(const NormArgs& a, int64_t row) {
+    prefetch_row(a.ckpt.q + row * a.ckpt.pitch, (int)a.ckpt.pitch);
+    prefetch_row(a.ckpt.scale + row * (a.ckpt.pitch / kCkptBlock), (int)(a.ckpt.pitch / kCkptBlock));
+  }
 };
 template <class Src, bool VEC>
 __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, int lane, float mean, float rstd,
@@ -69,10 +83,8 @@ __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, i
 }
 
 // dx alone: one block a row, any length.  With the column sums' kernel below,
-// which reads the operands again, it takes the rows beyond 8192 columns, which
-// the registers of one block do not hold with the next rows in flight: 2048 x
-// 16384 bf16 99 us (30 % of the copy rate).  (A ring of rows in shared memory
-// took 87 there and was slower at all shorter rows.)
+// which reads the operands again, it takes the rows that no block's registers
+// hold, beyond 16384 columns.
 template <class TDY, class Src, bool VEC>
 __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
   __shared__ float red[2][8];
@@ -225,10 +237,11 @@ __device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
 // Bound by instruction issue before memory in bf16 (eight columns a lane and
 // row: two loads, one store and about 100 other instructions), so pairs of
 // float32 operations go in one instruction and addresses advance by addition.
-// 8192 x 4096 takes 47 us in bf16 (63 % of the copy rate), 46 from the
-// checkpoint, 70 in f32 (85 %); G = 2 at 4096 x 8192 bf16 takes 54.  1021 x
-// 5003 f32 from the checkpoint, whose rows start at odd elements and come
-// by single ones, takes 24 us (29 %).  About 4 us of each is the kernel that adds the partials.
+// 8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 66 in f32 (90 %); G
+// = 2 at 4096 x 8192 bf16 takes 48.  (A partial written by single elements,
+// 32 bytes apart across a warp, cost 3 to 7 us.)  1021 x 5003 f32 from the
+// checkpoint, whose rows start at odd elements and come by single ones, takes
+// 24 us (29 %).  About 4 us of each is the kernel that adds the partials.
 template <class TDY, class Src, bool VEC, int G, int D, int K>
 __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs a, int W, float* part) {
   __shared__ float red[2][16][4];   // [warp][value]
@@ -357,21 +370,31 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
   float* p = part + (int64_t)blockIdx.x * 2 * a.cols;
   const int width = W * kGroupCols;
 #pragma unroll
-  for (int g = 0; g < G; ++g)
+  for (int g = 0; g < G; ++g) {
+    float b[8], q[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      unpack2f(sb[g][j], b[2 * j], b[2 * j + 1]);
+      unpack2f(sg[g][j], q[2 * j], q[2 * j + 1]);
+    }
+    const int c0 = (g * W + warp) * kGroupCols;
+    if (VEC && slots == 1 && a.cols % 4 == 0 && c0 + lane * 8 + 8 <= a.cols) {
+      store8(p + c0 + lane * 8, b);   // (a partial's rows start on 16 bytes)
+      store8(p + a.cols + c0 + lane * 8, q);
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int c = (g * W + warp) * kGroupCols + group_col<VEC>(lane, j);
-      float b[2], q[2];
-      unpack2f(sb[g][j / 2], b[0], b[1]);
-      unpack2f(sg[g][j / 2], q[0], q[1]);
+      const int c = c0 + group_col<VEC>(lane, j);
       if (G == 1 && slots > 1) {
-        sums[(slot * 2 + 0) * width + c] = b[j & 1];
-        sums[(slot * 2 + 1) * width + c] = q[j & 1];
+        sums[(slot * 2 + 0) * width + c] = b[j];
+        sums[(slot * 2 + 1) * width + c] = q[j];
       } else if (c < a.cols) {
-        p[c] = b[j & 1];
-        p[a.cols + c] = q[j & 1];
+        p[c] = b[j];
+        p[a.cols + c] = q[j];
       }
     }
+  }
   if (G == 1 && slots > 1) {
     __syncthreads();
     for (int i = threadIdx.x; i < 2 * width; i += 512) {
@@ -381,6 +404,124 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
       for (int k = 0; k < slots; ++k) v += sums[(k * 2 + which) * width + c];
       p[which * a.cols + c] = v;
     }
+  }
+}
+
+// Rows of up to 16384 columns: dx and the partial column sums in one pass, a
+// block of 32 warps to an SM, two groups of 256 columns a warp.  gamma and the
+// column sums live in shared memory (192 KB), where a thread meets its own
+// columns alone, four at a time; the registers hold the row, and the next one
+// is on its way to L2.  2048 x 16384 bf16 takes 50 us (59 % of the copy rate;
+// by the two kernels that longer rows take, 99), 2388 x 10336 f32 78 (129).  Up
+// to 8192 columns, where column sums fit the registers above, those are
+// faster: 4096 x 8192 bf16 48 us, here 82.
+constexpr int kWideGroups = 2, kWidePlane = kWideGroups * 2 * 1024;   // float4s of one value a column
+constexpr int kWideSmem = 3 * kWidePlane * 16;
+
+template <class TDY, class Src, bool VEC>
+__global__ void __launch_bounds__(1024, 1) ts_norm_backward_wide_kernel(const NormArgs a, float* part) {
+  extern __shared__ float4 wide[];
+  __shared__ float red[2][2][32];   // [value][warp]
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float4* const gamma = wide + threadIdx.x;   // [group][half][thread]
+  float4* const sb = gamma + kWidePlane;
+  float4* const sg = sb + kWidePlane;
+#pragma unroll
+  for (int g = 0; g < kWideGroups; ++g) {
+    float v[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (a.gamma) load_group<VEC>(a.gamma, (g * 32 + warp) * kGroupCols, a.cols, lane, v);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      gamma[(g * 2 + i) * 1024] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      sb[(g * 2 + i) * 1024] = sg[(g * 2 + i) * 1024] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  const float n = 1.f / (float)a.cols;
+  int buf = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const TDY* dyp = static_cast<const TDY*>(a.dy.p) + row * a.dy.ld;
+    const Src src(a, row);
+    RawGroup<TDY, VEC> dy[kWideGroups];
+    typename Src::template Raw<VEC> x[kWideGroups];
+#pragma unroll
+    for (int g = 0; g < kWideGroups; ++g) {
+      dy[g].load(dyp, (g * 32 + warp) * kGroupCols, a.cols, lane);
+      x[g].load(a, src, (g * 32 + warp) * kGroupCols, lane);
+    }
+    const float rs = a.rstd[row], mean = Src::mean(a, row);
+    if (row + gridDim.x < a.rows) {
+      prefetch_row(dyp + gridDim.x * a.dy.ld, a.cols * (int)sizeof(TDY));
+      Src::prefetch(a, row + gridDim.x);
+    }
+    const F2 scale = pack2f(rs, rs), shift = pack2f(-mean, -mean);
+    F2 u[kWideGroups][4], h[kWideGroups][4], s1 = 0, s2 = 0;
+#pragma unroll
+    for (int g = 0; g < kWideGroups; ++g) {
+      float du[8], dh[8];
+      dy[g].get(du);
+      x[g].get(dh);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = (g * 2 + i) * 1024;
+        const float4 gm = gamma[at];
+        float4 b = sb[at], q = sg[at];
+        const F2 g2[2] = {pack2f(gm.x, gm.y), pack2f(gm.z, gm.w)};
+        F2 b2[2] = {pack2f(b.x, b.y), pack2f(b.z, b.w)}, q2[2] = {pack2f(q.x, q.y), pack2f(q.z, q.w)};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int e = i * 4 + j * 2;
+          const F2 v = pack2f(du[e], du[e + 1]);
+          F2 hh = pack2f(dh[e], dh[e + 1]);
+          if (!Src::kCkpt) hh = mul2(add2(hh, shift), scale);
+          b2[j] = add2(b2[j], v);
+          q2[j] = fma2(v, hh, q2[j]);
+          const F2 w = mul2(v, g2[j]);
+          s1 = add2(s1, w);
+          s2 = fma2(w, hh, s2);
+          u[g][i * 2 + j] = w;
+          h[g][i * 2 + j] = hh;
+        }
+        unpack2f(b2[0], b.x, b.y);
+        unpack2f(b2[1], b.z, b.w);
+        unpack2f(q2[0], q.x, q.y);
+        unpack2f(q2[1], q.z, q.w);
+        sb[at] = b;
+        sg[at] = q;
+      }
+    }
+    const float s[2] = {sum2(s1), sum2(s2)};
+    float v = warp_sums<1>(s, lane);
+    if (lane % 16 == 0) red[buf][lane / 16][warp] = v;
+    __syncthreads();
+    // sixteen lanes to a value, two warps' sums each
+    v = red[buf][lane / 16][lane % 16 * 2] + red[buf][lane / 16][lane % 16 * 2 + 1];
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    buf ^= 1;   // (the next sums go to the other half, so one barrier is enough)
+    v *= -rs * n;
+    const float m1 = __shfl_sync(0xffffffffu, v, 0), m2 = __shfl_sync(0xffffffffu, v, 16);
+    const F2 a1 = pack2f(m1, m1), a2 = pack2f(m2, m2);
+    typename Src::Dx* dx = static_cast<typename Src::Dx*>(a.dx.p) + row * a.dx.ld;
+#pragma unroll
+    for (int g = 0; g < kWideGroups; ++g) {
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        unpack2f(fma2(h[g][j], a2, fma2(u[g][j], scale, a1)), o[2 * j], o[2 * j + 1]);
+      store_group<VEC>(dx, (g * 32 + warp) * kGroupCols, a.cols, lane, o);
+    }
+  }
+  if (!part) return;
+  __syncthreads();
+  float* p = part + (int64_t)blockIdx.x * 2 * a.cols;
+  const float* sums = reinterpret_cast<const float*>(wide + kWidePlane);
+  for (int c = threadIdx.x; c < a.cols; c += 1024) {
+    const int group = c / kGroupCols, in = c % kGroupCols, l = VEC ? in / 8 : in % 32, j = VEC ? in % 8 : in / 32;
+    const int at = ((group / 32 * 2 + j / 4) * 1024 + group % 32 * 32 + l) * 4 + j % 4;
+    p[c] = sums[at];
+    p[a.cols + c] = sums[kWidePlane * 4 + at];
   }
 }
 
@@ -426,7 +567,7 @@ int column_parts(const ts_ops& h, int64_t rows, int cols) {
   const int64_t tiles = (cols + kGroupCols - 1) / kGroupCols;
   int64_t p = (8 * (int64_t)h.nsm + tiles - 1) / tiles;
   p = std::min(p, (rows + 63) / 64);
-  p = std::min(p, (h.ws_bytes - 8 * (int64_t)cols) / (8 * (int64_t)cols));
+  p = std::min(p, (h.ws_bytes - 8 * (int64_t)cols - 256) / (8 * (int64_t)cols));
   return (int)std::max<int64_t>(std::min<int64_t>(p, 65535), 1);
 }
 
@@ -459,6 +600,27 @@ cudaError_t backward_fused(const ts_ops& h, const NormArgs& a, int W, cudaStream
 }
 
 template <class TDY, class Src, bool VEC>
+cudaError_t backward_wide(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
+  static std::atomic<uint64_t> ready{0};   // devices whose shared memory is opted in
+  const uint64_t bit = h.device < 64 ? 1ull << h.device : 0;
+  if (!bit || !(ready.load(std::memory_order_acquire) & bit)) {
+    cudaError_t e = cudaFuncSetAttribute(ts_norm_backward_wide_kernel<TDY, Src, VEC>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kWideSmem);
+    if (e != cudaSuccess) return e;
+    ready.fetch_or(bit, std::memory_order_release);
+  }
+  int64_t grid = std::min<int64_t>(a.rows, h.nsm);
+  grid = std::max<int64_t>(1, std::min(grid, (h.ws_bytes - 8 * (int64_t)a.cols) / (8 * (int64_t)a.cols)));
+  float* part = a.dgamma || a.dbeta ? reinterpret_cast<float*>(h.ws) : nullptr;
+  cudaLaunchConfig_t cfg = pdl_config((int)grid, 1024, kWideSmem, st);
+  cudaLaunchAttribute at[1];
+  pdl_attr(cfg, at);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ts_norm_backward_wide_kernel<TDY, Src, VEC>, a, part);
+  if (e != cudaSuccess || !part) return e;
+  return finish_columns(part, (int)grid, a.cols, a.dbeta, a.dgamma, a.accumulate, nullptr, st);
+}
+
+template <class TDY, class Src, bool VEC>
 cudaError_t backward_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
   // Up to 4096 columns the next pair of rows in flight; 8192 x 4096 bf16 took
   // 52 us by single rows.
@@ -468,6 +630,7 @@ cudaError_t backward_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
     return backward_fused<TDY, Src, VEC, 1, 1, 2>(h, a, W, st);
   }
   if (a.rows > 0 && a.cols <= 32 * kGroupCols) return backward_fused<TDY, Src, VEC, 2, 1, 1>(h, a, 16, st);
+  if (a.rows > 0 && a.cols <= kWideGroups * 32 * kGroupCols) return backward_wide<TDY, Src, VEC>(h, a, st);
   if (a.rows > 0) {
     cudaLaunchConfig_t cfg = pdl_config((int)a.rows, 256, 0, st);
     cudaLaunchAttribute at[1];
