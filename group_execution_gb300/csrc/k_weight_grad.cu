@@ -43,7 +43,7 @@
 //
 // Rows of dY that TMA cannot read (a start or pitch off 16 bytes) are first
 // copied to the workspace at an aligned pitch, as many tokens at a time as
-// fit there.
+// half of it takes.
 //
 // Every wait is bounded; on expiry the CTA records the error, drains its
 // copies, frees its TMEM and returns.
@@ -71,7 +71,10 @@ constexpr int kSets = 2 * kGroups;               // two sets of four warps a gro
 constexpr int kSetTokens = kKB / 2;
 constexpr int kExpandWarps = 4 * kSets;
 constexpr int kThreads = (12 + kExpandWarps) * 32;
-constexpr int kSmem = kSlots * kSlotBytes + 1024;
+constexpr int kStagePitch = 17;                  // floats of a row of 16 columns on the way to an unaligned dw
+constexpr int kStageFloats = 32 * kStagePitch;   // an epilogue warp's
+template <bool WIDE>
+constexpr int kSmem = kSlots * kSlotBytes + 1024 + (WIDE ? 0 : 8 * kStageFloats * 4);
 constexpr int kChain = 16;                       // blocks of kKB tokens one accumulation runs over
 constexpr int64_t kWaitNs = 2000000000LL;
 constexpr int64_t kPieceFloats = (int64_t)kTile * kTile;
@@ -151,10 +154,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Stores eight values of one row of dw from column j (vec: 8, 4 or 1 floats
-// at a time), scaled, shifted and accumulated as asked.
-__device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j, float g, float b, int vec,
-                                        float (&v)[8]) {
+// Eight values of one row of dw from column j, scaled and shifted as asked.
+__device__ __forceinline__ void affine8(const WgradKernel& P, int j, float g, float b, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= g;
   if (P.beta) {
@@ -168,6 +169,11 @@ __device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j,
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] += b * s[i];
   }
+}
+// Stores them (vec: 8 or 4 floats at a time), accumulated as asked.
+__device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j, float g, float b, int vec,
+                                        float (&v)[8]) {
+  affine8(P, j, g, b, v);
   float* d = row + j;
   if (vec == 8 && j + 8 <= P.n) {
     if (P.accumulate) {
@@ -179,7 +185,7 @@ __device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j,
     asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(d), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                  "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                  : "memory");
-  } else if (vec >= 4 && j + 8 <= P.n) {
+  } else if (j + 8 <= P.n) {
     if (P.accumulate) {
       float o[8];
       load8(d, o);
@@ -193,11 +199,15 @@ __device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j,
       if (j + i < P.n) d[i] = P.accumulate ? d[i] + v[i] : v[i];
   }
 }
-__device__ __forceinline__ int store_width(const WgradKernel& P) {
+// The floats of dw that a thread stores at a time; 1: a row is spread over
+// threads.
+__host__ __device__ __forceinline__ int store_width(const WgradKernel& P) {
   const uint64_t p = reinterpret_cast<uint64_t>(P.dw);
   return p % 32 == 0 && P.lddw % 8 == 0 ? 8 : p % 16 == 0 && P.lddw % 4 == 0 ? 4 : 1;
 }
 
+// WIDE: rows of dw on 16 bytes, at least.
+template <bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_wgrad_kernel(const __grid_constant__ WgradKernel P) {
   extern __shared__ uint8_t smem_raw[];
@@ -321,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---- epilogue ----
     const int q = warp & 3;   // the TMEM lane quarter this warp may access
     const int r = q * 32 + lane;
-    const int vec = store_width(P);
+    const int vec = WIDE ? store_width(P) : 1;
     // partials: [64 column quads][128 rows][4], so that a warp's 16-byte
     // accesses cover 512 contiguous bytes
     float4* chain = P.chain + (int64_t)(pair * 2 + h) * (kPieceFloats / 8) + r;
@@ -368,14 +378,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
               dst[(j / 4 + k) * kHalf] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
-          } else if (c < P.cols) {
+          } else if constexpr (WIDE) {
+            if (c < P.cols) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float e[8];
+#pragma unroll
+                for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
+                finish8(P, row, n0 + j + 8 * k, g, be, vec, e);
+              }
+            }
+          } else {
+            // rows of dw off 16 bytes go out through shared memory, half a
+            // warp to a row: 786 x 2810 x 1142 takes 16 us, a thread to a row 31
+            float* stage = reinterpret_cast<float*>(ring + kSlots * kSlotBytes) + (warp - 4) * kStageFloats;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
               float e[8];
 #pragma unroll
               for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
-              finish8(P, row, n0 + j + 8 * k, g, be, vec, e);
+              affine8(P, n0 + j + 8 * k, g, be, e);
+#pragma unroll
+              for (int m = 0; m < 8; ++m) stage[lane * kStagePitch + 8 * k + m] = e[m];
             }
+            __syncwarp();
+            // half a warp to a row
+            const int col = n0 + j + (lane & 15);
+            int left = P.cols - (c - lane + (lane >> 4));   // rows from this one on
+            if (col >= P.n) left = 0;
+            float* d = P.dw + (int64_t)(c - lane + (lane >> 4)) * P.lddw + col;
+            const float* s = stage + (lane >> 4) * kStagePitch + (lane & 15);
+#pragma unroll 1
+            for (int k0 = 0; k0 < 4; ++k0) {
+              float old[4] = {};
+              if (P.accumulate) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  if (2 * k < left) old[k] = d[2 * k * P.lddw];
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (2 * k < left) d[2 * k * P.lddw] = old[k] + s[2 * k * kStagePitch];
+              d += 8 * P.lddw;
+              s += 8 * kStagePitch;
+              left -= 8;
+            }
+            __syncwarp();
           }
         }
         tc_fence_before();
@@ -490,26 +538,72 @@ __global__ void __launch_bounds__(256) ts_wgrad_finish_kernel(const __grid_const
   const int tile = P.full + blockIdx.x / 32, b = blockIdx.x % 32;   // 32 blocks a tile: 8 columns of all 256 rows each
   const int h = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
   const int c = tile / P.tiles_n * kTile + threadIdx.x, j = tile % P.tiles_n * kTile + b * 8;
-  if (c >= P.cols || j >= P.n) return;
+  const bool in = c < P.cols && j < P.n;
   float v[8] = {};
-  for (int p = 0; p < P.pieces; ++p) {
+  for (int p = 0; in && p < P.pieces; ++p) {
     const float4* o =
         P.part + (int64_t)((blockIdx.x / 32 * P.pieces + p) * 2 + h) * (kPieceFloats / 8) + b * 2 * kHalf + r;
     const float4 x = __ldcg(o), y = __ldcg(o + kHalf);
     v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
   }
-  finish8(P, P.dw + (int64_t)c * P.lddw, j, P.gamma ? P.gamma[c] : 1.f, P.beta ? P.beta[c] : 0.f, store_width(P), v);
+  const float g = in && P.gamma ? P.gamma[c] : 1.f, be = in && P.beta ? P.beta[c] : 0.f;
+  const int vec = store_width(P);
+  if (vec > 1) {
+    if (in) finish8(P, P.dw + (int64_t)c * P.lddw, j, g, be, vec, v);
+    return;
+  }
+  // rows off 16 bytes: eight threads to a row's columns
+  __shared__ float sm[kTile][9];
+  if (in) affine8(P, j, g, be, v);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = v[k];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int at = i * (kTile / 8) + threadIdx.x / 8, k = threadIdx.x % 8, row = c - threadIdx.x + at;
+    if (row < P.cols && j + k < P.n) {
+      float* d = P.dw + (int64_t)row * P.lddw + j + k;
+      *d = P.accumulate ? *d + sm[at][k] : sm[at][k];
+    }
+  }
 }
 
-// dy's rows at an aligned pitch.
+// dy's rows at an aligned pitch.  A thread makes eight elements, out of the two
+// aligned pieces of 16 bytes that hold them, or by single ones where a piece
+// would reach past the row's ends.  (By single elements throughout, 8192 x
+// 4096 x 4096 took 348 us, 142 more than without the copy.)
 __global__ void __launch_bounds__(256) ts_repack_kernel(const __nv_bfloat16* src, int64_t ld, int64_t rows, int n,
                                                         __nv_bfloat16* dst, int64_t pitch) {
   pdl_launch_dependents();
   pdl_wait();
-  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y)
-    for (int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x; j < n; j += (int64_t)gridDim.x * 256)
-      dst[r * pitch + j] = src[r * ld + j];
+  const int per_row = (int)(pitch / 8);
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, r = i / per_row;
+  if (r >= rows) return;
+  const int j = (int)(i - r * per_row) * 8;
+  const __nv_bfloat16* s = src + r * ld + j;
+  __nv_bfloat16* d = dst + r * pitch + j;
+  const int off = (int)(reinterpret_cast<uintptr_t>(s) % 16 / 2);   // the same for all of a row
+  if (j < off || j - off + 16 > n) {
+    for (int k = 0; k < 8 && j + k < n; ++k) d[k] = s[k];
+    return;
+  }
+  const uint4 a = __ldcs(reinterpret_cast<const uint4*>(s - off)), b = __ldcs(reinterpret_cast<const uint4*>(s - off) + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  // the elements before the first one drop out: four, two and one of them
+  if (off & 4) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  }
+  if (off & 2) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  }
+  if (off & 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+  }
+  *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // dW of no tokens: beta's part is 0 too.
@@ -542,16 +636,18 @@ cudaError_t resident_pairs(int device, int* out) {
   static std::atomic<int> cached[64];
   int n = device < 64 ? cached[device].load(std::memory_order_acquire) : 0;
   if (!n) {
-    cudaError_t e = cudaFuncSetAttribute(ts_wgrad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(ts_wgrad_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<true>);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = pdl_config(2, kThreads, kSmem, nullptr);
+    e = cudaFuncSetAttribute(ts_wgrad_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<false>);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = pdl_config(2, kThreads, kSmem<false>, nullptr);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = 2;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&n, ts_wgrad_kernel, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, ts_wgrad_kernel<false>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorLaunchOutOfResources;
     if (device < 64) cached[device].store(n, std::memory_order_release);
@@ -591,10 +687,11 @@ cudaError_t product(const ts_ops& h, WgradKernel& P, const TsCkpt& x, const TsMa
   P.items = P.full + P.pieces * rem;
   P.chain = reinterpret_cast<float4*>(ws);
   P.part = P.chain + (nkb > kChain ? pairs : 0) * (kPieceFloats / 4);
-  cudaLaunchConfig_t cfg = pdl_config(2 * std::min(pairs, P.items), kThreads, kSmem, st);
+  const bool wide = store_width(P) > 1;
+  cudaLaunchConfig_t cfg = pdl_config(2 * std::min(pairs, P.items), kThreads, wide ? kSmem<true> : kSmem<false>, st);
   cudaLaunchAttribute at[1];
   pdl_attr(cfg, at);
-  e = cudaLaunchKernelEx(&cfg, ts_wgrad_kernel, P);
+  e = cudaLaunchKernelEx(&cfg, wide ? ts_wgrad_kernel<true> : ts_wgrad_kernel<false>, P);
   if (e != cudaSuccess || P.pieces == 1) return e;
   cudaLaunchConfig_t fin = pdl_config(rem * 32, 256, 0, st);
   pdl_attr(fin, at);
@@ -610,7 +707,8 @@ cudaError_t launch_weight_grad(const ts_ops& h, const WgradArgs& a, cudaStream_t
   const int64_t keep = a.beta ? ((int64_t)a.n * 4 + 255) / 256 * 256 : 0;
   int64_t room = h.ws_bytes - keep;
   float* colsum = keep ? reinterpret_cast<float*>(h.ws + room) : nullptr;
-  if (colsum || a.db) {
+  const bool aligned = rows_aligned(a.dy);
+  if ((colsum || a.db) && (aligned || a.rows == 0)) {
     e = launch_column_sums(h, a.dy, a.rows, a.n, colsum, a.db, a.accumulate, st);
     if (e != cudaSuccess) return e;
   }
@@ -631,31 +729,36 @@ cudaError_t launch_weight_grad(const ts_ops& h, const WgradArgs& a, cudaStream_t
   P.lddw = a.lddw;
   P.accumulate = a.accumulate;
   P.err = h.err;
-  if (rows_aligned(a.dy)) return product(h, P, a.x, a.dy, a.rows, h.ws, room, st);
-  // an aligned copy of dy in at most half of the workspace, the partials in
-  // the rest
+  if (aligned) return product(h, P, a.x, a.dy, a.rows, h.ws, room, st);
+  // an aligned copy of as many tokens of dy as leave the column sums' room and
+  // about half of the workspace; a call's whole work for each copy
   TsMat dy;
   dy.p = h.ws;
   dy.bf16 = 1;
   dy.ld = (a.n + 7) / 8 * 8;
-  const int64_t most = std::max<int64_t>(1, room / 2 / (dy.ld * 2));
-  for (int64_t t = 0; t < a.rows; t += most) {
-    const int64_t rows = std::min(most, a.rows - t);
-    cudaLaunchConfig_t cfg = pdl_config(1, 256, 0, st);
-    cfg.gridDim = dim3((a.n + 1023) / 1024, (unsigned)std::min<int64_t>(rows, 1024));
+  const int64_t most = std::max<int64_t>(1, (h.ws_bytes - 16 * (int64_t)a.n) / 16 * 9 / (dy.ld * 2));
+  const int64_t times = (a.rows + most - 1) / most, each = (a.rows + times - 1) / times;
+  for (int64_t t = 0; t < a.rows; t += each) {
+    const int64_t rows = std::min(each, a.rows - t);
+    cudaLaunchConfig_t cfg = pdl_config((int)((rows * (dy.ld / 8) + 255) / 256), 256, 0, st);
     pdl_attr(cfg, at);
-    e = cudaLaunchKernelEx(&cfg, ts_repack_kernel,
-                           static_cast<const __nv_bfloat16*>(a.dy.p) + t * a.dy.ld, a.dy.ld, rows, a.n,
-                           reinterpret_cast<__nv_bfloat16*>(h.ws), dy.ld);
+    e = cudaLaunchKernelEx(&cfg, ts_repack_kernel, static_cast<const __nv_bfloat16*>(a.dy.p) + t * a.dy.ld, a.dy.ld,
+                           rows, a.n, reinterpret_cast<__nv_bfloat16*>(h.ws), dy.ld);
     if (e != cudaSuccess) return e;
+    const int64_t used = (rows * dy.ld * 2 + 255) / 256 * 256;
+    if (colsum || a.db) {
+      ts_ops rest = h;
+      rest.ws += used;
+      rest.ws_bytes -= used;
+      e = launch_column_sums(rest, dy, rows, a.n, colsum, a.db, P.accumulate, st);
+      if (e != cudaSuccess) return e;
+    }
     TsCkpt x = a.x;
     x.q += t * x.pitch;
     x.scale += t * (x.pitch / kCkptBlock);
-    const int64_t used = (rows * dy.ld * 2 + 255) / 256 * 256;
     e = product(h, P, x, dy, rows, h.ws + used, room - used, st);
     if (e != cudaSuccess) return e;
     P.accumulate = 1;   // the later tokens add to the first ones'
-    P.beta = nullptr;
   }
   return cudaSuccess;
 }

@@ -162,6 +162,15 @@ def test_layer_norm_backward(ops, rows, cols, xt, dt, pad, from_ckpt):
     assert torch.equal(dx, dx2) and torch.equal(dg2, dg + dg) and torch.equal(db2, db + db)
 
 
+# long rows, several to an SM
+@pytest.mark.parametrize("from_ckpt", [False, True])
+@pytest.mark.parametrize("pad", [0, 8, 3])
+@pytest.mark.parametrize("xt, dt", TYPES)
+@pytest.mark.parametrize("rows, cols", [(400, 8200), (170, 16384)])
+def test_layer_norm_backward_of_long_rows(ops, rows, cols, xt, dt, pad, from_ckpt):
+    test_layer_norm_backward(ops, rows, cols, xt, dt, pad, from_ckpt)
+
+
 def test_layer_norm_gradient_by_differences(ops):
     # the forward kernel's directional difference against the backward
     # kernel's gradient: float32 outputs differ by 2^-22 or so, over a step of
@@ -320,6 +329,32 @@ def test_weight_grad(ops, rows, cols, n, pad, affine):
     ops.sync()
     gap_kept(dw2, pad)
     assert torch.equal(dw2, dw + dw) and torch.equal(db2, db + db)
+
+
+# rows of dy off 16 bytes go through a copy in the workspace, here by a few
+# hundred and by single tokens at a time; dw in the caller's buffer, with a gap
+@pytest.mark.parametrize("rows, cols, n", [(1500, 96, 601), (9, 40, 65535)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_grad_of_unaligned_rows_in_a_small_workspace(rows, cols, n, accumulate):
+    ops = TrainingOps(1 << 20)
+    b = OT.checkpoint_encode(normal(rows, rows, cols))
+    h = OT.checkpoint_decode(b, rows, cols)
+    dy = rounded(normal(rows + 1, rows, n) * 0.1, BF16)
+    gamma, beta = normal(1, cols) * 0.1 + 1, normal(2, cols) * 0.1
+    ref, rb = OT.weight_grad(h, dy, gamma, beta)
+    old, oldb = normal(3, cols, n), normal(4, n)
+    dw, db = empty((cols, n), F32, 3), vec(oldb)
+    dw.copy_(vec(old))
+    ops.weight_grad(Checkpoint(rows, cols, torch.from_numpy(b).cuda()), dev(dy, BF16, 2), dw, db=db, gamma=vec(gamma),
+                    beta=vec(beta), accumulate=accumulate)
+    ops.sync()
+    gap_kept(dw, 3)
+    base, baseb = (rounded(old, F32), rounded(oldb, F32)) if accumulate else (0.0 * old, 0.0 * oldb)
+    # every addition is off by 2^-23 of its partial sum at most: rows + 8, and
+    # one to each piece for what is added to
+    size = np.abs(h * gamma).T @ np.abs(dy) + np.abs(beta)[:, None] * np.abs(dy).sum(0)
+    within(dw, base + ref, 2.0 ** -23 * (2 * rows + 8) * (size + np.abs(base)) + 1e-30)
+    within(db, baseb + rb, 2.0 ** -23 * (2 * rows + 64) * (np.abs(dy).sum(0) + np.abs(baseb)) + 1e-30)
 
 
 def test_weight_grad_of_no_rows_and_marked_blocks(ops):
