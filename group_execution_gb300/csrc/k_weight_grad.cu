@@ -154,26 +154,22 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// Eight values of one row of dw from column j, scaled and shifted as asked.
-__device__ __forceinline__ void affine8(const WgradKernel& P, int j, float g, float b, float (&v)[8]) {
+// Eight values of one row of dw, scaled and, with beta, shifted by dy's column
+// sums s.
+__device__ __forceinline__ void affine8(const WgradKernel& P, const float* s, float g, float b, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] *= g;
   if (P.beta) {
-    float s[8];
-    if (j + 8 <= P.n) {   // (16-byte aligned: j is a multiple of 8)
-      load8(P.colsum + j, s);
-    } else {
+    float c[8];
+    load8(s, c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = j + i < P.n ? P.colsum[j + i] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += b * s[i];
+    for (int i = 0; i < 8; ++i) v[i] += b * c[i];
   }
 }
 // Stores them (vec: 8 or 4 floats at a time), accumulated as asked.
-__device__ __forceinline__ void finish8(const WgradKernel& P, float* row, int j, float g, float b, int vec,
-                                        float (&v)[8]) {
-  affine8(P, j, g, b, v);
+__device__ __forceinline__ void finish8(const WgradKernel& P, const float* s, float* row, int j, float g, float b,
+                                        int vec, float (&v)[8]) {
+  affine8(P, s, g, b, v);
   float* d = row + j;
   if (vec == 8 && j + 8 <= P.n) {
     if (P.accumulate) {
@@ -214,6 +210,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 5];
   __shared__ int abort_flag, issued;
   __shared__ uint32_t tmem_slot;
+  __shared__ __align__(16) float colsums[8][kTile / 2];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
                  tempty0 = tfull0 + 16, done_bar = tempty0 + 16;
@@ -342,6 +339,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int c = w.tile / P.tiles_n * kTile + h * kHalf + r, n0 = w.tile % P.tiles_n * kTile;
       const float g = P.gamma && c < P.cols ? P.gamma[c] : 1.f, be = P.beta && c < P.cols ? P.beta[c] : 0.f;
       float* row = P.dw + (int64_t)c * P.lddw;
+      if (P.beta) {
+        // dy's column sums of this warp's columns, fetched during the products
+        // (chunk by chunk in the epilogue they took 13 x 3720 x 1880 from 14
+        // to 19 us)
+#pragma unroll
+        for (int k = 0; k < kTile / 2; k += 32) {
+          const int at = n0 + (warp >= 8 ? kTile / 2 : 0) + k + lane;
+          colsums[warp - 4][k + lane] = at < P.n ? P.colsum[at] : 0.f;
+        }
+        __syncwarp();
+      }
       float4* piece = w.piece < 0 ? nullptr : P.part + (int64_t)(w.piece * 2 + h) * (kPieceFloats / 8) + r;
       for (int s0 = w.kb0; s0 < w.kb1; ++i) {
         const int s1 = segment_end(w, s0), b = i & 1;
@@ -385,7 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float e[8];
 #pragma unroll
                 for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
-                finish8(P, row, n0 + j + 8 * k, g, be, vec, e);
+                finish8(P, &colsums[warp - 4][j % (kTile / 2) + 8 * k], row, n0 + j + 8 * k, g, be, vec, e);
               }
             }
           } else {
@@ -397,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               float e[8];
 #pragma unroll
               for (int m = 0; m < 8; ++m) e[m] = v[8 * k + m];
-              affine8(P, n0 + j + 8 * k, g, be, e);
+              affine8(P, &colsums[warp - 4][j % (kTile / 2) + 8 * k], g, be, e);
 #pragma unroll
               for (int m = 0; m < 8; ++m) stage[lane * kStagePitch + 8 * k + m] = e[m];
             }
@@ -548,14 +556,17 @@ __global__ void __launch_bounds__(256) ts_wgrad_finish_kernel(const __grid_const
     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
   }
   const float g = in && P.gamma ? P.gamma[c] : 1.f, be = in && P.beta ? P.beta[c] : 0.f;
+  __shared__ __align__(16) float colsum[8];
+  if (P.beta && threadIdx.x < 8) colsum[threadIdx.x] = j + (int)threadIdx.x < P.n ? P.colsum[j + threadIdx.x] : 0.f;
+  __syncthreads();
   const int vec = store_width(P);
   if (vec > 1) {
-    if (in) finish8(P, P.dw + (int64_t)c * P.lddw, j, g, be, vec, v);
+    if (in) finish8(P, colsum, P.dw + (int64_t)c * P.lddw, j, g, be, vec, v);
     return;
   }
   // rows off 16 bytes: eight threads to a row's columns
   __shared__ float sm[kTile][9];
-  if (in) affine8(P, j, g, be, v);
+  if (in) affine8(P, colsum, g, be, v);
 #pragma unroll
   for (int k = 0; k < 8; ++k) sm[threadIdx.x][k] = v[k];
   __syncthreads();
