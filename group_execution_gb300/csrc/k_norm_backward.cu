@@ -147,9 +147,10 @@ __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
 // Partial column sums: block (bx, by) takes 256 columns and every gridDim.y-th
 // run of 8 rows, a warp a row, four runs in flight; the block's warps are
 // added in order.  part: [gridDim.y][2][cols], dy's sums and then, with a
-// Src, dy h's.
+// Src, dy h's; null with one block to a column, which then finishes it (fresh
+// as below).
 template <class TDY, class Src, bool VEC>
-__global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float* part) {
+__global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float* part, float* fresh) {
   __shared__ float sm[8][2][kGroupCols];
   pdl_launch_dependents();
   pdl_wait();
@@ -194,6 +195,12 @@ __global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float*
     for (int w = 0; w < 8; ++w) {
       b += sm[w][0][threadIdx.x];
       if (kH) g += sm[w][1][threadIdx.x];
+    }
+    if (!part) {
+      if (fresh) fresh[c] = b;
+      if (a.dbeta) a.dbeta[c] = a.accumulate ? a.dbeta[c] + b : b;
+      if (kH && a.dgamma) a.dgamma[c] = a.accumulate ? a.dgamma[c] + g : g;
+      return;
     }
     part[((int64_t)blockIdx.y * 2 + 0) * a.cols + c] = b;
     if (kH) part[((int64_t)blockIdx.y * 2 + 1) * a.cols + c] = g;
@@ -561,7 +568,9 @@ cudaError_t finish_columns(const float* part, int parts, int cols, float* dbeta,
 }
 
 // Row splits of a column sum: enough blocks for the device, 64 rows a block
-// at least, partials that fit the workspace (less its last 8 bytes a column,
+// at least (one block spares the second kernel: the bias gradient beside a
+// weight gradient of 3 x 511 x 264 takes 1.0 us more in place of 2.0; at 120
+// rows the longer block takes what it spares), partials that fit the workspace (less its last 8 bytes a column,
 // kept for a call's own sums).
 int column_parts(const ts_ops& h, int64_t rows, int cols) {
   const int64_t tiles = (cols + kGroupCols - 1) / kGroupCols;
@@ -578,9 +587,9 @@ cudaError_t columns(const ts_ops& h, const NormArgs& a, float* fresh, cudaStream
   cfg.gridDim = dim3((a.cols + kGroupCols - 1) / kGroupCols, parts);
   cudaLaunchAttribute at[1];
   pdl_attr(cfg, at);
-  float* part = reinterpret_cast<float*>(h.ws);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, ts_column_kernel<TDY, Src, VEC>, a, part);
-  if (e != cudaSuccess) return e;
+  float* part = parts > 1 ? reinterpret_cast<float*>(h.ws) : nullptr;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, ts_column_kernel<TDY, Src, VEC>, a, part, fresh);
+  if (e != cudaSuccess || !part) return e;
   return finish_columns(part, parts, a.cols, a.dbeta, a.dgamma, a.accumulate, fresh, st);
 }
 
