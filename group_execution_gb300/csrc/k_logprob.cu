@@ -550,8 +550,8 @@ struct RowGrad {
 // are one lane's each, what is left at its ends single lanes'.  A warp takes
 // kLpGroups consecutive groups of 32 chunks of a row, loaded together.
 //
-// One pass, bound by memory: 2048 x 65536 f32 takes 160 us with the entropy's
-// gradient (99 % of the copy rate; 167 with one group a warp), 4096 x 50001
+// One pass, bound by memory: 2048 x 65536 f32 takes 155 us with the entropy's
+// gradient (the copy's rate; by single groups a warp, and 16 bytes a store, 167), 4096 x 50001
 // bf16 at odd elements 150 us (80 %, by single elements 315).
 constexpr int kLpGroups = 2;
 

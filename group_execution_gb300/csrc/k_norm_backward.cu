@@ -244,8 +244,8 @@ __device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
 // Bound by instruction issue before memory in bf16 (eight columns a lane and
 // row: two loads, one store and about 100 other instructions), so pairs of
 // float32 operations go in one instruction and addresses advance by addition.
-// 8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 66 in f32 (90 %); G
-// = 2 at 4096 x 8192 bf16 takes 48.  (A partial written by single elements,
+// 8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 64 in f32 (92 %); G
+// = 2 at 4096 x 8192 bf16 takes 48 and f32 72 (84 with the choice of stores).  (A partial written by single elements,
 // 32 bytes apart across a warp, cost 3 to 7 us.)  1021 x 5003 f32 from the
 // checkpoint, whose rows start at odd elements and come by single ones, takes
 // 24 us (29 %).  About 4 us of each is the kernel that adds the partials.
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             unpack2f(fma2(h[k][g][j], a2, fma2(u[k][g][j], rr, a1)), o[2 * j], o[2 * j + 1]);
-          store_group<VEC>(dx, (g * W + warp) * kGroupCols, a.cols, lane, o);
+          store_group<VEC, G == 2>(dx, (g * W + warp) * kGroupCols, a.cols, lane, o);
         }
         dx += dx_step;
       }
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
 // column sums live in shared memory (192 KB), where a thread meets its own
 // columns alone, four at a time; the registers hold the row, and the next one
 // is on its way to L2.  2048 x 16384 bf16 takes 50 us (59 % of the copy rate;
-// by the two kernels that longer rows take, 99), 2388 x 10336 f32 78 (129).  Up
+// by the two kernels that longer rows take, 99), 2388 x 10336 f32 68 (129).  Up
 // to 8192 columns, where column sums fit the registers above, those are
 // faster: 4096 x 8192 bf16 48 us, here 82.
 constexpr int kWideGroups = 2, kWidePlane = kWideGroups * 2 * 1024;   // float4s of one value a column
