@@ -22,8 +22,10 @@ namespace {
 // Each takes N consecutive pieces and loads all of them before it works on
 // the first (one division to find its place).  us with N = 1, 2, 4: saving
 // 8192 x 4096 in bf16 27, 22, 24; loading it to bf16 20, -, 16; the tanh
-// derivative at 4097 x 4100 in bf16 18, -, 15, and with rows at odd elements
-// 22, 29, 51 (N scalar loads of 16 and 8 bits a value are too many registers).
+// derivative at 4097 x 4100 in bf16 18, -, 15.  With rows at odd elements, which
+// move by single ones, N = 1 is fastest (more are too many registers): at 8192 x
+// 4096 in bf16 saving takes 31 us, loading 28, the tanh derivative 35 (26
+// aligned).
 struct Pieces {
   int64_t rows;
   int cols, per_row;
@@ -70,13 +72,14 @@ __global__ void __launch_bounds__(256) ts_save_kernel(const TsMat x, const Piece
   pdl_wait();
   const int lane = threadIdx.x & (VEC ? 15 : 31);
   RawGroup<TX, VEC> raw[kSaveAtOnce<VEC>];
+  __shared__ __align__(16) float scratch[VEC ? 1 : 8][kGroupCols];
   for_pieces<VEC, kSaveAtOnce<VEC>>(
       g,
       [&](int u, int64_t r, int c0) { raw[u].load(static_cast<const TX*>(x.p) + r * x.ld, c0, g.cols, lane); },
       [&](int u, int64_t r, int c0) {
         float v[8];
         raw[u].get(v);
-        ckpt_store_group<VEC>(c, r, c0, lane, v);
+        ckpt_store_group<VEC>(c, r, c0, lane, v, scratch[VEC ? 0 : threadIdx.x >> 5]);
       });
 }
 
@@ -86,11 +89,12 @@ __global__ void __launch_bounds__(256) ts_load_kernel(const TsCkpt c, const Piec
   pdl_wait();
   const int lane = threadIdx.x & (VEC ? 15 : 31);
   RawCkpt<VEC> raw[kAtOnce<VEC>];
+  __shared__ __align__(8) CkptScratch<!VEC, 8> scratch;
   for_pieces<VEC, kAtOnce<VEC>>(
       g, [&](int u, int64_t r, int c0) { raw[u].load(c, r, c0, lane); },
       [&](int u, int64_t r, int c0) {
         float v[8];
-        raw[u].get(v);
+        raw[u].get(v, lane, scratch.mine());
         store_group<VEC>(static_cast<TY*>(y.p) + r * y.ld, c0, g.cols, lane, v);
       });
 }
@@ -110,6 +114,7 @@ __global__ void __launch_bounds__(256) ts_act_kernel(const TsMat dy, const TsCkp
   const int lane = threadIdx.x & (VEC ? 15 : 31);
   RawGroup<TDY, VEC> d[kAtOnce<VEC>];
   RawCkpt<VEC> raw[kAtOnce<VEC>];
+  __shared__ __align__(8) CkptScratch<!VEC, 8> scratch;
   for_pieces<VEC, kAtOnce<VEC>>(
       g,
       [&](int u, int64_t r, int c0) {
@@ -119,7 +124,7 @@ __global__ void __launch_bounds__(256) ts_act_kernel(const TsMat dy, const TsCkp
       [&](int u, int64_t r, int c0) {
         float v[8], a[8];
         d[u].get(v);
-        raw[u].get(a);
+        raw[u].get(a, lane, scratch.mine());
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] *= act_slope<ACT>(a[j]);
         store_group<VEC>(static_cast<TDX*>(dx.p) + r * dx.ld, c0, g.cols, lane, v);

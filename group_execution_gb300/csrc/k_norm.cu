@@ -41,6 +41,7 @@ template <class TX, class TY, bool VEC, int NW, int NC>
 __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8 ? 4 : NC == 2 ? 2 : 1) ts_norm_kernel(const NormArgs a) {
   constexpr int kRows = NW == 1 ? 4 : 1;   // rows a block works on at a time
   __shared__ float red[2][NW];
+  __shared__ __align__(16) float scratch[VEC ? 1 : kRows * NW][kGroupCols];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = NW == 1 ? 0 : threadIdx.x >> 5;
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8
       float h[8], g[8], b[8];
 #pragma unroll
       for (int j = 0; j < 4; ++j) unpack2f(mul2(v[i][j], scale), h[2 * j], h[2 * j + 1]);
-      if (a.ckpt.q) ckpt_store_group<VEC>(a.ckpt, row, c0, lane, h);
+      if (a.ckpt.q) ckpt_store_group<VEC>(a.ckpt, row, c0, lane, h, scratch[VEC ? 0 : threadIdx.x >> 5]);
       if (a.gamma) {
         load_group<VEC>(a.gamma, c0, a.cols, lane, g);
 #pragma unroll
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8
 template <class TX, class TY, bool VEC>
 __global__ void __launch_bounds__(1024) ts_norm_long_kernel(const NormArgs a) {
   __shared__ float red[2][32];
+  __shared__ __align__(16) float scratch[VEC ? 1 : 32][kGroupCols];
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -163,7 +165,7 @@ __global__ void __launch_bounds__(1024) ts_norm_long_kernel(const NormArgs a) {
     load_group<VEC>(x, c0, a.cols, lane, v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = c0 + group_col<VEC>(lane, j) < a.cols ? (v[j] - mean) * rstd : 0.f;
-    if (a.ckpt.q) ckpt_store_group<VEC>(a.ckpt, row, c0, lane, v);
+    if (a.ckpt.q) ckpt_store_group<VEC>(a.ckpt, row, c0, lane, v, scratch[VEC ? 0 : threadIdx.x >> 5]);
     if (a.gamma) {
       load_group<VEC>(a.gamma, c0, a.cols, lane, g);
 #pragma unroll

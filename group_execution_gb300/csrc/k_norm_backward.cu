@@ -38,7 +38,7 @@ struct FromX {
     __device__ __forceinline__ void load(const NormArgs& a, const FromX& s, int c0, int lane) {
       x.load(s.row, c0, a.cols, lane);
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const { x.get(v); }   // x itself
+    __device__ __forceinline__ void get(float (&v)[8], int, int8_t*) const { x.get(v); }   // x itself
   };
   __device__ __forceinline__ static float mean(const NormArgs& a, int64_t row) { return a.mean[row]; }
   __device__ __forceinline__ static void prefetch(const NormArgs& a, int64_t row) {
@@ -62,7 +62,7 @@ struct FromCkpt {
     __device__ __forceinline__ void load(const NormArgs&, const FromCkpt& s, int c0, int lane) {
       c.load(s.row, 0, c0, lane);
     }
-    __device__ __forceinline__ void get(float (&v)[8]) const { c.get(v); }   // h
+    __device__ __forceinline__ void get(float (&v)[8], int lane, int8_t* scratch) const { c.get(v, lane, scratch); }   // h
   };
   __device__ __forceinline__ static float mean(const NormArgs&, int64_t) { return 0.f; }
   __device__ __forceinline__ static void prefetch(const NormArgs& a, int64_t row) {
@@ -72,10 +72,10 @@ struct FromCkpt {
 };
 template <class Src, bool VEC>
 __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, int lane, float mean, float rstd,
-                                       float (&h)[8]) {
+                                       float (&h)[8], int8_t* scratch) {
   typename Src::template Raw<VEC> r;
   r.load(a, Src(a, row), c0, lane);
-  r.get(h);
+  r.get(h, lane, scratch);
   if (!Src::kCkpt) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = (h[j] - mean) * rstd;
@@ -88,6 +88,7 @@ __device__ __forceinline__ void load_h(const NormArgs& a, int64_t row, int c0, i
 template <class TDY, class Src, bool VEC>
 __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
   __shared__ float red[2][8];
+  __shared__ __align__(8) CkptScratch<Src::kCkpt && !VEC, 8> scratch;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
     const int c0 = (int)cc;
     float u[8], h[8], g[8];
     load_group<VEC>(dy, c0, a.cols, lane, u);
-    load_h<Src, VEC>(a, row, c0, lane, mean, rstd, h);
+    load_h<Src, VEC>(a, row, c0, lane, mean, rstd, h, scratch.mine());
     if (a.gamma) {
       load_group<VEC>(a.gamma, c0, a.cols, lane, g);
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
     const int c0 = (int)cc;
     float u[8], h[8], g[8];
     load_group<VEC>(dy, c0, a.cols, lane, u);
-    load_h<Src, VEC>(a, row, c0, lane, mean, rstd, h);
+    load_h<Src, VEC>(a, row, c0, lane, mean, rstd, h, scratch.mine());
     if (a.gamma) {
       load_group<VEC>(a.gamma, c0, a.cols, lane, g);
 #pragma unroll
@@ -152,9 +153,10 @@ __global__ void __launch_bounds__(256) ts_norm_dx_kernel(const NormArgs a) {
 template <class TDY, class Src, bool VEC>
 __global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float* part, float* fresh) {
   __shared__ float sm[8][2][kGroupCols];
+  constexpr bool kH = !std::is_void<Src>::value;
+  __shared__ __align__(8) CkptScratch<kH && !VEC, 8> scratch;
   pdl_launch_dependents();
   pdl_wait();
-  constexpr bool kH = !std::is_void<Src>::value;
   constexpr int kU = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c0 = blockIdx.x * kGroupCols;
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(256) ts_column_kernel(const NormArgs a, float*
       for (int j = 0; j < 8; ++j) sb[j] += v[j];
       if constexpr (kH) {
         float h[8];
-        load_h<Src, VEC>(a, rr, c0, lane, Src::mean(a, rr), a.rstd[rr], h);
+        load_h<Src, VEC>(a, rr, c0, lane, Src::mean(a, rr), a.rstd[rr], h, scratch.mine());
 #pragma unroll
         for (int j = 0; j < 8; ++j) sg[j] += v[j] * h[j];
       }
@@ -247,11 +249,12 @@ __device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
 // 8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 64 in f32 (92 %); G
 // = 2 at 4096 x 8192 bf16 takes 48 and f32 72 (84 with the choice of stores).  (A partial written by single elements,
 // 32 bytes apart across a warp, cost 3 to 7 us.)  1021 x 5003 f32 from the
-// checkpoint, whose rows start at odd elements and come by single ones, takes
-// 24 us (29 %).  About 4 us of each is the kernel that adds the partials.
+// checkpoint, whose rows of dy and dx start at odd elements and move by single
+// ones, takes 21 us (33 %).  About 4 us of each is the kernel that adds the partials.
 template <class TDY, class Src, bool VEC, int G, int D, int K>
 __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs a, int W, float* part) {
   __shared__ float red[2][16][4];   // [warp][value]
+  __shared__ __align__(8) CkptScratch<Src::kCkpt && !VEC, 16> scratch;
   __shared__ float sums[G == 1 ? 2 * 16 * kGroupCols : 1];   // the slots' column sums (G = 1, W < 16)
   pdl_launch_dependents();
   pdl_wait();
@@ -315,7 +318,7 @@ __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs
           for (int g = 0; g < G; ++g) {
             float du[8], dh[8];
             dy[d][k][g].get(du);
-            x[d][k][g].get(dh);
+            x[d][k][g].get(dh, lane, scratch.mine());
             if (G > 1) load_gamma(g);   // (from L1)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -429,6 +432,7 @@ template <class TDY, class Src, bool VEC>
 __global__ void __launch_bounds__(1024, 1) ts_norm_backward_wide_kernel(const NormArgs a, float* part) {
   extern __shared__ float4 wide[];
   __shared__ float red[2][2][32];   // [value][warp]
+  __shared__ __align__(8) CkptScratch<Src::kCkpt && !VEC, 32> scratch;
   pdl_launch_dependents();
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(1024, 1) ts_norm_backward_wide_kernel(const No
     for (int g = 0; g < kWideGroups; ++g) {
       float du[8], dh[8];
       dy[g].get(du);
-      x[g].get(dh);
+      x[g].get(dh, lane, scratch.mine());
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int at = (g * 2 + i) * 1024;

@@ -211,110 +211,84 @@ __device__ __forceinline__ int ckpt_quantise(float v, float inv) {
 }
 
 // Writes this warp's group (columns from c0, those at or past cols as zeros,
-// up to the pitch) of checkpoint row `r`.
+// up to the pitch) of checkpoint row `r`.  Without VEC the warp's values
+// change places in `scratch`, 256 floats of its own, first: a lane then has
+// eight columns that lie together, as with VEC (a byte at a time, and a block's
+// maximum over the whole warp, saving 8192 x 4096 bf16 at odd elements took 43 us
+// in place of 31).
 template <bool VEC>
-__device__ __forceinline__ void ckpt_store_group(const TsCkpt& c, int64_t r, int c0, int lane, const float (&v)[8]) {
-  int8_t* q = c.q + r * c.pitch;
-  uint8_t* s = c.scale + r * (c.pitch / kCkptBlock);
+__device__ __forceinline__ void ckpt_store_group(const TsCkpt& c, int64_t r, int c0, int lane, const float (&v)[8],
+                                                 float* scratch) {
+  float x[8];
   if (VEC) {
-    uint32_t m = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-    const unsigned quad = 0xfu << (threadIdx.x & 28);   // (half warps may be in different rows)
-    m = max(m, __shfl_xor_sync(quad, m, 1));
-    m = max(m, __shfl_xor_sync(quad, m, 2));
-    const int e = max((int)(m >> 23), 7);
-    const float inv = ckpt_inv_step(e);
-    uint32_t w[2] = {0, 0};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(ckpt_quantise(v[j], inv) & 0xff) << (8 * (j & 3));
-    const int col = c0 + lane * 8;
-    if (col < c.pitch) {
-      *reinterpret_cast<uint2*>(q + col) = make_uint2(w[0], w[1]);
-      if ((lane & 3) == 0) s[col / kCkptBlock] = (uint8_t)e;
-    }
+    for (int j = 0; j < 8; ++j) x[j] = v[j];
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(v[j]) & 0x7fffffffu);
-      const int e = max((int)(m >> 23), 7);
-      const int col = c0 + j * 32 + lane;
-      if (col < c.pitch) {
-        q[col] = (int8_t)ckpt_quantise(v[j], ckpt_inv_step(e));
-        if (lane == 0) s[col / kCkptBlock] = (uint8_t)e;
-      }
-    }
+    for (int j = 0; j < 8; ++j) scratch[j * 32 + lane] = v[j];
+    __syncwarp();
+    load8(scratch + lane * 8, x);
+    __syncwarp();
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+  const unsigned quad = 0xfu << (threadIdx.x & 28);   // (half warps may be in different rows)
+  m = max(m, __shfl_xor_sync(quad, m, 1));
+  m = max(m, __shfl_xor_sync(quad, m, 2));
+  const int e = max((int)(m >> 23), 7);
+  const float inv = ckpt_inv_step(e);
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j >> 2] |= (uint32_t)(ckpt_quantise(x[j], inv) & 0xff) << (8 * (j & 3));
+  const int col = c0 + lane * 8;
+  if (col < c.pitch) {
+    *reinterpret_cast<uint2*>(c.q + r * c.pitch + col) = make_uint2(w[0], w[1]);
+    if ((lane & 3) == 0) c.scale[r * (c.pitch / kCkptBlock) + col / kCkptBlock] = (uint8_t)e;
   }
 }
 
-// The values of this warp's group of checkpoint row `r`; 0 past the pitch.
+// A group of a checkpoint row, fetched some time before it is used: eight
+// columns that lie together to a lane.  Without VEC its bytes change places in
+// `scratch`, 256 bytes of the warp's own, when they are used (loaded one by
+// one, 8192 x 4096 from a checkpoint to bf16 rows at odd elements took 32 us in
+// place of 28).
 template <bool VEC>
-__device__ __forceinline__ void ckpt_load_group(const TsCkpt& c, int64_t r, int c0, int lane, float (&v)[8]) {
-  const int8_t* q = c.q + r * c.pitch;
-  const uint8_t* s = c.scale + r * (c.pitch / kCkptBlock);
-  if (VEC) {
+struct RawCkpt {
+  uint2 q;
+  uint32_t e[VEC ? 1 : 2];   // the eight columns' scale byte, or all eight of the group (a row's are a multiple of 4)
+  __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
     const int col = c0 + lane * 8;
-    if (col < c.pitch) {
-      const uint2 w = *reinterpret_cast<const uint2*>(q + col);
-      const float step = ckpt_step(s[col / kCkptBlock]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        v[j] = (float)(int8_t)((j < 4 ? w.x : w.y) >> (8 * (j & 3))) * step;
+    const uint8_t* s = c.scale + r * (c.pitch / kCkptBlock);
+    q = col < c.pitch ? *reinterpret_cast<const uint2*>(c.q + r * c.pitch + col) : make_uint2(0, 0);
+    if constexpr (VEC) {
+      e[0] = col < c.pitch ? s[col / kCkptBlock] : 7;
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = c0 + j * 32 + lane;
-      v[j] = col < c.pitch ? (float)q[col] * ckpt_step(s[col / kCkptBlock]) : 0.f;
+      for (int i = 0; i < 2; ++i)
+        e[i] = c0 + i * 128 < c.pitch ? *reinterpret_cast<const uint32_t*>(s + c0 / kCkptBlock + 4 * i) : 0x07070707u;
     }
   }
-}
-
-// A group of a checkpoint row, fetched some time before it is used.
-template <bool VEC>
-struct RawCkpt;
-template <>
-struct RawCkpt<true> {
-  uint2 q;
-  uint32_t e;
-  __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
-    const int col = c0 + lane * 8;
-    q = make_uint2(0, 0);
-    e = 7;
-    if (col < c.pitch) {
-      q = *reinterpret_cast<const uint2*>(c.q + r * c.pitch + col);
-      e = c.scale[r * (c.pitch / kCkptBlock) + col / kCkptBlock];
-    }
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const float step = ckpt_step(e);
+  __device__ __forceinline__ void get(float (&v)[8], int lane, int8_t* scratch) const {
+    if constexpr (VEC) {
+      const float step = ckpt_step(e[0]);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3))) * step;
+      for (int j = 0; j < 8; ++j) v[j] = (float)(int8_t)((j < 4 ? q.x : q.y) >> (8 * (j & 3))) * step;
+    } else {
+      *reinterpret_cast<uint2*>(scratch + lane * 8) = q;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = (float)scratch[j * 32 + lane] * ckpt_step((e[j / 4] >> (8 * (j & 3))) & 0xffu);
+      __syncwarp();
+    }
   }
 };
-template <>
-struct RawCkpt<false> {
-  int8_t q[8];
-  uint32_t e[2];   // the group's eight scale bytes (a row's are a multiple of 4)
-  __device__ __forceinline__ void load(const TsCkpt& c, int64_t r, int c0, int lane) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int col = c0 + j * 32 + lane;
-      q[j] = col < c.pitch ? c.q[r * c.pitch + col] : (int8_t)0;
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      e[i] = c0 + i * 128 < c.pitch
-                 ? *reinterpret_cast<const uint32_t*>(c.scale + r * (c.pitch / kCkptBlock) + c0 / kCkptBlock + 4 * i)
-                 : 0x07070707u;
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)q[j] * ckpt_step((e[j / 4] >> (8 * (j & 3))) & 0xffu);
-  }
+// The scratch of a block's WARPS for it.
+template <bool NEEDED, int WARPS>
+struct CkptScratch {
+  int8_t bytes[NEEDED ? WARPS : 1][kGroupCols];
+  __device__ __forceinline__ int8_t* mine() { return bytes[NEEDED ? threadIdx.x >> 5 : 0]; }
 };
 
 }  // namespace fg
