@@ -20,8 +20,8 @@
 //   warps 12-27 the checkpoint: two groups of eight that take turns by slot,
 //               64 tokens to each half: 16-byte loads of int8 values, a slot
 //               ahead, expanded to bf16, scaled and stored swizzled.
-// At 8192 x 4096 x 4096 this runs at 1350 TFLOP/s (70 % of the burst rate of
-// a plain bf16 product, 79 % of its sustained rate): the expansion's stores,
+// At 8192 x 4096 x 4096 this runs at 1335 TFLOP/s (69 % of the burst rate of
+// a plain bf16 product, 78 % of its sustained rate): the expansion's stores,
 // the copies' writes and the MMA's reads fill the 1024 cycles of
 // shared memory that a slot's MMAs take.  What was measured on the way (us a
 // call, and cycles of the issuing warp): a slot's wait, commit and first MMA
