@@ -194,14 +194,15 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
 //
 // 4096 x 50001 bf16 (rows at odd elements) takes 105 us with k = 20, 91 with
 // k = 8 and 73 with k = 0, where the logits' bytes at the copy rate take 60;
-// 2048 x 65536 f32 with k = 20 takes 95 of 79.  Instruction issue
-// bounds the bf16 rows: 86 instructions to a warp's 32 chunks, 16.8 thousand a
-// row with k = 0 (77 % of the issue slots), 25.4 thousand with k = 20 (81 %), by
-// the noting and by a row's end, where the bound, two selections and the second
-// reading are chains of latency too.  Other forms of that end, at k = 20: k passes over the row 3407 us, a selection by counting 210, a block's
-// ninth warp that finishes rows for the others 126, one selection from the
-// logits at or above a bound of the whole row 110, the chunks' maxima in
-// shared memory in place of the list 97, but the short rows 12 % slower.
+// 2048 x 65536 f32 with k = 20 takes 95 of 79.  Instruction issue bounds the
+// bf16 rows: 86 instructions to a warp's 32 chunks, 16.8 thousand a row with k =
+// 0 (77 % of the issue slots), 25.4 thousand with k = 20 (81 %), by the noting
+// and by a row's end, where the bound, two selections and the second reading
+// are chains of latency too.  Other forms of that end, at k = 20: k passes over
+// the row 3407 us, a selection by counting 210, a block's ninth warp that
+// finishes rows for the others 126, one selection from the logits at or above a
+// bound of the whole row 110, the chunks' maxima in shared memory in place of
+// the list 97, but the short rows 12 % slower.
 template <class T, int U, int W, int BLOCKS>
 __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kernel(const LogprobArgs a) {
   constexpr int kRows = W == 1 ? 4 : 1, kN = W * 32;   // rows a block, threads a row

@@ -38,7 +38,8 @@ __device__ __forceinline__ float row_sum(float v, float* red, int warp, int lane
 // instead of 44 from float32 to bf16 with the checkpoint, where memory's copy
 // rate allows 35.)
 template <class TX, class TY, bool VEC, int NW, int NC>
-__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8 ? 4 : NC == 2 ? 2 : 1) ts_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(NW == 1 ? 128 : NW * 32, NW == 1 ? 5 : NW == 8 ? 4 : NC == 2 ? 2 : 1)
+    ts_norm_kernel(const NormArgs a) {
   constexpr int kRows = NW == 1 ? 4 : 1;   // rows a block works on at a time
   __shared__ float red[2][NW];
   __shared__ __align__(16) float scratch[VEC ? 1 : kRows * NW][kGroupCols];

@@ -62,7 +62,9 @@ struct FromCkpt {
     __device__ __forceinline__ void load(const NormArgs&, const FromCkpt& s, int c0, int lane) {
       c.load(s.row, 0, c0, lane);
     }
-    __device__ __forceinline__ void get(float (&v)[8], int lane, int8_t* scratch) const { c.get(v, lane, scratch); }   // h
+    __device__ __forceinline__ void get(float (&v)[8], int lane, int8_t* scratch) const {
+      c.get(v, lane, scratch);   // h
+    }
   };
   __device__ __forceinline__ static float mean(const NormArgs&, int64_t) { return 0.f; }
   __device__ __forceinline__ static void prefetch(const NormArgs& a, int64_t row) {

@@ -555,8 +555,8 @@ typedef struct ts_ops ts_ops;
 fg_status ts_create(int64_t workspace_bytes, ts_ops** out);
 
 /* Synchronises the stream, then reads and clears the handle's error word:
- * FG_ETIMEOUT when a bounded wait (2 s) of a ts_weight_grad or
- * ts_layer_norm_backward kernel expired; that call's results are incomplete. */
+ * FG_ETIMEOUT when a bounded wait (2 s) of a ts_weight_grad kernel expired;
+ * that call's results are incomplete. */
 fg_status ts_sync_status(ts_ops* h, void* cuda_stream);
 
 void ts_destroy(ts_ops* h);
