@@ -646,15 +646,16 @@ cudaError_t backward_rows(const ts_ops& h, const NormArgs& a, cudaStream_t st) {
   }
   if (a.rows > 0 && a.cols <= 32 * kGroupCols) return backward_fused<TDY, Src, VEC, 2, 1, 1>(h, a, 16, st);
   if (a.rows > 0 && a.cols <= kWideGroups * 32 * kGroupCols) return backward_wide<TDY, Src, VEC>(h, a, st);
-  if (a.rows > 0) {
-    cudaLaunchConfig_t cfg = pdl_config((int)a.rows, 256, 0, st);
-    cudaLaunchAttribute at[1];
-    pdl_attr(cfg, at);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, ts_norm_dx_kernel<TDY, Src, VEC>, a);
+  // The sums first: dx may be dy.
+  if (a.dgamma || a.dbeta) {
+    cudaError_t e = columns<TDY, Src, VEC>(h, a, nullptr, st);
     if (e != cudaSuccess) return e;
   }
-  if (!a.dgamma && !a.dbeta) return cudaSuccess;
-  return columns<TDY, Src, VEC>(h, a, nullptr, st);
+  if (a.rows == 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = pdl_config((int)a.rows, 256, 0, st);
+  cudaLaunchAttribute at[1];
+  pdl_attr(cfg, at);
+  return cudaLaunchKernelEx(&cfg, ts_norm_dx_kernel<TDY, Src, VEC>, a);
 }
 
 template <class TDY, class Src>
