@@ -61,6 +61,14 @@ fg_status check_checkpoint(const void* p, bool needed) {
   if (reinterpret_cast<uintptr_t>(p) % 16) return err(FG_EINVAL, "checkpoint: must be 16-byte aligned");
   return FG_OK;
 }
+// An output that is an input too: rows have to lie alike, or one row's output
+// is another row's input (one row's pitch says nothing).
+fg_status check_in_place(const char* names, const void* out_p, int out_dtype, int64_t out_ld, const void* in_p,
+                         int in_dtype, int64_t in_ld, int64_t rows) {
+  if (out_p && out_p == in_p && (out_dtype != in_dtype || (rows > 1 && out_ld != in_ld)))
+    return err(FG_EINVAL, std::string(names) + " needs the same dtype and row pitch");
+  return FG_OK;
+}
 TsMat mat(const void* p, int dtype, int64_t ld) { return TsMat{p, dtype == FG_BF16, ld}; }
 TsOut out(void* p, int dtype, int64_t ld) { return TsOut{p, dtype == FG_BF16, ld}; }
 
@@ -153,6 +161,7 @@ fg_status ts_layer_norm(ts_ops* h, const void* x, fg_dtype x_dtype, int64_t ldx,
   TS_TRY(check_array("mean", mean, false));
   TS_TRY(check_array("rstd", rstd, false));
   TS_TRY(check_checkpoint(checkpoint, false));
+  TS_TRY(check_in_place("y in place of x", y, y_dtype, ldy, x, x_dtype, ldx, rows));
   if (!(eps >= 0.f)) return err(FG_EINVAL, "eps must not be negative");
   if (rows == 0) return FG_OK;
   NormArgs a;
@@ -179,6 +188,7 @@ fg_status ts_layer_norm_backward(ts_ops* h, const void* dy, fg_dtype dy_dtype, i
   if (x && checkpoint) return err(FG_EINVAL, "give x or its checkpoint, not both");
   TS_TRY(check_matrix("dy", dy, dy_dtype, lddy, rows, cols));
   TS_TRY(check_matrix("dx", dx, dx_dtype, lddx, rows, cols));
+  TS_TRY(check_in_place("dx in place of dy", dx, dx_dtype, lddx, dy, dy_dtype, lddy, rows));
   if (!checkpoint) {
     TS_TRY(check_matrix("x", x, x_dtype, ldx, rows, cols));
     if (x_dtype != dx_dtype) return err(FG_EINVAL, "dx has the dtype of x");
@@ -248,6 +258,7 @@ fg_status ts_activation_backward(ts_ops* h, int32_t opcode, const void* dy, fg_d
   TS_TRY(check_extent(rows, cols));
   TS_TRY(check_matrix("dy", dy, dy_dtype, lddy, rows, cols));
   TS_TRY(check_matrix("dx", dx, dx_dtype, lddx, rows, cols));
+  TS_TRY(check_in_place("dx in place of dy", dx, dx_dtype, lddx, dy, dy_dtype, lddy, rows));
   TS_TRY(check_checkpoint(checkpoint, rows > 0));
   if (rows == 0) return FG_OK;
   return done(launch_activation_backward(*h, act, mat(dy, dy_dtype, lddy),
@@ -328,8 +339,7 @@ fg_status ts_token_logprobs_backward(ts_ops* h, const void* logits, fg_dtype dty
   TS_TRY(check_array("g_logprob", g_logprob, rows > 0));
   TS_TRY(check_array("g_entropy", g_entropy, false));
   TS_TRY(check_array("entropy", entropy, rows > 0 && g_entropy));
-  if (logits && dlogits == logits && (d_dtype != dtype || ldd != ld))
-    return err(FG_EINVAL, "dlogits in place of logits needs the same dtype and row pitch");
+  TS_TRY(check_in_place("dlogits in place of logits", dlogits, d_dtype, ldd, logits, dtype, ld, rows));
   if (rows == 0) return FG_OK;
   LogprobArgs a;
   a.logits = mat(logits, dtype, ld);

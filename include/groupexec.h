@@ -538,7 +538,8 @@ void tf_layout_destroy(tf_layout* l);
  * >= columns) and any alignment to their element (rows that all start on 16
  * bytes run faster); vectors and row statistics are dense float32.  All
  * arithmetic and all sums are in float32; a bf16 output is rounded once.  No
- * output may overlap an input except where stated.  rows = 0 computes empty
+ * output may overlap an input except where stated (an output that starts where
+ * an input does, but has another dtype or row pitch, is FG_EINVAL).  rows = 0 computes empty
  * sums; cols is at least 1; extents are at most 2^31 - 65536.  Results do not
  * depend on scheduling: no sum uses atomics.
  *

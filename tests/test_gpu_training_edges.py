@@ -6,9 +6,9 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from group_execution_gb300 import Checkpoint
+from group_execution_gb300 import Checkpoint, _lib
 from oracle import training as OT
-from tests.test_gpu_training import BF16, F32, TOL, close, dev, empty, gap_kept, host, normal, ops, rounded, vec, within  # noqa: F401
+from tests.test_gpu_training import BF16, F32, TOL, close, dev, empty, gap_kept, host, normal, ops, refused, rounded, vec, within  # noqa: F401, E501
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,35 @@ def test_layer_norm_backward_in_place(ops, rows, cols, pad, dtype, from_ckpt):  
     n = 2.0 ** -24 * (rows / 8 + 64)
     within(dg, rg, n * np.abs(dy * h).sum(0) + 2.0 ** -22 * (np.abs(dy) * (np.abs(h) + 1)).sum(0) + 1e-30)
     within(db, rb, n * np.abs(dy).sum(0) + 1e-30)
+
+
+@pytest.mark.parametrize("op", ["relu", "sigmoid", "tanh"])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows, cols, pad", [(1, 1, 0), (5, 257, 1), (700, 1000, 8), (300, 4096, 0)])
+def test_activation_backward_in_place(ops, op, dtype, rows, cols, pad):  # noqa: F811
+    a = {"relu": lambda v: np.maximum(v, 0), "sigmoid": lambda v: 1 / (1 + np.exp(-v)), "tanh": np.tanh}[op](normal(cols, rows, cols))
+    b = OT.checkpoint_encode(a)
+    dy = rounded(normal(cols + 1, rows, cols), dtype)
+    t = empty((rows, cols), dtype, pad)
+    t.copy_(dev(dy, dtype))
+    ops.activation_backward(op, t, Checkpoint(rows, cols, torch.from_numpy(b).cuda()), t)
+    close(t, OT.activation_backward(op, dy, OT.checkpoint_decode(b, rows, cols)), TOL[dtype])
+    gap_kept(t, pad)
+
+
+def test_in_place_needs_the_same_type_and_pitch(ops):  # noqa: F811
+    # one buffer of 64 rows' room, seen as float32 and bf16 and at two pitches
+    x = torch.zeros((64, 64), device="cuda")
+    as_bf16, narrow = x.view(BF16)[:32, :32], x[:32, :32]
+    wide = torch.as_strided(x, (32, 32), (128, 1))
+    s = torch.zeros(32, device="cuda")
+    ck, E = Checkpoint(32, 32, torch.zeros(32 * 132, dtype=torch.uint8, device="cuda")), _lib.FG_EINVAL
+    for y in (as_bf16, wide):
+        refused(E, ops.layer_norm, narrow, None, None, y, s, s)
+        refused(E, ops.layer_norm_backward, y, ck, None, None, s, narrow, None, None)
+        refused(E, ops.activation_backward, "tanh", narrow, ck, y)
+        refused(E, ops.token_logprobs_backward, narrow, torch.zeros(32, dtype=torch.int64, device="cuda"), s, None, s, None, y)
+    # a single row has no pitch; the same rows are fine
+    ops.layer_norm(narrow[:1], None, None, wide[:1], None, None)
+    ops.activation_backward("tanh", narrow, ck, narrow)
+    ops.sync()
