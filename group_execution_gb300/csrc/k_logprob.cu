@@ -1,8 +1,9 @@
 // Log probabilities of given tokens under rows of logits, with the entropy
 // and the k most likely alternatives, and their gradient.  With L = log sum
 // exp(x):
-//   logprob = x_tok - L,  H = log sum e - sum e (x - max) / sum e,
-// and for output gradients g (logprob) and w (entropy)
+//   logprob = x_tok - L,  H = log s - sum e^(x - m) (x - m) / s,  s = sum e^(x - m),
+// for any reference m, here one at most kLag below the row's largest logit: the
+// two terms of H cancel the further, the further m is below it.  For output gradients g (logprob) and w (entropy)
 //   dx_v = g (1[v = tok] - p_v) - w p_v (log p_v + H).
 // A row whose every logit is -inf has no distribution: L and the log
 // probabilities are -inf, the entropy and the gradient 0.  A row that holds a
@@ -29,6 +30,13 @@ struct Softmax {
   float m, s, t;
 };
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+// How far a logit may lie above the reference of its sums.  The entropy is then
+// off by the roundings of numbers of that size (with 32, which float32's range
+// allows, confident rows were 1e-5 off and their entropy negative).  With 0
+// each larger logit of a rising row moves the sums, and each move costs an
+// exponential's error.  4096 x 50001 bf16 without alternatives takes 73.6 us
+// with 32, 73.9 with 2, 74.2 with 1, 74.6 with 0.
+constexpr float kLag = 1.f;
 
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -180,8 +188,8 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
 //
 // Each thread first loads U chunks of eight logits.  Their maximum over the
 // row's threads is the reference of every thread's sums; a thread moves its
-// own only when a chunk exceeds it by 2^5, which keeps the exponentials in
-// range without a running maximum per logit.  From the same chunks comes a
+// own when a chunk exceeds it by kLag (few do, after the first ones), so
+// there is no running maximum per logit.  From the same chunks comes a
 // lower bound of the k-th largest logit: every warp takes the r-th largest of
 // its lanes' maxima, and the q-th largest of these, q r >= k, has at least k
 // logits at or above it.  A chunk below the bound costs one comparison; one
@@ -192,8 +200,8 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
 // order), its own k-th largest is the next bound and the row is read again
 // for the list alone; the bound rises every time.
 //
-// 4096 x 50001 bf16 (rows at odd elements) takes 105 us with k = 20, 91 with
-// k = 8 and 73 with k = 0, where the logits' bytes at the copy rate take 60;
+// 4096 x 50001 bf16 (rows at odd elements) takes 106 us with k = 20, 92 with
+// k = 8 and 74 with k = 0, where the logits' bytes at the copy rate take 60;
 // 2048 x 65536 f32 with k = 20 takes 95 of 79.  Instruction issue bounds the
 // bf16 rows: 86 instructions to a warp's 32 chunks, 16.8 thousand a row with k =
 // 0 (77 % of the issue slots), 25.4 thousand with k = 20 (81 %), by the noting
@@ -291,7 +299,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kern
   Softmax acc{seed, 0.f, 0.f};
   uint64_t s2 = 0, t2 = 0;
   float minus_m = seed == -INFINITY ? 0.f : -seed;
-  float limit = seed + 32.f;
+  float limit = seed + kLag;
   auto sums = [&](const float (&v)[8]) {
     const uint64_t l2 = pack2f(kLog2e, kLog2e), m2 = pack2f(minus_m, minus_m);
 #pragma unroll
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kern
     s2 = pack2f(acc.s, 0.f);
     t2 = pack2f(acc.t, 0.f);
     minus_m = -m;
-    limit = m + 32.f;
+    limit = m + kLag;
   };
   auto note = [&](float m, int col) {
     const unsigned long long k = composite(m, col);
@@ -370,19 +378,11 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kern
     if (rounds * U * kN + tid + u * kN < chunks) take(c[u], col + u * kN * 8);
 
   settle();
-  int one;
-  __match_all_sync(0xffffffffu, __float_as_uint(acc.m), &one);
-  if (one) {   // no lane moved its reference
-    acc.s = warp_sum(acc.s);
-    acc.t = warp_sum(acc.t);
-  } else {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Softmax p{__shfl_xor_sync(0xffffffffu, acc.m, o), __shfl_xor_sync(0xffffffffu, acc.s, o),
-                      __shfl_xor_sync(0xffffffffu, acc.t, o)};
-      acc = merge(acc, p);
-    }
-  }
+  // a warp's sums, about its lanes' largest reference
+  const float top_m = key_value(__reduce_max_sync(0xffffffffu, order_key(acc.m)));
+  if (acc.m != top_m) move_reference(acc, top_m);
+  acc.s = warp_sum(acc.s);
+  acc.t = warp_sum(acc.t);
   if (W > 1 && lane == 0) sh.warp[warp] = acc;
   row_sync<W>();
   unsigned long long mine = 0;   // the lane-th largest, in the row's first warp
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kern
   const float ln = logf(acc.s), lse = none ? -INFINITY : acc.m + ln;
   if (lane == 0) {
     if (a.lse) a.lse[row] = lse;
-    if (a.entropy) a.entropy[row] = none ? 0.f : ln - kLn2 * (acc.t / acc.s);
+    if (a.entropy) a.entropy[row] = none ? 0.f : max_nan(ln - kLn2 * (acc.t / acc.s), 0.f);
     if (a.logprob) a.logprob[row] = tok < 0 || tok >= a.vocab ? 0.f : none ? -INFINITY : tok_logit - lse;
   }
   if (lane < a.k) {

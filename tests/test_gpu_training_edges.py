@@ -80,3 +80,51 @@ def test_in_place_needs_the_same_type_and_pitch(ops):  # noqa: F811
     ops.layer_norm(narrow[:1], None, None, wide[:1], None, None)
     ops.activation_backward("tanh", narrow, ck, narrow)
     ops.sync()
+
+
+# ---- log probabilities ------------------------------------------------------------
+
+
+def peaked(kind, rows, vocab):
+    """Confident rows: one logit in the row's last tenth lies 0.5 to 31 above
+    the rest; or all logits in rising order."""
+    r = np.random.default_rng(vocab + rows)
+    x = (r.normal(size=(rows, vocab)) * 2.5).astype(np.float32)
+    if kind == "rising":
+        return np.sort(x * r.uniform(0.1, 12, size=(rows, 1)).astype(np.float32), axis=1)
+    at = r.integers(vocab - vocab // 10 - 1, vocab, size=rows)
+    x[np.arange(rows), at] = x.max(1) + r.uniform(0.5, 31, size=rows)
+    return x
+
+
+# a row cut over a cluster, eight warps, four warps, one warp to a row
+@pytest.mark.parametrize("k", [0, 20])
+@pytest.mark.parametrize("kind", ["late", "rising"])
+@pytest.mark.parametrize("dtype, pad", [(F32, 0), (F32, 3), (BF16, 7)])
+@pytest.mark.parametrize("rows, vocab", [(64, 50001), (650, 16391), (650, 5003), (2500, 1500)])
+def test_token_logprobs_of_confident_rows(ops, rows, vocab, dtype, pad, kind, k):  # noqa: F811
+    x = rounded(peaked(kind, rows, vocab), dtype)
+    tokens = x.argmax(1)
+    tokens[::3] = np.random.default_rng(1).integers(0, vocab, size=len(tokens[::3]))
+    lp, ent, lse, tlp, ids = OT.token_logprobs(x, tokens, k)
+    out = [torch.empty(rows, device="cuda") for _ in range(3)]
+    gl = torch.empty((rows, k), device="cuda") if k else None
+    gi = torch.empty((rows, k), dtype=torch.int32, device="cuda") if k else None
+    ops.token_logprobs(dev(x, dtype, pad), torch.from_numpy(tokens).cuda(), *out, gl, gi)
+    glp, gent, glse = (host(o) for o in out)
+    # With the sums about a reference within 1 of the row's largest logit, s =
+    # sum e^(x - m) is at most a few times its largest term: a thread adds 4
+    # values a chunk (at most 16 chunks here), then come at most 24 joins, each
+    # addition 2^-24 of s off.  ln s and t / s are then about 1 + H, a dozen
+    # roundings of 2^-24.  An exponential's own error (2^-22, and 2^-23 of its
+    # argument, at most 64 where it counts) enters the entropy times p |log p|.
+    unit = 2.0 ** -24 * (4 * 16 + 24 + 12 + (4 + 128) * ent)
+    assert (np.abs(gent - ent) <= unit).all(), np.max((np.abs(gent - ent) / unit))
+    assert (gent >= 0).all()
+    # lse = m + ln s, and x - lse: two roundings of numbers of that size more
+    big = np.abs(x).max(1)
+    assert (np.abs(glse - lse) <= unit + 2.0 ** -23 * (big + 16)).all()
+    assert (np.abs(glp - lp) <= unit + 2.0 ** -22 * (big + 16)).all()
+    if k:
+        np.testing.assert_array_equal(gi.cpu().numpy(), ids)
+        assert (np.abs(host(gl) - tlp) <= (unit + 2.0 ** -22 * (big + 16))[:, None]).all()
