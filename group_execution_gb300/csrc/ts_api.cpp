@@ -189,7 +189,7 @@ fg_status ts_layer_norm_backward(ts_ops* h, const void* dy, fg_dtype dy_dtype, i
   TS_TRY(check_matrix("dy", dy, dy_dtype, lddy, rows, cols));
   TS_TRY(check_matrix("dx", dx, dx_dtype, lddx, rows, cols));
   TS_TRY(check_in_place("dx in place of dy", dx, dx_dtype, lddx, dy, dy_dtype, lddy, rows));
-  if (!checkpoint) {
+  if (!checkpoint && (x || rows > 0)) {   // (no rows: either buffer may be null)
     TS_TRY(check_matrix("x", x, x_dtype, ldx, rows, cols));
     if (x_dtype != dx_dtype) return err(FG_EINVAL, "dx has the dtype of x");
     TS_TRY(check_array("mean", mean, rows > 0));

@@ -128,3 +128,17 @@ def test_token_logprobs_of_confident_rows(ops, rows, vocab, dtype, pad, kind, k)
     if k:
         np.testing.assert_array_equal(gi.cpu().numpy(), ids)
         assert (np.abs(host(gl) - tlp) <= (unit + 2.0 ** -22 * (big + 16))[:, None]).all()
+
+
+# ---- no rows --------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [40, 17000])
+def test_layer_norm_backward_from_an_empty_checkpoint(ops, cols, dtype, accumulate):  # noqa: F811
+    dy, dx, s = torch.empty((0, cols), dtype=dtype, device="cuda"), torch.empty((0, cols), dtype=dtype, device="cuda"), vec([])
+    dg, db = torch.full((cols,), 5.0, device="cuda"), torch.full((cols,), 6.0, device="cuda")
+    ops.layer_norm_backward(dy, Checkpoint(0, cols), None, None, s, dx, dg, db, accumulate=accumulate)
+    ops.sync()
+    assert (dg == (5 if accumulate else 0)).all() and (db == (6 if accumulate else 0)).all()
