@@ -92,6 +92,7 @@ SIGNATURES = {
     "tf_bucket_ready": (_I32, [_P, _I32, _P]),
     "tf_layout_destroy": (None, [_P]),
     "ts_create": (_I32, [_I64, _P]),
+    "ts_set_wait_limit": (_I32, [_P, _I64, _I32]),
     "ts_sync_status": (_I32, [_P, _P]),
     "ts_destroy": (None, [_P]),
     "ts_layer_norm": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _F, _P, _I32, _I64, _P, _P, _P, _P]),

@@ -45,8 +45,8 @@
 // copied to the workspace at an aligned pitch, as many tokens at a time as
 // half of it takes.
 //
-// Every wait is bounded; on expiry the CTA records the error, drains its
-// copies, frees its TMEM and returns.
+// Every wait is bounded; on expiry the CTA records the error, the pair waits
+// for the copies that either CTA has in flight, frees its TMEM and returns.
 #include <cuda.h>
 
 #include <algorithm>
@@ -76,7 +76,6 @@ constexpr int kStageFloats = 32 * kStagePitch;   // an epilogue warp's
 template <bool WIDE>
 constexpr int kSmem = kSlots * kSlotBytes + 1024 + (WIDE ? 0 : 8 * kStageFloats * 4);
 constexpr int kChain = 16;                       // blocks of kKB tokens one accumulation runs over
-constexpr int64_t kWaitNs = 2000000000LL;
 constexpr int64_t kPieceFloats = (int64_t)kTile * kTile;
 
 struct WgradKernel {
@@ -95,6 +94,8 @@ struct WgradKernel {
   float4* part;        // the cut tiles' pieces
   float4* chain;       // each pair's running partial
   int32_t* err;
+  int64_t wait_limit_ns;
+  int inject;
 };
 
 struct Item {
@@ -112,13 +113,13 @@ __device__ __forceinline__ int segment_end(const Item& w, int kb0) {
   return w.kb1 - kb0 > kChain ? kb0 + kChain : w.kb1;
 }
 
-// Waits for the phase with the given parity, at most kWaitNs and only while
+// Waits for the phase with the given parity, at most `limit` ns and only while
 // no thread of the CTA has given up.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int64_t limit, volatile int* abort_flag) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity))
-    if (*abort_flag || (int64_t)(global_ns() - t0) > kWaitNs) return false;
+    if (*abort_flag || (int64_t)(global_ns() - t0) > limit) return false;
   return true;
 }
 // Four int8 values -> two bf16 pairs, times a power of two, exactly: with
@@ -138,6 +139,10 @@ __device__ __forceinline__ void expand4(uint32_t w, __nv_bfloat162 step, uint32_
 __device__ __forceinline__ __nv_bfloat162 bf16_step(uint32_t e) {
   const uint32_t h = e < 255 ? (max(e, 7u) - 6) << 7 : 0x7fc0u, w = h | h << 16;
   return *reinterpret_cast<const __nv_bfloat162*>(&w);
+}
+
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 // 16 consecutive f32 columns of this warp's 32 lanes of tensor memory.
@@ -208,7 +213,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_wgrad_kernel(const __grid_constant__ WgradKernel P) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 5];
-  __shared__ int abort_flag, issued;
+  __shared__ int abort_flag, issued[2];         // copies that either lane of warp 0 has issued
+  __shared__ int peer_gave_up, peer_issued;     // written by the pair's other CTA
   __shared__ uint32_t tmem_slot;
   __shared__ __align__(16) float colsums[8][kTile / 2];
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -221,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
   const int nkb = (P.rows + kKB - 1) / kKB;
   if (threadIdx.x == 0) {
-    abort_flag = issued = 0;
+    abort_flag = issued[0] = issued[1] = 0;
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(full0 + 8 * s, 1 + 2 * 8);   // the even CTA's expect_tx, a group of eight warps in each CTA
       mbar_init(empty0 + 8 * s, 1);
@@ -244,7 +250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ---- dY producer: lane 0 the first 64 columns, lane 1 the rest ----
-    if (lane < 2) {
+    if (lane < 2 && !P.inject) {
       const int g = lane;
       tma_prefetch(&P.dy);
       const uint64_t keep = l2_evict_last();
@@ -256,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Item w = item_of(P, x, nkb);
         const int n0 = w.tile % P.tiles_n * kTile + h * kHalf + g * 64;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, &abort_flag)) {
+          if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
           }
@@ -269,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (g == 0) issued = it;
+      issued[g] = it;
       if (!ok) {
         abort_flag = 1;
         set_error(P.err, DEVERR_TIMEOUT);
@@ -290,13 +296,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Item w = item_of(P, x, nkb);
         for (int s0 = w.kb0; s0 < w.kb1 && ok; ++i) {
           const int s1 = segment_end(w, s0), b = i & 1;
-          if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, &abort_flag)) {
+          if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
           for (int kb = s0; kb < s1; ++kb) {
-            if (!wait_bar(full0 + 8 * s, ph, &abort_flag)) {
+            if (!wait_bar(full0 + 8 * s, ph, P.wait_limit_ns, &abort_flag)) {
               ok = false;
               break;
             }
@@ -354,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float4* piece = w.piece < 0 ? nullptr : P.part + (int64_t)(w.piece * 2 + h) * (kPieceFloats / 8) + r;
       for (int s0 = w.kb0; s0 < w.kb1; ++i) {
         const int s1 = segment_end(w, s0), b = i & 1;
-        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, &abort_flag));
+        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, P.wait_limit_ns, &abort_flag));
         if (!ok) break;
         tc_fence_after();
         const uint32_t acc0 = tmem + ((uint32_t)(q * 32) << 16) + b * kTile;
@@ -500,7 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int blk = group; lx < P.items; blk += kGroups) {
       const int s = blk % kSlots;
       if (blk >= kSlots) {
-        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ((blk / kSlots) & 1) ^ 1, &abort_flag));
+        ok = __all_sync(0xffffffffu, wait_bar(empty0 + 8 * s, ((blk / kSlots) & 1) ^ 1, P.wait_limit_ns, &abort_flag));
         if (!ok) break;
       }
       uint8_t* dst = ring + s * kSlotBytes;
@@ -528,15 +534,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (abort_flag && leader && threadIdx.x == 0) {
-    // dY's copies in flight complete on the even CTA's barriers; the slots
-    // they fill may lack arrivals, so each wait may run to its limit
-    for (int k = issued - kSlots < 0 ? 0 : issued - kSlots; k < issued; ++k)
-      mbar_wait(full0 + 8 * (k % kSlots), (k / kSlots) & 1, kDrainLimitNs);
+  const int mine = issued[0] > issued[1] ? issued[0] : issued[1];
+  if (threadIdx.x == 0) {
+    st_cluster(cluster_addr(smem_u32(&peer_gave_up), h ^ 1), abort_flag);
+    st_cluster(cluster_addr(smem_u32(&peer_issued), h ^ 1), mine);
   }
+  __syncwarp();
   // no CTA leaves while its peer may still write to its shared memory or
   // issue MMAs into its TMEM
   cluster_sync();
+  if (abort_flag || peer_gave_up) {   // (the same in both CTAs)
+    // either CTA's copies in flight complete on the even CTA's barriers; the
+    // slots they fill may lack arrivals, so each wait may run to its limit
+    if (leader && threadIdx.x == 0) {
+      const int last = mine > peer_issued ? mine : peer_issued;
+      for (int k = last - kSlots < 0 ? 0 : last - kSlots; k < last; ++k)
+        mbar_wait(full0 + 8 * (k % kSlots), (k / kSlots) & 1, kDrainLimitNs);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after();
   if (warp == 1) tmem_dealloc<2>(tmem, 512);
 }
@@ -743,6 +760,8 @@ cudaError_t launch_weight_grad(const ts_ops& h, const WgradArgs& a, cudaStream_t
   P.lddw = a.lddw;
   P.accumulate = a.accumulate;
   P.err = h.err;
+  P.wait_limit_ns = h.wait_limit_ns;
+  P.inject = h.inject;
   if (aligned) return product(h, P, a.x, a.dy, a.rows, h.ws, room, st);
   // an aligned copy of as many tokens of dy as leave the column sums' room and
   // about half of the workspace; a call's whole work for each copy

@@ -14,6 +14,8 @@ struct ts_ops {
   uint8_t* ws = nullptr;
   int64_t ws_bytes = 0;
   int32_t* err = nullptr;   // latched by a bounded wait that expired
+  int64_t wait_limit_ns = 2000000000LL;
+  int inject = 0;           // failure injection for tests: no copies are issued
 };
 
 namespace fg {

@@ -10,6 +10,7 @@
 #include <utility>
 
 #include "groupexec.h"
+#include "host.h"
 #include "launch.h"
 #include "ts.h"
 
@@ -126,6 +127,15 @@ fg_status ts_create(int64_t workspace_bytes, ts_ops** out_h) {
     return cuda_err(e, "cudaMemset(error word)");
   }
   *out_h = h.release();
+  return FG_OK;
+}
+
+fg_status ts_set_wait_limit(ts_ops* h, int64_t wait_limit_ns, int32_t flags) {
+  if (!h) return err(FG_EINVAL, "null handle");
+  if (wait_limit_ns <= 0) return err(FG_EINVAL, "wait_limit_ns must be positive");
+  if (flags & ~FG_FLAG_INJECT_NO_LOADS) return err(FG_EINVAL, "unknown flag");
+  h->wait_limit_ns = wait_limit_ns;
+  h->inject = (flags & FG_FLAG_INJECT_NO_LOADS) != 0;
   return FG_OK;
 }
 

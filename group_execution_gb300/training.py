@@ -84,12 +84,14 @@ class Checkpoint:
 class TrainingOps:
     """A handle of the training-step operators on the current device.  Calls
     of one handle must be ordered (one stream, or streams that wait for each
-    other); use one handle per concurrent stream."""
+    other); use one handle per concurrent stream.  wait_limit_ns bounds every
+    device-side wait."""
 
-    def __init__(self, workspace_bytes=0):
+    def __init__(self, workspace_bytes=0, wait_limit_ns=2_000_000_000, flags=0):
         self.lib = _lib.load()
         self.h = C.c_void_p()
         _lib.check(self.lib.ts_create(workspace_bytes, C.byref(self.h)))
+        _lib.check(self.lib.ts_set_wait_limit(self.h, wait_limit_ns, flags))
         self.device = torch.cuda.current_device()
 
     def __del__(self):

@@ -555,9 +555,13 @@ typedef struct ts_ops ts_ops;
  * gradients need 16 bytes a column of dy (FG_EUNSUPPORTED otherwise). */
 fg_status ts_create(int64_t workspace_bytes, ts_ops** out);
 
+/* How long a device-side wait of the handle's later calls may last (ns, at least
+ * 1; 2 s unless set).  flags: 0. */
+fg_status ts_set_wait_limit(ts_ops* h, int64_t wait_limit_ns, int32_t flags);
+
 /* Synchronises the stream, then reads and clears the handle's error word:
- * FG_ETIMEOUT when a bounded wait (2 s) of a ts_weight_grad kernel expired;
- * that call's results are incomplete. */
+ * FG_ETIMEOUT when a bounded wait of a ts_weight_grad kernel expired; that
+ * call's results are incomplete. */
 fg_status ts_sync_status(ts_ops* h, void* cuda_stream);
 
 void ts_destroy(ts_ops* h);

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from group_execution_gb300 import Checkpoint, _lib
+from group_execution_gb300 import Checkpoint, TrainingOps, _lib
 from oracle import training as OT
 from tests.test_gpu_training import BF16, F32, TOL, close, dev, empty, gap_kept, host, normal, ops, refused, rounded, vec, within  # noqa: F401, E501
 
@@ -142,3 +142,41 @@ def test_layer_norm_backward_from_an_empty_checkpoint(ops, cols, dtype, accumula
     ops.layer_norm_backward(dy, Checkpoint(0, cols), None, None, s, dx, dg, db, accumulate=accumulate)
     ops.sync()
     assert (dg == (5 if accumulate else 0)).all() and (db == (6 if accumulate else 0)).all()
+
+
+# ---- expired waits ---------------------------------------------------------------
+
+
+# one tile; pieces of tiles; whole tiles of two accumulations; rows of dy that
+# go through a copy
+@pytest.mark.parametrize("rows, cols, n, pad", [(300, 200, 144, 0), (3000, 600, 700, 8), (2300, 2560, 2304, 0), (1000, 333, 777, 5)])
+def test_weight_grad_reports_an_expired_wait(rows, cols, n, pad):
+    # no copy is ever issued, so every wait runs out after 1 ms: the kernel
+    # gives its tensor memory back and returns, the handle reports it once, and
+    # the next calls of this and of another handle are right
+    stuck = TrainingOps(wait_limit_ns=1_000_000, flags=_lib.FG_FLAG_INJECT_NO_LOADS)
+    b = OT.checkpoint_encode(normal(rows, rows, cols))
+    h = OT.checkpoint_decode(b, rows, cols)
+    dy = rounded(normal(rows + 1, rows, n) * 0.1, BF16)
+    ck, d = Checkpoint(rows, cols, torch.from_numpy(b).cuda()), dev(dy, BF16, pad)
+    dw = torch.zeros((cols, n), device="cuda")
+    stuck.weight_grad(ck, d, dw)
+    refused(_lib.FG_ETIMEOUT, stuck.sync)
+    stuck.sync()                      # the error word was cleared
+    ref = OT.weight_grad(h, dy)[0]
+    _lib.check(stuck.lib.ts_set_wait_limit(stuck.h, 2_000_000_000, 0))
+    for handle in (TrainingOps(), stuck):
+        dw.fill_(float("nan"))
+        handle.weight_grad(ck, d, dw)
+        handle.sync()
+        # the bound of every weight gradient here: products are exact, each of
+        # rows + 8 additions is off by 2^-23 of its partial sum at most
+        within(dw, ref, 2.0 ** -23 * (rows + 8) * (np.abs(h).T @ np.abs(dy)) + 1e-30)
+
+
+def test_wait_limit_refusals(ops):  # noqa: F811
+    E = _lib.FG_EINVAL
+    refused(E, TrainingOps, 0, wait_limit_ns=0)
+    refused(E, TrainingOps, 0, wait_limit_ns=-5)
+    refused(E, TrainingOps, 0, flags=1)
+    assert ops.lib.ts_set_wait_limit(None, 1, 0) == E
