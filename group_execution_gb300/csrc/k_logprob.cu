@@ -183,6 +183,19 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
   return v;
 }
 
+// Notes k in the row's list if it is at or above tau.  The i-th note takes any of
+// i + 1 places, of which the list has the first: a full one holds a sample of
+// all notes, evenly spread over them.  (Stores to one place may meet; either
+// note will do.)
+template <int W>
+__device__ __forceinline__ void note_sample(LpShared<W>& sh, unsigned long long k, unsigned long long tau) {
+  constexpr uint32_t kRoom = sizeof(sh.cand) / 8;
+  if (k < tau) return;
+  uint32_t i = atomicAdd(&sh.count, 1);
+  if (i >= kRoom) i = __umulhi(i * 2654435769u, i + 1);
+  if (i < kRoom) *static_cast<volatile unsigned long long*>(&sh.cand[i]) = k;
+}
+
 // One row, or one of a cluster's equal segments of a row, to W warps.  One
 // pass:
 //
@@ -198,7 +211,10 @@ __device__ __forceinline__ unsigned long long largest32(const unsigned long long
 // column), so at the end those are picked from the list, read again (L2) and
 // their logits picked from.  Should the list overflow (logits in rising
 // order), its own k-th largest is the next bound and the row is read again
-// for the list alone; the bound rises every time.
+// for the list alone; should it overflow again, it then holds a sample of all
+// notes, whose k-th largest leaves about k / 1024 of them, whatever their order.
+// Rising rows are thus read twice more up to 2^15 chunks (700 x 131072 f32 takes
+// 170 us, random logits 70 to 125), three times up to 2^20.
 //
 // 4096 x 50001 bf16 (rows at odd elements) takes 106 us with k = 20, 92 with
 // k = 8 and 74 with k = 0, where the logits' bytes at the copy rate take 60;
@@ -396,12 +412,20 @@ __global__ void __launch_bounds__(W == 1 ? 128 : W * 32, BLOCKS) ts_logprob_kern
       tau = sh.top[a.k - 1];
       if (tid == 0) sh.count = 0;
       row_sync<W>();
-      for (int i = tid; i < chunks; i += kN) {
+      int i = tid;
+      for (; i + 3 * kN < chunks; i += 4 * kN) {
+        Chunk<T> ch[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) ch[u].load(x + first + (int64_t)(i + u * kN) * 8);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) note_sample(sh, composite(ch[u].top(), first + (i + u * kN) * 8), tau);
+      }
+      for (; i < chunks; i += kN) {
         Chunk<T> ch;
         ch.load(x + first + (int64_t)i * 8);
-        note(ch.top(), first + i * 8);
+        note_sample(sh, composite(ch.top(), first + i * 8), tau);
       }
-      if (my_loose >= 0) note(loose_v, my_loose);
+      if (my_loose >= 0) note_sample(sh, composite(loose_v, my_loose), tau);
       row_sync<W>();
       n = sh.count;
     }

@@ -130,6 +130,35 @@ def test_token_logprobs_of_confident_rows(ops, rows, vocab, dtype, pad, kind, k)
         assert (np.abs(host(gl) - tlp) <= (unit + 2.0 ** -22 * (big + 16))[:, None]).all()
 
 
+@pytest.mark.parametrize("k", [1, 32])
+@pytest.mark.parametrize("rows, vocab", [(1, 1 << 27), (3, 400_003), (700, 40_000)])
+def test_top_logits_of_rising_rows(ops, rows, vocab, k):  # noqa: F811
+    # Every chunk lies above those before it, so none can be left out by them:
+    # a row is read again until a bound from a sample leaves few enough, about
+    # four times at most here.  An atomic for each noted chunk makes a reading
+    # a few times longer than one of random logits.
+    rising = (torch.arange(vocab, device="cuda") * (30.0 / vocab)).expand(rows, vocab).contiguous()
+    random = torch.randn((rows, vocab), generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")
+    ids, lp = torch.empty((rows, k), dtype=torch.int32, device="cuda"), torch.empty((rows, k), device="cuda")
+
+    def microseconds(x):
+        times = []
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            ops.token_logprobs(x, None, None, None, None, lp, ids)
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 1e3)
+        return sorted(times)[1]
+
+    fast, slow = microseconds(random), microseconds(rising)
+    # equal logits (float32 has fewer values than the row): lowest column first
+    want = torch.sort(rising[0], descending=True, stable=True)[1][:k].to(torch.int32)
+    assert torch.equal(ids, want.expand(rows, k))
+    assert slow <= 50 * fast, (slow, fast)
+
+
 # ---- no rows --------------------------------------------------------------------
 
 
