@@ -209,3 +209,137 @@ def test_wait_limit_refusals(ops):  # noqa: F811
     refused(E, TrainingOps, 0, wait_limit_ns=-5)
     refused(E, TrainingOps, 0, flags=1)
     assert ops.lib.ts_set_wait_limit(None, 1, 0) == E
+
+
+# ---- loops that run more than once ---------------------------------------------------
+
+
+def device_rows(seed, rows, cols, dtype, scale=1.0, shift=0.0):
+    """A matrix made and held on the GPU, and the same in 64 bits."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    x = (torch.randn((rows, cols), generator=gen, device="cuda") * scale + shift).to(dtype)
+    return x, x.double()
+
+
+def device_close(got, ref, tol):
+    """close(), on the GPU."""
+    err = (got.double() - ref).abs() / torch.maximum(ref.abs(), ref.square().mean().sqrt())
+    assert err.max().item() <= tol, err.max().item()
+
+
+# several rows to every resident block, of each number of warps and groups a
+# row (8, 16 and 16 warps; a warp to a row), an even and an odd number of them
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("xt, yt", [(F32, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("rows, cols", [(9001, 520), (7000, 1024), (3001, 2048), (2000, 4096), (1501, 5003), (1000, 8192),
+                                        (701, 16384), (700, 12000)])
+def test_layer_norm_of_many_rows(ops, rows, cols, xt, yt, pad):  # noqa: F811
+    x, xd = device_rows(cols, rows, cols, xt, 1.5, 0.4)
+    src, y = empty((rows, cols), xt, pad), empty((rows, cols), yt, pad)
+    src.copy_(x)
+    gamma, beta = vec(normal(1, cols) * 0.1 + 1), vec(normal(2, cols) * 0.1)
+    m, r, ck = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), Checkpoint(rows, cols)
+    ops.layer_norm(src, gamma, beta, y, m, r, ckpt=ck)
+    ops.sync()
+    gap_kept(y, pad)
+    mean = xd.mean(1)
+    d = xd - mean[:, None]
+    rstd = (d.square().mean(1) + 1e-5).rsqrt()
+    h = d * rstd[:, None]
+    # the tolerances of single rows (a few dozen roundings, one more in bf16)
+    device_close(y, h * gamma.double() + beta.double(), TOL[yt])
+    device_close(m, mean, 1e-5)
+    device_close(r, rstd, 1e-5)
+    back = torch.empty((rows, cols), device="cuda")
+    ops.checkpoint_load(ck, back)
+    top = torch.nn.functional.pad(h.abs(), (0, -cols % 32)).unflatten(1, (-1, 32)).amax(2)
+    step = torch.exp2(torch.floor(torch.log2(top * (1 + 1e-5))) - 6).repeat_interleave(32, 1)[:, :cols]
+    # half a step, a whole one for what 127 steps do not reach, and h's error
+    assert ((back.double() - h).abs() <= torch.where(h.abs() > 127 * step, step, step / 2) + 2e-5 * h.abs().clamp(min=1)).all()
+
+
+# W = 4, 8, 16 warps a row and G = 2, 32 warps, with even and odd numbers of
+# rows a slot: the next rows in flight, both halves of the row sums' buffer
+@pytest.mark.parametrize("from_ckpt", [False, True])
+@pytest.mark.parametrize("pad", [0, 3])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows, cols", [(3001, 1000), (2600, 1024), (1900, 2048), (1001, 2048), (1000, 4096), (609, 4000),
+                                        (760, 5003), (457, 8192), (700, 12000)])
+def test_layer_norm_backward_of_many_rows(ops, rows, cols, dtype, pad, from_ckpt):  # noqa: F811
+    x, xd = device_rows(cols, rows, cols, dtype, 1.5, 0.4)
+    dy, dyd = device_rows(cols + 1, rows, cols, dtype)
+    gamma = vec(normal(1, cols) * 0.1 + 1)
+    mean = xd.mean(1).float()
+    rstd = ((xd - mean.double()[:, None]).square().mean(1) + 1e-5).rsqrt().float()
+    h = (xd - mean.double()[:, None]) * rstd.double()[:, None]
+    if from_ckpt:
+        src = Checkpoint(rows, cols)
+        ops.checkpoint_save(h.float(), src)
+        back = torch.empty((rows, cols), device="cuda")
+        ops.checkpoint_load(src, back)
+        h = back.double()
+    else:
+        src = empty((rows, cols), dtype, pad)
+        src.copy_(x)
+    dyt, dx = empty((rows, cols), dtype, pad), empty((rows, cols), dtype, pad)
+    dyt.copy_(dy)
+    dg, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    ops.layer_norm_backward(dyt, src, gamma, None if from_ckpt else mean, rstd, dx, dg, db)
+    ops.sync()
+    gap_kept(dx, pad)
+    u = dyd * gamma.double()
+    device_close(dx, rstd.double()[:, None] * (u - u.mean(1, keepdim=True) - h * (u * h).mean(1, keepdim=True)), TOL[dtype])
+    # at most rows / 8 + 64 additions one after the other, and h is a few
+    # roundings off
+    n = 2.0 ** -24 * (rows / 8 + 64)
+    bound = n * (dyd * h).abs().sum(0) + 2.0 ** -22 * (dyd.abs() * (h.abs() + 1)).sum(0)
+    assert ((dg.double() - (dyd * h).sum(0)).abs() <= bound).all()
+    assert ((db.double() - dyd.sum(0)).abs() <= n * dyd.abs().sum(0)).all()
+    again = torch.empty_like(dx)
+    ops.layer_norm_backward(dyt, src, gamma, None if from_ckpt else mean, rstd, again, dg.clone(), db.clone())
+    assert torch.equal(again, dx)
+
+
+# whole tiles for every pair of CTAs and more tokens than one accumulator
+# takes: the running partial in the workspace is written and read back
+@pytest.mark.parametrize("affine, accumulate", [(False, False), (True, False), (True, True), (False, True)])
+@pytest.mark.parametrize("rows, cols, n, pad", [(2304, 2560, 2304, 0), (2433, 2816, 2200, 0), (2304, 2560, 2303, 1), (8192, 2560, 2048, 0),
+                                                (4200, 5003, 2050, 2)])
+def test_weight_grad_of_many_tokens(ops, rows, cols, n, pad, affine, accumulate):  # noqa: F811
+    x, _ = device_rows(rows, rows, cols, F32)
+    ck, h = Checkpoint(rows, cols), torch.empty((rows, cols), device="cuda")
+    ops.checkpoint_save(x, ck)
+    ops.checkpoint_load(ck, h)
+    dy, dyd = device_rows(rows + 1, rows, n, BF16, 0.1)
+    dyt, dw, db = empty((rows, n), BF16, pad), empty((cols, n), F32, pad), torch.empty(n, device="cuda")
+    dyt.copy_(dy)
+    old, _ = device_rows(5, cols, n, F32)
+    dw.copy_(old)
+    more = {"db": db}
+    hd = h.double()
+    if affine:
+        more |= {"gamma": vec(normal(1, cols) * 0.1 + 1), "beta": vec(normal(2, cols) * 0.1)}
+        hd = hd * more["gamma"].double() + more["beta"].double()
+    db.fill_(3.0)
+    ops.weight_grad(ck, dyt, dw, accumulate=accumulate, **more)
+    ops.sync()
+    gap_kept(dw, pad)
+    ref = hd.t() @ dyd
+    err = dw.double() - ref
+    if accumulate:
+        err -= old.double()
+    # every addition is off by 2^-23 of its partial sum at most
+    size = hd.abs().t() @ dyd.abs() + (old.double().abs() if accumulate else 0)
+    assert (err.abs() <= 2.0 ** -23 * (rows + 8) * size).all()
+    # the tensor core truncates as it adds, so an accumulator's error grows with
+    # its additions: 2.8e-6 of the norm for 8192 tokens in one, a quarter of that
+    # for the 2048 that one takes.  Half way: 1.4e-6 (and the addition to dw)
+    norm = ref.norm() + (0.1 * old.double().norm() if accumulate else 0)
+    assert err.norm() <= 1.4e-6 * norm, (err.norm() / norm).item()
+    want = dyd.sum(0) + (3.0 if accumulate else 0)
+    assert ((db.double() - want).abs() <= 2.0 ** -24 * (rows / 8 + 64) * (dyd.abs().sum(0) + 3)).all()
+    kept, keptb = dw.clone(), db.clone()
+    dw.copy_(old)
+    db.fill_(3.0)
+    ops.weight_grad(ck, dyt, dw, accumulate=accumulate, **more)
+    assert torch.equal(dw, kept) and torch.equal(db, keptb)
