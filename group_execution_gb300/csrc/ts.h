@@ -33,7 +33,7 @@ struct TsOut {
   int elem() const { return bf16 ? 2 : 4; }
 };
 
-// Whether every row starts on 16 bytes (one row: its start alone).
+// Whether every row starts on 16 bytes (the pitch of a single row counts too).
 inline bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 template <class M>
 inline bool rows_aligned(const M& m) {
@@ -56,10 +56,6 @@ inline TsCkpt ckpt_view(void* buf, int64_t rows, int64_t cols) {
   c.scale = buf ? static_cast<uint8_t*>(buf) + rows * c.pitch : nullptr;
   return c;
 }
-
-// Opts a kernel in to `bytes` of dynamic shared memory (once per kernel and
-// device for the largest size asked for so far).
-cudaError_t opt_in_smem(const void* kernel, int bytes);
 
 struct NormArgs {
   TsMat x, dy;

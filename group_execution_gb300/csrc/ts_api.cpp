@@ -2,12 +2,9 @@
 // checks, the handle with its workspace and error word, and the launches.
 #include <cuda_runtime.h>
 
-#include <map>
 #include <memory>
-#include <mutex>
 #include <new>
 #include <string>
-#include <utility>
 
 #include "groupexec.h"
 #include "host.h"
@@ -74,22 +71,6 @@ TsMat mat(const void* p, int dtype, int64_t ld) { return TsMat{p, dtype == FG_BF
 TsOut out(void* p, int dtype, int64_t ld) { return TsOut{p, dtype == FG_BF16, ld}; }
 
 }  // namespace
-
-namespace fg {
-cudaError_t opt_in_smem(const void* kernel, int bytes) {
-  static std::mutex mu;
-  static std::map<std::pair<int, const void*>, int> done;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> g(mu);
-  int& have = done[{dev, kernel}];
-  if (have >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess) have = bytes;
-  return e;
-}
-}  // namespace fg
 
 #define TS_TRY(x) \
   if (fg_status s_ = (x)) return s_
