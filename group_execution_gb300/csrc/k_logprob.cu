@@ -219,8 +219,8 @@ __device__ __forceinline__ void note_sample(LpShared<W>& sh, unsigned long long 
 // 4096 x 50001 bf16 (rows at odd elements) takes 106 us with k = 20, 92 with
 // k = 8 and 74 with k = 0, where the logits' bytes at the copy rate take 60;
 // 2048 x 65536 f32 with k = 20 takes 95 of 79.  Instruction issue bounds the
-// bf16 rows: 86 instructions to a warp's 32 chunks, 16.8 thousand a row with k =
-// 0 (77 % of the issue slots), 25.4 thousand with k = 20 (81 %), by the noting
+// bf16 rows: 87 instructions to a warp's 32 chunks, 17.0 thousand a row with k =
+// 0 (77 % of the issue slots), 25.5 thousand with k = 20 (81 %), by the noting
 // and by a row's end, where the bound, two selections and the second reading
 // are chains of latency too.  Other forms of that end, at k = 20: k passes over
 // the row 3407 us, a selection by counting 210, a block's ninth warp that
@@ -532,7 +532,9 @@ cudaError_t logprob_rows(const ts_ops& h, const LogprobArgs& a, cudaStream_t st)
   return logprob_launch<T, U, 8, 5>(a, a.rows, 1, st);
 }
 
-// One row's constants: dlogits = p (a - w log p) plus g at the token.
+// One row's constants: dlogits = p (a - w log p) plus g at the token.  p is 2 to
+// the rounded (x - lse) log2(e): off by 2^-22 of itself and |log p| 2^-23 more
+// (2.4e-6 at p = e^-20), which a sum over a row's gradient does not see.
 struct RowGrad {
   float lse, a, w, g;
   int tok;      // -1: the row is not scored

@@ -245,14 +245,17 @@ __device__ __forceinline__ float warp_sums(const float (&s)[2 * K], int lane) {
 // every row, so gamma (G = 1) and both column sums stay in its registers; at
 // the end the block adds its slots in order and writes one partial.
 //
-// Bound by instruction issue before memory in bf16 (eight columns a lane and
-// row: two loads, one store and about 100 other instructions), so pairs of
-// float32 operations go in one instruction and addresses advance by addition.
-// 8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 64 in f32 (92 %); G
-// = 2 at 4096 x 8192 bf16 takes 48 and f32 72 (84 with the choice of stores).  (A partial written by single elements,
-// 32 bytes apart across a warp, cost 3 to 7 us.)  1021 x 5003 f32 from the
-// checkpoint, whose rows of dy and dx start at odd elements and move by single
-// ones, takes 21 us (33 %).  About 4 us of each is the kernel that adds the partials.
+// Bound by latency before memory in bf16: a warp's 152 instructions for 256
+// columns of a row (pairs of float32 operations in one, addresses advanced by
+// addition) keep the schedulers busy in 46 % of the cycles, and the SM's 16
+// warps wait for shuffles, shared memory, loads and the barrier of each pair of
+// rows.  8192 x 4096 takes 44 us in bf16 (67 % of the copy rate), 64 in f32 (92
+// %); G = 2 at 4096 x 8192 bf16 takes 48 and f32 72 (84 with the choice of
+// stores).  (A partial written by single elements, 32 bytes apart across a warp,
+// cost 3 to 7 us.)  1021 x 5003 f32 from the checkpoint, whose rows of dy and dx
+// start at odd elements and move by single ones, and whose second group of
+// columns most warps lack, takes 21 us (32 %).  About 4 us of each is the kernel
+// that adds the partials.
 template <class TDY, class Src, bool VEC, int G, int D, int K>
 __global__ void __launch_bounds__(512, 1) ts_norm_backward_kernel(const NormArgs a, int W, float* part) {
   __shared__ float red[2][16][4];   // [warp][value]

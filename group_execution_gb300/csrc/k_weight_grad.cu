@@ -20,10 +20,11 @@
 //   warps 12-27 the checkpoint: two groups of eight that take turns by slot,
 //               64 tokens to each half: 16-byte loads of int8 values, a slot
 //               ahead, expanded to bf16, scaled and stored swizzled.
-// At 8192 x 4096 x 4096 this runs at 1335 TFLOP/s (69 % of the burst rate of
-// a plain bf16 product, 78 % of its sustained rate): the expansion's stores,
-// the copies' writes and the MMA's reads fill the 1024 cycles of
-// shared memory that a slot's MMAs take.  What was measured on the way (us a
+// At 8192 x 4096 x 4096 this takes 210 us, 1309 TFLOP/s (68 % of the burst rate
+// of a plain bf16 product, 76 % of its sustained rate; 224 us when it runs for
+// 100 ms on end): the expansion's stores, the copies' writes and the MMA's reads
+// fill the 1024 cycles of shared memory that a slot's MMAs take.  dY's column
+// sums, where asked for, are a pass of their own before it, 15 to 20 us.  What was measured on the way (us a
 // call, and cycles of the issuing warp): a slot's wait, commit and first MMA
 // cost about 600 cycles beside the MMAs, so slots hold 128 tokens; an arrival
 // that releases to the cluster costs about 2000 (626 us), so arrivals release
@@ -348,8 +349,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (P.beta) {
         // dy's column sums of this warp's columns, fetched during the products
         // (chunk by chunk in the epilogue they took 13 x 3720 x 1880 from 14
-        // to 19 us and 512 x 4096 x 4096 from 38 to 45; at 8192 tokens, bound
-        // by shared memory, this way costs 4 us of 230)
+        // to 19 us and 512 x 4096 x 4096 from 38 to 45; the product of 8192
+        // tokens, bound by shared memory, was 207 us that way and is 211 this
+        // way, without beta too)
 #pragma unroll
         for (int k = 0; k < kTile / 2; k += 32) {
           const int at = n0 + (warp >= 8 ? kTile / 2 : 0) + k + lane;
