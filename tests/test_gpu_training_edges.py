@@ -8,7 +8,8 @@ torch = pytest.importorskip("torch")
 
 from group_execution_gb300 import Checkpoint, TrainingOps, _lib
 from oracle import training as OT
-from tests.test_gpu_training import BF16, F32, TOL, close, dev, empty, gap_kept, host, normal, ops, refused, rounded, vec, within  # noqa: F401, E501
+from tests.test_gpu_training import (BF16, F32, TOL, close, dev, empty, gap_kept, host, normal, ops,  # noqa: F401
+                                     refused, rounded, vec, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -54,7 +55,8 @@ def test_layer_norm_backward_in_place(ops, rows, cols, pad, dtype, from_ckpt):  
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("rows, cols, pad", [(1, 1, 0), (5, 257, 1), (700, 1000, 8), (300, 4096, 0)])
 def test_activation_backward_in_place(ops, op, dtype, rows, cols, pad):  # noqa: F811
-    a = {"relu": lambda v: np.maximum(v, 0), "sigmoid": lambda v: 1 / (1 + np.exp(-v)), "tanh": np.tanh}[op](normal(cols, rows, cols))
+    f = {"relu": lambda v: np.maximum(v, 0), "sigmoid": lambda v: 1 / (1 + np.exp(-v)), "tanh": np.tanh}[op]
+    a = f(normal(cols, rows, cols))
     b = OT.checkpoint_encode(a)
     dy = rounded(normal(cols + 1, rows, cols), dtype)
     t = empty((rows, cols), dtype, pad)
@@ -69,13 +71,13 @@ def test_in_place_needs_the_same_type_and_pitch(ops):  # noqa: F811
     x = torch.zeros((64, 64), device="cuda")
     as_bf16, narrow = x.view(BF16)[:32, :32], x[:32, :32]
     wide = torch.as_strided(x, (32, 32), (128, 1))
-    s = torch.zeros(32, device="cuda")
+    s, t = torch.zeros(32, device="cuda"), torch.zeros(32, dtype=torch.int64, device="cuda")
     ck, E = Checkpoint(32, 32, torch.zeros(32 * 132, dtype=torch.uint8, device="cuda")), _lib.FG_EINVAL
     for y in (as_bf16, wide):
         refused(E, ops.layer_norm, narrow, None, None, y, s, s)
         refused(E, ops.layer_norm_backward, y, ck, None, None, s, narrow, None, None)
         refused(E, ops.activation_backward, "tanh", narrow, ck, y)
-        refused(E, ops.token_logprobs_backward, narrow, torch.zeros(32, dtype=torch.int64, device="cuda"), s, None, s, None, y)
+        refused(E, ops.token_logprobs_backward, narrow, t, s, None, s, None, y)
     # a single row has no pitch; the same rows are fine
     ops.layer_norm(narrow[:1], None, None, wide[:1], None, None)
     ops.activation_backward("tanh", narrow, ck, narrow)
@@ -166,7 +168,8 @@ def test_top_logits_of_rising_rows(ops, rows, vocab, k):  # noqa: F811
 @pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("cols", [40, 17000])
 def test_layer_norm_backward_from_an_empty_checkpoint(ops, cols, dtype, accumulate):  # noqa: F811
-    dy, dx, s = torch.empty((0, cols), dtype=dtype, device="cuda"), torch.empty((0, cols), dtype=dtype, device="cuda"), vec([])
+    dy, s = torch.empty((0, cols), dtype=dtype, device="cuda"), vec([])
+    dx = dy.clone()
     dg, db = torch.full((cols,), 5.0, device="cuda"), torch.full((cols,), 6.0, device="cuda")
     ops.layer_norm_backward(dy, Checkpoint(0, cols), None, None, s, dx, dg, db, accumulate=accumulate)
     ops.sync()
@@ -178,7 +181,8 @@ def test_layer_norm_backward_from_an_empty_checkpoint(ops, cols, dtype, accumula
 
 # one tile; pieces of tiles; whole tiles of two accumulations; rows of dy that
 # go through a copy
-@pytest.mark.parametrize("rows, cols, n, pad", [(300, 200, 144, 0), (3000, 600, 700, 8), (2300, 2560, 2304, 0), (1000, 333, 777, 5)])
+@pytest.mark.parametrize("rows, cols, n, pad", [(300, 200, 144, 0), (3000, 600, 700, 8), (2300, 2560, 2304, 0),
+                                                (1000, 333, 777, 5)])
 def test_weight_grad_reports_an_expired_wait(rows, cols, n, pad):
     # no copy is ever issued, so every wait runs out after 1 ms: the kernel
     # gives its tensor memory back and returns, the handle reports it once, and
@@ -231,8 +235,8 @@ def device_close(got, ref, tol):
 # row (8, 16 and 16 warps; a warp to a row), an even and an odd number of them
 @pytest.mark.parametrize("pad", [0, 3])
 @pytest.mark.parametrize("xt, yt", [(F32, F32), (F32, BF16), (BF16, BF16)])
-@pytest.mark.parametrize("rows, cols", [(9001, 520), (7000, 1024), (3001, 2048), (2000, 4096), (1501, 5003), (1000, 8192),
-                                        (701, 16384), (700, 12000)])
+@pytest.mark.parametrize("rows, cols", [(9001, 520), (7000, 1024), (3001, 2048), (2000, 4096), (1501, 5003),
+                                        (1000, 8192), (701, 16384), (700, 12000)])
 def test_layer_norm_of_many_rows(ops, rows, cols, xt, yt, pad):  # noqa: F811
     x, xd = device_rows(cols, rows, cols, xt, 1.5, 0.4)
     src, y = empty((rows, cols), xt, pad), empty((rows, cols), yt, pad)
@@ -255,7 +259,8 @@ def test_layer_norm_of_many_rows(ops, rows, cols, xt, yt, pad):  # noqa: F811
     top = torch.nn.functional.pad(h.abs(), (0, -cols % 32)).unflatten(1, (-1, 32)).amax(2)
     step = torch.exp2(torch.floor(torch.log2(top * (1 + 1e-5))) - 6).repeat_interleave(32, 1)[:, :cols]
     # half a step, a whole one for what 127 steps do not reach, and h's error
-    assert ((back.double() - h).abs() <= torch.where(h.abs() > 127 * step, step, step / 2) + 2e-5 * h.abs().clamp(min=1)).all()
+    bound = torch.where(h.abs() > 127 * step, step, step / 2) + 2e-5 * h.abs().clamp(min=1)
+    assert ((back.double() - h).abs() <= bound).all()
 
 
 # W = 4, 8, 16 warps a row and G = 2, 32 warps, with even and odd numbers of
@@ -263,8 +268,8 @@ def test_layer_norm_of_many_rows(ops, rows, cols, xt, yt, pad):  # noqa: F811
 @pytest.mark.parametrize("from_ckpt", [False, True])
 @pytest.mark.parametrize("pad", [0, 3])
 @pytest.mark.parametrize("dtype", [F32, BF16])
-@pytest.mark.parametrize("rows, cols", [(3001, 1000), (2600, 1024), (1900, 2048), (1001, 2048), (1000, 4096), (609, 4000),
-                                        (760, 5003), (457, 8192), (700, 12000)])
+@pytest.mark.parametrize("rows, cols", [(3001, 1000), (2600, 1024), (1900, 2048), (1001, 2048), (1000, 4096),
+                                        (609, 4000), (760, 5003), (457, 8192), (700, 12000)])
 def test_layer_norm_backward_of_many_rows(ops, rows, cols, dtype, pad, from_ckpt):  # noqa: F811
     x, xd = device_rows(cols, rows, cols, dtype, 1.5, 0.4)
     dy, dyd = device_rows(cols + 1, rows, cols, dtype)
@@ -288,7 +293,8 @@ def test_layer_norm_backward_of_many_rows(ops, rows, cols, dtype, pad, from_ckpt
     ops.sync()
     gap_kept(dx, pad)
     u = dyd * gamma.double()
-    device_close(dx, rstd.double()[:, None] * (u - u.mean(1, keepdim=True) - h * (u * h).mean(1, keepdim=True)), TOL[dtype])
+    ref = rstd.double()[:, None] * (u - u.mean(1, keepdim=True) - h * (u * h).mean(1, keepdim=True))
+    device_close(dx, ref, TOL[dtype])
     # at most rows / 8 + 64 additions one after the other, and h is a few
     # roundings off
     n = 2.0 ** -24 * (rows / 8 + 64)
@@ -303,8 +309,8 @@ def test_layer_norm_backward_of_many_rows(ops, rows, cols, dtype, pad, from_ckpt
 # whole tiles for every pair of CTAs and more tokens than one accumulator
 # takes: the running partial in the workspace is written and read back
 @pytest.mark.parametrize("affine, accumulate", [(False, False), (True, False), (True, True), (False, True)])
-@pytest.mark.parametrize("rows, cols, n, pad", [(2304, 2560, 2304, 0), (2433, 2816, 2200, 0), (2304, 2560, 2303, 1), (8192, 2560, 2048, 0),
-                                                (4200, 5003, 2050, 2)])
+@pytest.mark.parametrize("rows, cols, n, pad", [(2304, 2560, 2304, 0), (2433, 2816, 2200, 0), (2304, 2560, 2303, 1),
+                                                (8192, 2560, 2048, 0), (4200, 5003, 2050, 2)])
 def test_weight_grad_of_many_tokens(ops, rows, cols, n, pad, affine, accumulate):  # noqa: F811
     x, _ = device_rows(rows, rows, cols, F32)
     ck, h = Checkpoint(rows, cols), torch.empty((rows, cols), device="cuda")

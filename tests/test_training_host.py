@@ -14,7 +14,8 @@ class OnDevice:
     def __init__(self, shape, dtype=torch.float32, device=0):
         self.t, self.device = torch.empty(shape, dtype=dtype), device
         self.shape, self.dtype = self.t.shape, dtype
-        self.stride, self.data_ptr, self.is_contiguous, self.numel = self.t.stride, self.t.data_ptr, self.t.is_contiguous, self.t.numel
+        self.stride, self.data_ptr = self.t.stride, self.t.data_ptr
+        self.is_contiguous, self.numel = self.t.is_contiguous, self.t.numel
 
     def get_device(self):
         return self.device
