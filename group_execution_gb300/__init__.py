@@ -7,8 +7,9 @@ A thin Python layer over libgroupexec.so (C ABI in include/groupexec.h):
                 (``launch_group``) or per operator (``launch_unfused``);
 * ``TensorFusion`` -- pack many float32 gradients into one bf16 fusion buffer
                 and unpack them again, one kernel each;
-* ``TrainingOps`` -- layer norm, 8-bit activation checkpoints (``Checkpoint``)
-                and token log probabilities, with their gradients.
+* ``TrainingOps`` -- layer norm, 8-bit activation checkpoints (``Checkpoint``),
+                token log probabilities, the embedding of tokens and the
+                cross entropy of a linear layer, with their gradients.
 
 PyTorch supplies device memory and streams only; every step runs in the
 library's kernels.  There is no CPU fallback.
@@ -21,12 +22,13 @@ from . import _lib
 from ._lib import FgError, OPCODES, EXEC_KINDS, FG_F32, FG_BF16  # noqa: F401
 
 __all__ = ["Graph", "Plan", "Partition", "TensorFusion", "FgError", "OPCODES", "graph_from_spec", "plan_threshold",
-           "merge_buckets", "simulate", "TrainingOps", "Checkpoint", "checkpoint_layout"]
+           "merge_buckets", "simulate", "TrainingOps", "Checkpoint", "checkpoint_layout",
+           "linear_cross_entropy_workspace"]
 
 
 def __getattr__(name):
     # loaded on first use: the rest of the package imports without PyTorch
-    if name in ("TrainingOps", "Checkpoint", "checkpoint_layout"):
+    if name in ("TrainingOps", "Checkpoint", "checkpoint_layout", "linear_cross_entropy_workspace"):
         from . import training
         value = globals()[name] = getattr(training, name)
         return value

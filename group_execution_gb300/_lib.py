@@ -105,6 +105,12 @@ SIGNATURES = {
     "ts_weight_grad": (_I32, [_P, _P, _I64, _I64, _P, _P, _P, _I32, _I64, _I64, _P, _I64, _P, _I32, _P]),
     "ts_token_logprobs": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _P]),
     "ts_token_logprobs_backward": (_I32, [_P, _P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _I32, _I64, _P]),
+    "ts_embedding": (_I32, [_P, _P, _I64, _P, _I32, _I64, _I64, _I64, _F, _P, _I32, _I64, _P]),
+    "ts_embedding_backward": (_I32, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _F, _P, _I32, _I64, _I32, _P]),
+    "ts_linear_cross_entropy_workspace": (_I32, [_I64, _I64, _I64, _PI64, _PI64]),
+    "ts_linear_cross_entropy": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "ts_linear_cross_entropy_backward": (_I32, [_P, _P, _I64, _P, _I64, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P,
+                                                _I32, _I64, _P, _I32, _I64, _I32, _P]),
 }
 
 _lock = threading.Lock()

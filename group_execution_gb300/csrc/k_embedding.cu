@@ -1,0 +1,596 @@
+// Embedding of tokens, y_t = scale * table[id_t], and the table's gradient,
+// dtable_v = scale * sum of dy_t over the tokens t with id_t = v.
+//
+// The lookup is bound by memory: a warp takes 256 columns of a token's row at
+// a time, four such pieces in flight where there are enough of them.
+//
+// The gradient sums in token order, so that it is the same every time and no
+// atomics touch a sum: the tokens are sorted by id (a stable radix sort, up to
+// 9 bits a pass), and the sorted list is cut into chunks of equal length,
+// however often a token occurs.  A warp sums one chunk's rows over 256 columns
+// in registers and writes each id's row once.  An id whose tokens lie in more
+// than one chunk leaves a float32 partial in the workspace for each, which a
+// second kernel adds in order.  Rows of the table that no token uses are zeroed
+// by other blocks of the same launch, which look them up in the sorted list.
+#include <algorithm>
+
+#include "launch.h"
+#include "ts_device.cuh"
+
+namespace fg {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+// ---- lookup -------------------------------------------------------------------
+
+struct EmbedKernel {
+  const int64_t* ids;
+  const void* table;
+  void* y;
+  int64_t rows, vocab, ldt, ldy, units;
+  int cols, packs;   // a unit is GROUPS groups of columns of one token, `packs` of them a token
+  float scale;
+};
+
+template <class T, class U, bool VEC, int GROUPS>
+__global__ void __launch_bounds__(kThreads) ts_embed_kernel(const __grid_constant__ EmbedKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= P.units) return;
+  const int64_t t = u / P.packs;
+  const int c0 = (int)(u - t * P.packs) * GROUPS * kGroupCols;
+  const int64_t id = P.ids[t];
+  const bool there = id >= 0 && id < P.vocab;
+  const T* src = static_cast<const T*>(P.table) + (there ? id : 0) * P.ldt;
+  U* dst = static_cast<U*>(P.y) + t * P.ldy;
+  RawGroup<T, VEC> raw[GROUPS];
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) raw[g].load(src, c0 + g * kGroupCols, there ? P.cols : 0, lane);
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    if (c0 + g * kGroupCols >= P.cols) break;
+    float v[8];
+    raw[g].get(v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = there ? v[j] * P.scale : 0.f;
+    store_group<VEC>(dst, c0 + g * kGroupCols, P.cols, lane, v);
+  }
+}
+
+// ---- tokens sorted by id ----------------------------------------------------------
+
+constexpr int kSortThreads = 1024, kSortWarps = 32;
+constexpr int kMaxBits = 9, kMaxBins = 1 << kMaxBits;
+constexpr int kSortAlone = 8192;   // tokens that one block sorts by itself
+constexpr int kTilePer = 4;        // 32-token rounds a warp of a tile of a longer list
+constexpr int kTile = kTilePer * kSortThreads;
+
+struct SortKernel {
+  const int64_t* ids;
+  int64_t vocab;
+  int rows, passes, bits;
+  // one pass over a longer list
+  const uint32_t* key_in;   // null: from the ids
+  const uint32_t* idx_in;
+  uint32_t* key;
+  uint32_t* idx;
+  uint32_t* counts;        // [tiles][bins] of this pass
+  uint32_t* next_counts;   // of the next one, or null
+  int shift, tiles;
+};
+
+// An id as a key: ids outside the table sort last.
+__device__ __forceinline__ uint32_t id_key(int64_t id, int64_t vocab) {
+  return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
+}
+
+// Exclusive sum of v over the block's threads; every thread takes part.
+__device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t s = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t n = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s += n;
+  }
+  if (lane == 31) warp_sums[warp] = s;
+  __syncthreads();
+  if (warp == 0) {
+    const uint32_t w = warp_sums[lane];
+    uint32_t x = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t n = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += n;
+    }
+    warp_sums[lane] = x - w;
+  }
+  __syncthreads();
+  return warp_sums[warp] + s - v;
+}
+
+// The ranks of a warp's `per` rounds of 32 keys among the warp's keys of the
+// same digit, in order, and the counts in hist[digit] (a row of this warp's
+// own).  Rounds past `n` keys take no part.
+template <int PER>
+__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[PER], int first, int n, int bins, uint32_t* hist,
+                                           uint32_t (&rank)[PER]) {
+  const int lane = threadIdx.x & 31;
+  for (int d = lane; d < bins; d += 32) hist[d] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < PER; ++r) {
+    if (first + r * 32 >= n) break;
+    const bool in = first + r * 32 + lane < n;
+    const uint32_t d = in ? digit[r] : 0xffffffffu;
+    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    const uint32_t base = in ? hist[d] : 0;
+    __syncwarp();
+    if (in && (peers & ((1u << lane) - 1)) == 0) hist[d] = base + __popc(peers);
+    __syncwarp();
+    rank[r] = base + __popc(peers & ((1u << lane) - 1));
+  }
+}
+// Turns the warps' counts of each digit into the sums of the warps before, and
+// returns the digit's total (thread d < bins).
+__device__ __forceinline__ uint32_t warp_offsets(uint32_t* hist, int bins) {
+  uint32_t sum = 0;
+  if ((int)threadIdx.x < bins) {
+#pragma unroll 8
+    for (int w = 0; w < kSortWarps; ++w) {
+      const uint32_t c = hist[w * kMaxBins + threadIdx.x];
+      hist[w * kMaxBins + threadIdx.x] = sum;
+      sum += c;
+    }
+  }
+  return sum;
+}
+
+// Up to kSortAlone tokens in one block: every pass between two halves of shared
+// memory, the last one to the workspace.
+constexpr int kAlonePer = kSortAlone / kSortThreads;
+constexpr int kAloneSmem = (kSortWarps * kMaxBins + kMaxBins + 32 + 4 * kSortAlone) * 4;
+
+__global__ void __launch_bounds__(kSortThreads, 1) ts_sort_alone_kernel(const __grid_constant__ SortKernel P) {
+  extern __shared__ uint32_t smem[];
+  uint32_t* hist = smem;
+  uint32_t* base = hist + kSortWarps * kMaxBins;
+  uint32_t* sums = base + kMaxBins;
+  uint32_t* buf = sums + 32;   // key, idx, key, idx
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
+  const int per = (P.rows + kSortThreads - 1) / kSortThreads, first = warp * per * 32;
+  // a warp's rounds follow each other in the list, so that ranks keep its order
+  uint32_t key[kAlonePer], idx[kAlonePer];
+#pragma unroll
+  for (int r = 0; r < kAlonePer; ++r) {
+    const int i = first + r * 32 + lane;
+    idx[r] = i;
+    key[r] = r < per && i < P.rows ? id_key(P.ids[i], P.vocab) : 0;
+  }
+  const int n = min(P.rows, first + per * 32);
+  for (int pass = 0; pass < P.passes; ++pass) {
+    uint32_t* out = buf + (pass & 1) * 2 * kSortAlone;
+    uint32_t digit[kAlonePer], rank[kAlonePer];
+#pragma unroll
+    for (int r = 0; r < kAlonePer; ++r) digit[r] = (key[r] >> (pass * P.bits)) & (bins - 1);
+    warp_ranks(digit, first, n, bins, hist + warp * kMaxBins, rank);
+    __syncthreads();
+    const uint32_t at = block_exclusive(warp_offsets(hist, bins), sums);
+    if ((int)threadIdx.x < bins) base[threadIdx.x] = at;
+    __syncthreads();
+    const bool last = pass + 1 == P.passes;
+#pragma unroll
+    for (int r = 0; r < kAlonePer; ++r) {
+      if (r < per && first + r * 32 + lane < n) {
+        const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
+        if (last) {
+          P.key[pos] = key[r];
+          P.idx[pos] = idx[r];
+        } else {
+          out[pos] = key[r];
+          out[kSortAlone + pos] = idx[r];
+        }
+      }
+    }
+    if (last) break;
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kAlonePer; ++r) {
+      const int i = first + r * 32 + lane;
+      if (r < per && i < n) {
+        key[r] = out[i];
+        idx[r] = out[kSortAlone + i];
+      }
+    }
+  }
+}
+
+// Longer lists: the first pass's counts by tile (the later passes' are made by
+// the pass before), and one pass.
+__global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __grid_constant__ SortKernel P) {
+  __shared__ uint32_t hist[kMaxBins];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int bins = 1 << P.bits;
+  if ((int)threadIdx.x < bins) hist[threadIdx.x] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kTilePer; ++r) {
+    const int64_t i = (int64_t)blockIdx.x * kTile + r * kSortThreads + threadIdx.x;
+    if (i < P.rows) atomicAdd(&hist[id_key(P.ids[i], P.vocab) & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < bins) {
+    P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
+    // the later passes' counts start at zero
+    for (int p = 1; p < P.passes; ++p)
+      P.counts[((int64_t)p * P.tiles + blockIdx.x) * bins + threadIdx.x] = 0;
+  }
+}
+
+__global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid_constant__ SortKernel P) {
+  extern __shared__ uint32_t smem[];
+  uint32_t* hist = smem;
+  uint32_t* base = hist + kSortWarps * kMaxBins;
+  uint32_t* sums = base + kMaxBins;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
+  const int tile0 = blockIdx.x * kTile, first = warp * kTilePer * 32;
+  const int n = min(P.rows - tile0, first + kTilePer * 32);
+  uint32_t key[kTilePer], idx[kTilePer], digit[kTilePer], rank[kTilePer];
+#pragma unroll
+  for (int r = 0; r < kTilePer; ++r) {
+    const int i = first + r * 32 + lane;
+    key[r] = idx[r] = 0;
+    if (i < n) {
+      key[r] = P.key_in ? P.key_in[tile0 + i] : id_key(P.ids[tile0 + i], P.vocab);
+      idx[r] = P.key_in ? P.idx_in[tile0 + i] : tile0 + i;
+    }
+    digit[r] = (key[r] >> P.shift) & (bins - 1);
+  }
+  warp_ranks(digit, first, n, bins, hist + warp * kMaxBins, rank);
+  __syncthreads();
+  warp_offsets(hist, bins);
+  uint32_t before = 0, total = 0;
+  if ((int)threadIdx.x < bins) {
+    const uint32_t* c = P.counts + threadIdx.x;
+#pragma unroll 8
+    for (int b = 0; b < P.tiles; ++b) {
+      const uint32_t v = c[(int64_t)b * bins];
+      total += v;
+      if (b < (int)blockIdx.x) before += v;
+    }
+  }
+  const uint32_t at = block_exclusive(total, sums);
+  if ((int)threadIdx.x < bins) base[threadIdx.x] = at + before;
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kTilePer; ++r) {
+    if (first + r * 32 + lane < n) {
+      const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
+      P.key[pos] = key[r];
+      P.idx[pos] = idx[r];
+      if (P.next_counts)
+        atomicAdd(&P.next_counts[(int64_t)(pos / kTile) * bins + ((key[r] >> (P.shift + P.bits)) & (bins - 1))], 1u);
+    }
+  }
+}
+
+// ---- sums of the sorted tokens' rows ------------------------------------------------
+
+struct EmbedBackKernel {
+  const uint32_t* key;   // sorted
+  const uint32_t* idx;
+  const void* dy;
+  void* d;
+  float* part;           // [chunks][2][part_cols]: a chunk's first id's, its last id's
+  int64_t lddy, ldd, part_cols, units, unit_blocks, vocab;
+  int rows, cols, groups, chunk, chunks;
+  float scale;
+};
+
+constexpr int kFillRows = 8;   // rows of the table a warp looks up at a time
+
+__device__ __forceinline__ float* part_at(const EmbedBackKernel& P, int chunk, int slot, int group, int lane) {
+  return P.part + ((int64_t)chunk * 2 + slot) * P.part_cols + group * kGroupCols + lane * 8;
+}
+
+// old + scale * sum, or scale * sum
+template <bool ACC>
+__device__ __forceinline__ void finish(float scale, const float (&acc)[8], const float (&old)[8], float (&v)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = ACC ? fmaf(scale, acc[j], old[j]) : scale * acc[j];
+}
+
+// T: dy's type, U: dtable's; ACC adds to what dtable holds.
+template <class T, class U, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_constant__ EmbedBackKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  U* d = static_cast<U*>(P.d);
+  if (blockIdx.x >= P.unit_blocks) {
+    // rows that no token uses
+    const int64_t r0 = ((int64_t)(blockIdx.x - P.unit_blocks) * kWarps + warp) * kFillRows;
+    const int64_t v = r0 + lane;
+    bool absent = lane < kFillRows && v < P.vocab;
+    if (absent) {
+      int lo = 0, hi = P.rows;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)P.key[mid] < v) lo = mid + 1;
+        else hi = mid;
+      }
+      absent = !(lo < P.rows && (int64_t)P.key[lo] == v);
+    }
+    const float zero[8] = {};
+    for (uint32_t m = __ballot_sync(0xffffffffu, absent); m; m &= m - 1) {
+      U* row = d + (r0 + __ffs(m) - 1) * P.ldd;
+      for (int c = 0; c < P.cols; c += kGroupCols) store_group<VEC>(row, c, P.cols, lane, zero);
+    }
+    return;
+  }
+  const int64_t u = (int64_t)blockIdx.x * kWarps + warp;
+  if (u >= P.units) return;
+  const int chunk = (int)(u / P.groups), group = (int)(u - (int64_t)chunk * P.groups), c0 = group * kGroupCols;
+  const int p0 = chunk * P.chunk, p1 = min(P.rows, p0 + P.chunk);
+  const T* dy = static_cast<const T*>(P.dy);
+  const uint32_t vocab = (uint32_t)P.vocab;
+  bool open = p0 > 0 && P.key[p0 - 1] == P.key[p0];   // the first id has tokens in the chunk before
+  float acc[8] = {};
+  constexpr int kU = ACC ? 4 : 8;   // rows in flight
+  for (int q = p0; q < p1; q += 32) {
+    const int at = q + lane;
+    const uint32_t k = at < p1 ? P.key[at] : vocab, ix = at < p1 ? P.idx[at] : 0;
+    const uint32_t next = at + 1 < P.rows && at < p1 ? P.key[at + 1] : 0xffffffffu;
+    const int n = min(32, p1 - q);
+    for (int j = 0; j < n; j += kU) {
+      RawGroup<T, VEC> raw[kU];
+      RawGroup<U, VEC> old[ACC ? kU : 1];
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const uint32_t ki = __shfl_sync(0xffffffffu, k, (j + i) & 31), xi = __shfl_sync(0xffffffffu, ix, (j + i) & 31);
+        const bool in = j + i < n && ki < vocab;
+        raw[i].load(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
+        if constexpr (ACC) {
+          const uint32_t ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
+          const bool ends = in && ni != ki;
+          old[i].load(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kU; ++i) {
+        const uint32_t ki = __shfl_sync(0xffffffffu, k, (j + i) & 31), ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
+        if (j + i >= n) break;
+        if (ki >= vocab) return;   // (padded places sort last)
+        float v[8];
+        raw[i].get(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] += v[e];
+        const bool ends = ni != ki;
+        if (!ends && q + j + i + 1 < p1) continue;
+        if (open || !ends) {
+          float* o = part_at(P, chunk, open ? 0 : 1, group, lane);
+          reinterpret_cast<float4*>(o)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+          float was[8] = {};
+          if constexpr (ACC) old[i].get(was);
+          finish<ACC>(P.scale, acc, was, v);
+          store_group<VEC>(d + (int64_t)ki * P.ldd, c0, P.cols, lane, v);
+        }
+        open = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+      }
+    }
+  }
+}
+
+// An id whose tokens begin in this warp's chunk and end in a later one.
+template <class U, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_constant__ EmbedBackKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= P.units) return;
+  const int chunk = (int)(u / P.groups), group = (int)(u - (int64_t)chunk * P.groups), c0 = group * kGroupCols;
+  const int64_t p0 = (int64_t)chunk * P.chunk, p1 = p0 + P.chunk;
+  if (p1 >= P.rows) return;
+  const uint32_t k = P.key[p1 - 1];
+  if (k >= (uint32_t)P.vocab || P.key[p1] != k) return;
+  if (p0 > 0 && P.key[p0 - 1] == k) return;   // it began before
+  U* row = static_cast<U*>(P.d) + (int64_t)k * P.ldd;
+  float acc[8], was[8] = {}, v[8];
+  load8(part_at(P, chunk, 1, group, lane), acc);
+  if constexpr (ACC) load_group<VEC>(row, c0, P.cols, lane, was);
+  for (int64_t e = chunk + 1;; e += 32) {
+    // lane i: whether the id goes on past chunk e + i
+    const int64_t after = (e + lane + 1) * P.chunk;
+    const uint32_t stops = __ballot_sync(0xffffffffu, !(after < P.rows && P.key[after] == k));
+    const int n = stops ? __ffs(stops) : 32;
+    for (int j = 0; j < n; j += 4) {
+      float x[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j + i < n) load8(part_at(P, (int)e + j + i, 0, group, lane), x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (j + i < n) {
+#pragma unroll
+          for (int m = 0; m < 8; ++m) acc[m] += x[i][m];
+        }
+      }
+    }
+    if (stops) break;
+  }
+  finish<ACC>(P.scale, acc, was, v);
+  store_group<VEC>(row, c0, P.cols, lane, v);
+}
+
+template <class K, class A>
+cudaError_t launch(K kernel, int64_t grid, int block, int smem, const A& args, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = pdl_config((int)grid, block, smem, st);
+  cudaLaunchAttribute at[1];
+  pdl_attr(cfg, at);
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+// Calls f with the types of two matrices and whether all their rows are on 16 bytes.
+template <class A, class B, class F>
+cudaError_t by_type(const A& a, const B& b, F f) {
+  const bool vec = rows_aligned(a) && rows_aligned(b);
+  auto second = [&](auto x) {
+    using X = decltype(x);
+    if (b.bf16) return vec ? f(X(), __nv_bfloat16(), std::true_type()) : f(X(), __nv_bfloat16(), std::false_type());
+    return vec ? f(X(), float(), std::true_type()) : f(X(), float(), std::false_type());
+  };
+  return a.bf16 ? second(__nv_bfloat16()) : second(float());
+}
+
+constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+
+}  // namespace
+
+cudaError_t launch_embedding(const ts_ops& h, const EmbedArgs& a, cudaStream_t st) {
+  EmbedKernel P = {};
+  P.ids = a.ids;
+  P.table = a.table.p;
+  P.y = a.y.p;
+  P.rows = a.rows;
+  P.vocab = a.vocab;
+  P.ldt = a.table.ld;
+  P.ldy = a.y.ld;
+  P.cols = a.cols;
+  P.scale = a.scale;
+  const int groups = (a.cols + kGroupCols - 1) / kGroupCols;
+  // four pieces a warp, once that leaves every SM a few warps
+  const int pack = a.rows * groups >= (int64_t)h.nsm * 64 && groups >= 4 ? 4 : 1;
+  P.packs = (groups + pack - 1) / pack;
+  P.units = a.rows * P.packs;
+  const int64_t grid = (P.units + kWarps - 1) / kWarps;
+  if (grid > kMaxGrid) return cudaErrorInvalidConfiguration;
+  return by_type(a.table, a.y, [&](auto t, auto u, auto vec) {
+    using T = decltype(t);
+    using U = decltype(u);
+    constexpr bool V = decltype(vec)::value;
+    return launch(pack == 4 ? ts_embed_kernel<T, U, V, 4> : ts_embed_kernel<T, U, V, 1>, grid, kThreads, 0, P, st);
+  });
+}
+
+// The workspace of a sorted list of `rows` tokens, with the counts of a list
+// that more than one block sorts.
+namespace {
+struct SortPlan {
+  int passes, bits, tiles;
+  int64_t counts_bytes, bytes;
+};
+SortPlan sort_plan(int64_t rows, int64_t vocab) {
+  SortPlan s = {};
+  int key_bits = 1;
+  while (key_bits < 32 && (vocab >> key_bits)) ++key_bits;   // (the key of a padded place is `vocab`)
+  s.passes = (key_bits + kMaxBits - 1) / kMaxBits;
+  s.bits = (key_bits + s.passes - 1) / s.passes;
+  s.tiles = (int)((rows + kTile - 1) / kTile);
+  const bool alone = rows <= kSortAlone;
+  s.counts_bytes = alone ? 0 : ((int64_t)s.passes * s.tiles << s.bits) * 4;
+  s.bytes = (rows * 4 + 255) / 256 * 256 * (alone ? 2 : 4) + (s.counts_bytes + 255) / 256 * 256;
+  return s;
+}
+}  // namespace
+
+int64_t embedding_backward_workspace(int64_t rows, int64_t vocab) { return sort_plan(rows, vocab).bytes; }
+
+cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaStream_t st) {
+  EmbedBackKernel P = {};
+  const SortPlan s = sort_plan(a.rows, a.vocab);
+  cudaError_t e = cudaSuccess;
+  if (a.rows > 0) {
+    const int64_t list = (a.rows * 4 + 255) / 256 * 256;
+    uint32_t* at[4];
+    for (int i = 0; i < 4; ++i) at[i] = reinterpret_cast<uint32_t*>(h.ws + i * list);
+    SortKernel S = {};
+    S.ids = a.ids;
+    S.vocab = a.vocab;
+    S.rows = (int)a.rows;
+    S.passes = s.passes;
+    S.bits = s.bits;
+    S.tiles = s.tiles;
+    S.key = at[0];
+    S.idx = at[1];
+    if (a.rows <= kSortAlone) {
+      e = cudaFuncSetAttribute(ts_sort_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAloneSmem);
+      if (e != cudaSuccess) return e;
+      e = launch(ts_sort_alone_kernel, 1, kSortThreads, kAloneSmem, S, st);
+    } else {
+      constexpr int smem = (kSortWarps * kMaxBins + kMaxBins + 32) * 4;
+      uint32_t* counts = reinterpret_cast<uint32_t*>(h.ws + 4 * list);
+      e = cudaFuncSetAttribute(ts_sort_pass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      S.counts = counts;
+      e = launch(ts_sort_count_kernel, s.tiles, kSortThreads, 0, S, st);
+      for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
+        // the last pass ends in the first list
+        const int out = (s.passes - 1 - p) & 1 ? 2 : 0;
+        S.key = at[out];
+        S.idx = at[out + 1];
+        S.key_in = p ? at[2 - out] : nullptr;
+        S.idx_in = p ? at[3 - out] : nullptr;
+        S.shift = p * s.bits;
+        S.counts = counts + ((int64_t)p * s.tiles << s.bits);
+        S.next_counts = p + 1 < s.passes ? counts + ((int64_t)(p + 1) * s.tiles << s.bits) : nullptr;
+        e = launch(ts_sort_pass_kernel, s.tiles, kSortThreads, smem, S, st);
+      }
+    }
+    if (e != cudaSuccess) return e;
+    P.key = at[0];
+    P.idx = at[1];
+  }
+  P.dy = a.dy.p;
+  P.d = a.d.p;
+  P.lddy = a.dy.ld;
+  P.ldd = a.d.ld;
+  P.vocab = a.vocab;
+  P.rows = (int)a.rows;
+  P.cols = a.cols;
+  P.scale = a.scale;
+  P.groups = (a.cols + kGroupCols - 1) / kGroupCols;
+  P.part_cols = (int64_t)P.groups * kGroupCols;
+  P.part = reinterpret_cast<float*>(h.ws + s.bytes);
+  if (a.rows > 0) {
+    // as many chunks as give every SM some warps, of 4 to 32 tokens, and as the
+    // workspace has room for partials
+    const int64_t want = a.rows * P.groups / ((int64_t)h.nsm * 16);
+    const int64_t room = (h.ws_bytes - s.bytes) / (P.part_cols * 8);
+    P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
+    if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))
+      P.chunk = room < 2 ? (int)a.rows : (int)((a.rows + room - 1) / room);
+    P.chunks = (int)((a.rows + P.chunk - 1) / P.chunk);
+    P.units = (int64_t)P.chunks * P.groups;
+    P.unit_blocks = (P.units + kWarps - 1) / kWarps;
+  }
+  const int64_t fill = a.accumulate ? 0 : (a.vocab + kWarps * kFillRows - 1) / (kWarps * kFillRows);
+  if (P.unit_blocks + fill > kMaxGrid) return cudaErrorInvalidConfiguration;
+  if (P.unit_blocks + fill == 0) return cudaSuccess;
+  return by_type(a.dy, a.d, [&](auto t, auto u, auto vec) {
+    using T = decltype(t);
+    using U = decltype(u);
+    constexpr bool V = decltype(vec)::value;
+    cudaError_t e = launch(a.accumulate ? ts_embed_sum_kernel<T, U, V, true> : ts_embed_sum_kernel<T, U, V, false>,
+                           P.unit_blocks + fill, kThreads, 0, P, st);
+    if (e != cudaSuccess || P.chunks < 2) return e;
+    return launch(a.accumulate ? ts_embed_join_kernel<U, V, true> : ts_embed_join_kernel<U, V, false>, P.unit_blocks,
+                  kThreads, 0, P, st);
+  });
+}
+
+}  // namespace fg

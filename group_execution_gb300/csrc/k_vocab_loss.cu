@@ -1,0 +1,974 @@
+// Softmax cross entropy of a linear layer over a vocabulary, l = x w^T, and its
+// gradients, in pieces of the vocabulary: the logits [rows, vocab] are never
+// kept.
+//
+//   lse_t = log sum_v exp l_tv, loss_t = lse_t - l_t,target
+//   d_tv = (g_t + h_t) exp(l_tv - lse_t) - g_t [v = target_t]
+//   dx = d w, dw = d^T x
+//
+// Everything large is a product on the 5th-generation tensor cores.  Forward:
+// one product whose epilogue reduces each row of a tile's 128 columns to a
+// maximum and a sum of exponentials (8 bytes for 128 logits), which a small
+// kernel joins.  Backward, for each piece of the vocabulary: the logits again,
+// turned by the epilogue into d, rounded to bf16 (the tensor cores' operand) in
+// the workspace; then, in one launch, the piece's dw and its part of dx, which
+// float32 sums in the workspace collect.
+//
+// The product kernel is persistent: CTA pairs walk 256 x 256 tiles (2-SM
+// tcgen05.mma, cta_group::2), K 128 at a time; each CTA stages half of the
+// tile's rows of A and half of its columns of B in a ring of shared-memory
+// slots (128-byte swizzled TMA boxes of 64 x 128 elements, whichever way the
+// operand lies).  Warps, in each CTA:
+//   warp 0      TMA producer of the A half,
+//   warp 1      allocates TMEM (two accumulators) and, in the even CTA, issues
+//               the MMAs from one thread,
+//   warp 2      TMA producer of the B half,
+//   warps 4-11  epilogue: a thread owns half of one row of the CTA's 128 x 256
+//               accumulator; it overlaps the next tile's MMAs.
+//
+// Every wait is bounded; on expiry the CTA records the error, the pair waits
+// for the copies that either CTA has in flight, frees its TMEM and returns.
+#include <cuda.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "launch.h"
+#include "ts_device.cuh"
+
+namespace fg {
+namespace {
+
+constexpr int kTile = 256;                       // rows and columns of a pair's tile
+constexpr int kHalf = kTile / 2;                 // ... and one CTA stages of each operand
+constexpr int kKB = 128;                         // of K in a ring slot
+constexpr int kBoxBytes = 64 * kHalf * 2;        // one TMA box
+constexpr int kOperandBytes = 2 * kBoxBytes;     // 32 KB
+constexpr int kSlotBytes = 2 * kOperandBytes;
+constexpr int kSlots = 3;
+constexpr int kStageBytes = 32 * 128;            // an epilogue warp's rows on their way out
+constexpr int kThreads = 12 * 32;
+constexpr int kSmem = kSlots * kSlotBytes + 8 * kStageBytes + 1024;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+enum Mode { kLoss, kDlogits, kGrad };
+
+struct VocabKernel {
+  CUtensorMap x, w, d;       // loads: x [rows, cols], w's piece [vocab, cols], d [rows, dpitch]
+  CUtensorMap store_d;       // d, in boxes of 64 x 32
+  CUtensorMap store_dx;      // dx's sums [splits, rows, cols] float32
+  CUtensorMap store_dw;      // dw's piece
+  int rows, cols, vocab;     // vocab: of the piece
+  int v0;                    // its first row of w
+  int64_t total;             // the whole vocabulary's size
+  int tiles_t, tiles_v, tiles_c;
+  // forward
+  float2* part;              // [128-column parts][rows]: reference (log2) and sum
+  float* tlogit;             // the target's logit
+  const int64_t* targets;
+  // backward
+  const float* lse;
+  const float* g_loss;
+  const float* g_lse;
+  int splits;                // of dx's K
+  int nx, nw, late, extra;   // dx and dw items; see item_of
+  int add_dx;                // the piece adds to dx's sums
+  int dw_kind;               // 0 bf16 by TMA, 1 float32 by TMA, 2 by threads
+  int dw_bf16, accumulate;
+  void* dw;
+  int64_t lddw;
+  int32_t* err;
+  int64_t wait_limit_ns;
+  int inject;
+};
+
+// What a pair works on: a tile at (m0, n0) of a product, over blocks [kb0, kb1)
+// of kKB.
+struct Item {
+  int kind;   // 0 logits, 1 dx, 2 dw, -1 none
+  int m0, n0, kb0, kb1, K, split;
+};
+
+constexpr int kRowGroup = 16;   // row tiles that walk the vocabulary together (their rows of x stay in L2)
+
+template <int MODE>
+__device__ __forceinline__ Item item_of(const VocabKernel& P, int pair, int npair, int k) {
+  Item w = {};
+  if constexpr (MODE != kGrad) {
+    const int64_t x = pair + (int64_t)k * npair;
+    if (x >= (int64_t)P.tiles_t * P.tiles_v) return Item{-1};
+    const int per = kRowGroup * P.tiles_v, g = (int)(x / per), r = (int)(x - (int64_t)g * per);
+    const int gm = min(kRowGroup, P.tiles_t - g * kRowGroup);
+    w.m0 = (g * kRowGroup + r % gm) * kTile;
+    w.n0 = r / gm * kTile;
+    w.K = P.cols;
+    w.kb1 = (P.cols + kKB - 1) / kKB;
+    return w;
+  } else {
+    // dx's long items first, one after the other over all pairs; where their
+    // last round leaves pairs free, those take `extra` items of dw before the
+    // others join them
+    const int mine = pair < P.nx ? (P.nx - pair + npair - 1) / npair : 0;
+    if (k < mine) {
+      const int x = pair + k * npair, per = P.tiles_t * P.tiles_c, r = x % per;
+      w.kind = 1;
+      w.split = x / per;
+      w.m0 = r / P.tiles_c * kTile;
+      w.n0 = r % P.tiles_c * kTile;
+      const int nkb = (P.vocab + kKB - 1) / kKB;
+      w.kb0 = (int)((int64_t)nkb * w.split / P.splits);
+      w.kb1 = (int)((int64_t)nkb * (w.split + 1) / P.splits);
+      w.K = P.vocab;
+      return w;
+    }
+    const int j = k - mine, early = npair - P.late;
+    int x;
+    if (pair >= P.late && j < P.extra) x = pair - P.late + j * early;
+    else x = P.extra * early + pair + (pair >= P.late ? j - P.extra : j) * npair;
+    if (x >= P.nw) return Item{-1};
+    w.kind = 2;
+    w.m0 = x / P.tiles_c * kTile;
+    w.n0 = x % P.tiles_c * kTile;
+    w.kb1 = (P.rows + kKB - 1) / kKB;
+    w.K = P.rows;
+    return w;
+  }
+}
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int64_t limit, volatile int* abort_flag) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait(bar, parity))
+    if (*abort_flag || (int64_t)(global_ns() - t0) > limit) return false;
+  return true;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ float exp2_approx(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(z), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int x, int y, uint32_t src) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(m)),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+
+// An epilogue warp's 32 rows x 128 bytes on their way out, 128-byte swizzled.
+struct Stage {
+  uint8_t* p;
+  __device__ __forceinline__ void put(int row, int chunk, uint4 v) const {
+    *reinterpret_cast<uint4*>(p + row * 128 + ((chunk ^ (row & 7)) << 4)) = v;
+  }
+  // Column `col` (float32) of a row.
+  __device__ __forceinline__ float get(int row, int col) const {
+    return *reinterpret_cast<const float*>(p + row * 128 + (((col >> 2) ^ (row & 7)) << 4) + (col & 3) * 4);
+  }
+  // 32 float32 columns
+  __device__ __forceinline__ void put_f32(int row, const float (&v)[32]) const {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      put(row, c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
+                             __float_as_uint(v[4 * c + 3])));
+  }
+  // 32 columns in bf16, the first or second half of the 128 bytes
+  __device__ __forceinline__ void put_bf16(int row, int half, const float (&v)[32]) const {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      put(row, half * 4 + c, make_uint4(bf16x2(v[8 * c], v[8 * c + 1]), bf16x2(v[8 * c + 2], v[8 * c + 3]),
+                                        bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7])));
+  }
+};
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    ts_vocab_kernel(const __grid_constant__ VocabKernel P) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 5];
+  __shared__ int abort_flag, issued[2];         // slots that either producer has issued copies for
+  __shared__ int peer_gave_up, peer_issued;     // written by the pair's other CTA
+  __shared__ uint32_t tmem_slot;
+  uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
+                 tempty0 = tfull0 + 16, done_bar = tempty0 + 16;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (int)cluster_ctarank();
+  const bool leader = h == 0;
+  const uint16_t pair_mask = 3u;
+  const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
+  if (threadIdx.x == 0) {
+    abort_flag = issued[0] = issued[1] = 0;
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(full0 + 8 * s, 1);   // the even CTA's expect_tx
+      mbar_init(empty0 + 8 * s, 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(tfull0 + 8 * b, 1);
+      mbar_init(tempty0 + 8 * b, 16);   // the epilogue warps of the pair
+    }
+    mbar_init(done_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // the peer's barriers are initialised before any remote arrival
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  pdl_launch_dependents();
+  pdl_wait();
+
+  if (warp == 0 || warp == 2) {
+    // ---- operand producers ----
+    if (lane == 0 && !P.inject) {
+      const bool isA = warp == 0;
+      const uint64_t keep = l2_evict_last();
+      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + (isA ? 0 : kOperandBytes);
+      int it = 0, s = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        const Item w = item_of<MODE>(P, pair, npair, k);
+        if (w.kind < 0) break;
+        // an operand lies K-major (columns are K) or MN-major (rows are K)
+        const CUtensorMap* map;
+        bool mn;
+        if constexpr (MODE == kGrad) {
+          map = isA ? &P.d : w.kind == 1 ? &P.w : &P.x;
+          mn = !isA || w.kind == 2;
+        } else {
+          map = isA ? &P.x : &P.w;
+          mn = false;
+        }
+        const int o = (isA ? w.m0 : w.n0) + h * kHalf;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, P.wait_limit_ns, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (leader && isA) mbar_expect_tx(full0 + 8 * s, 2 * kSlotBytes);
+          const uint32_t dst = dst0 + s * kSlotBytes, cbar = cbar0 + 8 * s;
+          tma_load_2d_pair(dst, map, mn ? o : kb * kKB, mn ? kb * kKB : o, cbar, keep);
+          tma_load_2d_pair(dst + kBoxBytes, map, (mn ? o : kb * kKB) + 64, mn ? kb * kKB : o, cbar, keep);
+          ++it;
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+      }
+      issued[isA ? 0 : 1] = it;
+      if (!ok) {
+        abort_flag = 1;
+        set_error(P.err, DEVERR_TIMEOUT);
+      }
+    }
+  } else if (warp == 1) {
+    // ---- MMA issuer ----
+    if (lane == 0 && leader) {
+      const uint32_t base = smem_u32(ring);
+      int s = 0, i = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (; ok; ++i) {
+        const Item w = item_of<MODE>(P, pair, npair, i);
+        if (w.kind < 0) break;
+        const int b = i & 1;
+        if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, P.wait_limit_ns, &abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // MN-major: atoms of 64 columns x 8 of K, the second 64 columns one box
+        // on, 16 of K 2 KB on.  K-major: atoms of 8 rows x 64 of K, 16 of K 32
+        // bytes on, the second 64 of K one box on.
+        const bool a_mn = MODE == kGrad && w.kind == 2, b_mn = MODE == kGrad;
+        const uint32_t idesc = idesc_bf16_f32(kTile, kTile, a_mn, b_mn);
+        const uint64_t ad0 = smem_desc_sw128(base, a_mn ? kBoxBytes : 16, 1024),
+                       bd0 = smem_desc_sw128(base + kOperandBytes, b_mn ? kBoxBytes : 16, 1024);
+        const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
+        const uint32_t a_half = (a_mn ? 4 * 2048 : kBoxBytes) >> 4, b_half = (b_mn ? 4 * 2048 : kBoxBytes) >> 4;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (!wait_bar(full0 + 8 * s, ph, P.wait_limit_ns, &abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t so = (uint32_t)(s * kSlotBytes) >> 4;
+          const int left = w.K - kb * kKB;   // (past K both operands are zeros)
+#pragma unroll
+          for (int kk = 0; kk < kKB / 16; ++kk) {
+            if (kk * 16 >= left) break;
+            tc_mma_bf16<2>(tmem + b * kTile, ad0 + so + (kk >> 2) * a_half + (kk & 3) * a_step,
+                           bd0 + so + (kk >> 2) * b_half + (kk & 3) * b_step, idesc, kb != w.kb0 || kk != 0);
+          }
+          tc_commit_mask(empty0 + 8 * s, pair_mask);
+          if (++s == kSlots) {
+            s = 0;
+            ph ^= 1;
+          }
+        }
+        if (ok) tc_commit_mask(tfull0 + 8 * b, pair_mask);
+      }
+      if (!ok) {
+        abort_flag = 1;
+        set_error(P.err, DEVERR_TIMEOUT);
+      }
+      // every MMA issued has completed before either CTA may free TMEM
+      tc_commit_mask(done_bar, pair_mask);
+      mbar_wait(done_bar, 0, kDrainLimitNs);
+    }
+  } else if (warp >= 4) {
+    // ---- epilogue ----
+    const int q = warp & 3, set = (warp - 4) >> 2;   // the TMEM lane quarter this warp may access, its column half
+    const Stage stage = {ring + kSlots * kSlotBytes + (warp - 4) * kStageBytes};
+    const uint32_t stage_u32 = smem_u32(stage.p);
+    bool ok = true;
+    for (int i = 0;; ++i) {
+      const Item w = item_of<MODE>(P, pair, npair, i);
+      if (w.kind < 0) break;
+      const int b = i & 1, r0 = w.m0 + h * kHalf + q * 32, row = r0 + lane;
+      const int c0 = w.n0 + set * kHalf;   // this warp's first column
+      float lse2 = 0.f, coef = 0.f, g = 0.f;
+      int target = -1;   // the target's column of the piece
+      if constexpr (MODE != kGrad) {
+        if (row < P.rows) {
+          const int64_t t = P.targets ? P.targets[row] : -1;
+          target = t >= P.v0 && t < (int64_t)P.v0 + P.vocab ? (int)(t - P.v0) : -1;
+          if constexpr (MODE == kDlogits) {
+            // (a row of -inf logits takes no gradient)
+            const float l = P.lse[row];
+            const bool none = l == -INFINITY;
+            lse2 = none ? 0.f : l * kLog2e;
+            g = t >= 0 && t < P.total && !none ? P.g_loss[row] : 0.f;
+            coef = g + (P.g_lse && !none ? P.g_lse[row] : 0.f);
+          }
+        }
+      }
+      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, P.wait_limit_ns, &abort_flag));
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * kTile + set * kHalf;
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+      };
+      // before the stage is written again, its last store has read it
+      auto stage_free = [&]() {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+      };
+      auto stage_full = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      if constexpr (MODE == kLoss) {
+        // the sums' reference is the largest logit so far, in log2
+        float m2 = -INFINITY, sum = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < kHalf; j += 32) {
+          float v[32];
+          tmem_ld32(acc + j, v);
+          if (j + 32 == kHalf) release();
+          const int left = P.vocab - c0 - j;   // columns of the vocabulary from here on
+          if (left <= 0) continue;
+          const int at = target - c0 - j;
+          if (at >= 0 && at < 32) {
+            float l = 0.f;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) l = c == at ? v[c] : l;
+            P.tlogit[row] = l;
+          }
+          if (left < 32) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= left) v[c] = -INFINITY;
+          }
+          float top = v[0];
+#pragma unroll
+          for (int c = 1; c < 32; ++c) top = fmaxf(top, v[c]);
+          const float next = fmaxf(m2, top * kLog2e);
+          const float ref = next == -INFINITY ? 0.f : next;
+          float s[4] = {};
+#pragma unroll
+          for (int c = 0; c < 32; ++c) s[c & 3] += exp2_approx(fmaf(v[c], kLog2e, -ref));
+          sum = sum * exp2_approx(m2 - ref) + ((s[0] + s[1]) + (s[2] + s[3]));
+          m2 = next;
+        }
+        if (row < P.rows && c0 < P.vocab)
+          P.part[(int64_t)(c0 / kHalf) * P.rows + row] = make_float2(m2, sum);
+      } else if constexpr (MODE == kDlogits) {
+#pragma unroll 1
+        for (int j = 0; j < kHalf; j += 64) {
+          stage_free();
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float v[32];
+            tmem_ld32(acc + j + 32 * k, v);
+            if (j + 64 == kHalf && k == 1) release();
+            const int cc = c0 + j + 32 * k, left = P.vocab - cc, at = target - cc;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = coef * exp2_approx(fmaf(v[c], kLog2e, -lse2));
+            if (at >= 0 && at < 32) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] -= c == at ? g : 0.f;
+            }
+            if (left < 32 || coef == 0.f) {
+              // past the vocabulary, and in rows without a gradient whatever their logits
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c >= left || (coef == 0.f && g == 0.f)) v[c] = 0.f;
+            }
+            stage.put_bf16(lane, k, v);
+          }
+          stage_full();
+          if (lane == 0) {
+            if (r0 < P.rows) tma_store_2d(&P.store_d, c0 + j, r0, stage_u32);
+            bulk_commit();
+          }
+        }
+      } else {
+        const bool dx = w.kind == 1;
+        const int m_end = dx ? P.rows : P.vocab;
+        if (!dx && P.dw_kind == 0) {
+#pragma unroll 1
+          for (int j = 0; j < kHalf; j += 64) {
+            stage_free();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float v[32];
+              tmem_ld32(acc + j + 32 * k, v);
+              if (j + 64 == kHalf && k == 1) release();
+              stage.put_bf16(lane, k, v);
+            }
+            stage_full();
+            if (lane == 0) {
+              if (r0 < m_end && c0 + j < P.cols) tma_store_2d(&P.store_dw, c0 + j, r0, stage_u32);
+              bulk_commit();
+            }
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < kHalf; j += 32) {
+            stage_free();
+            float v[32];
+            tmem_ld32(acc + j, v);
+            if (j + 32 == kHalf) release();
+            if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = 0.f;
+            }
+            stage.put_f32(lane, v);
+            if (dx || P.dw_kind == 1) {
+              stage_full();
+              if (lane == 0) {
+                if (r0 < m_end && c0 + j < P.cols) {
+                  if (!dx) {
+                    if (P.accumulate) tma_add_2d(&P.store_dw, c0 + j, r0, stage_u32);
+                    else tma_store_2d(&P.store_dw, c0 + j, r0, stage_u32);
+                  } else {
+                    if (P.add_dx) tma_add_3d(&P.store_dx, c0 + j, r0, w.split, stage_u32);
+                    else tma_store_3d(&P.store_dx, c0 + j, r0, w.split, stage_u32);
+                  }
+                }
+                bulk_commit();
+              }
+            } else {
+              // rows of dw that TMA cannot write, or that bf16 values are added to
+              __syncwarp();
+              const int col = c0 + j + lane, n = col < P.cols ? min(32, P.vocab - r0) : 0;
+              for (int r = 0; r < n; ++r) {
+                const int64_t at = (int64_t)(r0 + r) * P.lddw + col;
+                const float x = stage.get(r, lane);
+                if (P.dw_bf16) {
+                  __nv_bfloat16* d = static_cast<__nv_bfloat16*>(P.dw) + at;
+                  *d = __float2bfloat16_rn(P.accumulate ? __bfloat162float(*d) + x : x);
+                } else {
+                  float* d = static_cast<float*>(P.dw) + at;
+                  *d = P.accumulate ? *d + x : x;
+                }
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) {
+      abort_flag = 1;
+      set_error(P.err, DEVERR_TIMEOUT);
+    }
+    if (lane == 0) bulk_wait<0>();   // the stores issued here have completed
+  }
+  tc_fence_before();
+  __syncthreads();
+  const int mine = issued[0] > issued[1] ? issued[0] : issued[1];
+  if (threadIdx.x == 0) {
+    st_cluster(cluster_addr(smem_u32(&peer_gave_up), h ^ 1), abort_flag);
+    st_cluster(cluster_addr(smem_u32(&peer_issued), h ^ 1), mine);
+  }
+  __syncwarp();
+  // no CTA leaves while its peer may still write to its shared memory or
+  // issue MMAs into its TMEM
+  cluster_sync();
+  if (abort_flag || peer_gave_up) {   // (the same in both CTAs)
+    // either CTA's copies in flight complete on the even CTA's barriers; the
+    // slots they fill may lack copies, so each wait may run to its limit
+    if (leader && threadIdx.x == 0) {
+      const int last = mine > peer_issued ? mine : peer_issued;
+      for (int k = last - kSlots < 0 ? 0 : last - kSlots; k < last; ++k)
+        mbar_wait(full0 + 8 * (k % kSlots), (k / kSlots) & 1, kDrainLimitNs);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc<2>(tmem, 512);
+}
+
+// ---- small kernels ------------------------------------------------------------------
+
+struct JoinKernel {
+  const float2* part;
+  const float* tlogit;
+  const int64_t* targets;
+  float* loss;
+  float* lse;
+  int64_t vocab;
+  int rows, parts;
+};
+
+// The parts of 32 rows: lane = row, eight warps share the parts.
+__global__ void __launch_bounds__(256) ts_loss_join_kernel(const __grid_constant__ JoinKernel P) {
+  __shared__ float2 sm[8][32];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * 32 + lane;
+  float m = -INFINITY, s = 0.f;
+  auto add = [&](float2 v) {
+    const float next = fmaxf(m, v.x), ref = next == -INFINITY ? 0.f : next;
+    s = s * exp2_approx(m - ref) + v.y * exp2_approx(v.x - ref);
+    m = next;
+  };
+  if (row < P.rows) {
+    int p = warp;
+    for (; p + 24 < P.parts; p += 32) {
+      float2 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = P.part[(int64_t)(p + 8 * k) * P.rows + row];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) add(v[k]);
+    }
+    for (; p < P.parts; p += 8) add(P.part[(int64_t)p * P.rows + row]);
+  }
+  sm[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp || row >= P.rows) return;
+  for (int k = 1; k < 8; ++k) add(sm[k][lane]);
+  // the reference is a rounded log2, the sum relative to it as rounded
+  const float lse = s == 0.f ? -INFINITY : (m + log2f(s)) * kLn2;
+  if (P.lse) P.lse[row] = lse;
+  if (P.loss) {
+    const int64_t t = P.targets[row];
+    P.loss[row] = t < 0 || t >= P.vocab ? 0.f : lse == -INFINITY ? INFINITY : lse - P.tlogit[row];
+  }
+}
+
+struct RepackKernel {
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;
+  int64_t ld, pitch, rows, vocab, units;
+  int cols, groups;
+  const int64_t* targets;   // if not null, rows without a target are zeros
+  const float* lse;         // if not null, rows whose lse is -inf are zeros
+};
+
+// bf16 rows at a pitch that TMA can read.  A row that takes no gradient has d = 0,
+// and may hold anything: dw takes it as zeros.
+template <bool VEC>
+__global__ void __launch_bounds__(256) ts_loss_repack_kernel(const __grid_constant__ RepackKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (u >= P.units) return;
+  const int64_t r = u / P.groups;
+  const int c0 = (int)(u - r * P.groups) * kGroupCols;
+  bool keep = true;
+  if (P.targets) {
+    const int64_t t = P.targets[r];
+    keep = t >= 0 && t < P.vocab;
+  }
+  if (P.lse && P.lse[r] == -INFINITY) keep = false;
+  __nv_bfloat16* dst = P.dst + r * P.pitch;
+  RawGroup<__nv_bfloat16, VEC> raw;
+  raw.load(P.src + r * P.ld, c0, keep ? P.cols : 0, lane);
+  if constexpr (VEC) {
+    if (c0 + lane * 8 < P.pitch) *reinterpret_cast<uint4*>(dst + c0 + lane * 8) = raw.q[0];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (c0 + j * 32 + lane < P.pitch) dst[c0 + j * 32 + lane] = raw.e[j];
+  }
+}
+
+struct DxKernel {
+  const float* sums;   // [splits][rows][pitch]
+  void* dx;
+  int64_t pitch, rows, ld, units;
+  int cols, groups, splits;
+};
+
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) ts_loss_dx_kernel(const __grid_constant__ DxKernel P) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  if (u >= P.units) return;
+  const int64_t r = u / P.groups;
+  const int c0 = (int)(u - r * P.groups) * kGroupCols;
+  float v[8];
+  load_group<VEC>(P.sums + r * P.pitch, c0, P.cols, lane, v);
+  for (int s = 1; s < P.splits; ++s) {
+    float x[8];
+    load_group<VEC>(P.sums + ((int64_t)s * P.rows + r) * P.pitch, c0, P.cols, lane, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += x[j];
+  }
+  store_group<VEC>(static_cast<T*>(P.dx) + r * P.ld, c0, P.cols, lane, v);
+}
+
+// dw of no rows
+template <class T>
+__global__ void __launch_bounds__(256) ts_loss_zero_kernel(T* dw, int64_t lddw, int vocab, int cols) {
+  pdl_launch_dependents();
+  pdl_wait();
+  for (int64_t v = blockIdx.x; v < vocab; v += gridDim.x)
+    for (int c = threadIdx.x; c < cols; c += 256) dw[v * lddw + c] = from_f32<T>(0.f);
+}
+
+// ---- host ----------------------------------------------------------------------------
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn encoder() {
+  static EncodeFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(p);
+  });
+  return fn;
+}
+
+// A map of a matrix, or (rank 3) of `depth` dense ones, with boxes of box_cols x
+// box_rows.
+cudaError_t make_map(CUtensorMap* m, const void* p, int bf16, int64_t cols, int64_t rows, int64_t ld, int box_cols,
+                     int box_rows, int rank = 2, int64_t depth = 1) {
+  EncodeFn enc = encoder();
+  if (!enc) return cudaErrorNotSupported;
+  const int size = bf16 ? 2 : 4;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)depth};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * size), (cuuint64_t)(ld * size * rows)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1}, es[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, rank,
+             const_cast<void*>(p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+// The pairs that run at once on the device; also opts in to the shared memory.
+cudaError_t resident_pairs(int device, int* out) {
+  static std::atomic<int> cached[64];
+  int n = device < 64 ? cached[device].load(std::memory_order_acquire) : 0;
+  if (!n) {
+    const void* kernels[3] = {(const void*)ts_vocab_kernel<kLoss>, (const void*)ts_vocab_kernel<kDlogits>,
+                              (const void*)ts_vocab_kernel<kGrad>};
+    for (const void* k : kernels) {
+      const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = pdl_config(2, kThreads, kSmem, nullptr);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, ts_vocab_kernel<kGrad>, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    if (device < 64) cached[device].store(n, std::memory_order_release);
+  }
+  *out = n;
+  return cudaSuccess;
+}
+
+template <class K, class A>
+cudaError_t launch(K kernel, int64_t grid, int block, int smem, const A& args, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = pdl_config((int)grid, block, smem, st);
+  cudaLaunchAttribute at[1];
+  pdl_attr(cfg, at);
+  return cudaLaunchKernelEx(&cfg, kernel, args);
+}
+
+int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
+int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
+int64_t pitch_of(int64_t cols) { return round_up(cols, 8); }
+
+// Copies rows of a bf16 matrix to dst at pitch_of(cols); see the kernel.
+cudaError_t repack(const TsMat& m, int64_t row0, int64_t rows, int cols, void* dst, const int64_t* targets,
+                   const float* lse, int64_t vocab, cudaStream_t st) {
+  RepackKernel R = {};
+  R.src = static_cast<const __nv_bfloat16*>(m.p) + row0 * m.ld;
+  R.dst = static_cast<__nv_bfloat16*>(dst);
+  R.ld = m.ld;
+  R.pitch = pitch_of(cols);
+  R.rows = rows;
+  R.vocab = vocab;
+  R.cols = cols;
+  R.groups = (cols + kGroupCols - 1) / kGroupCols;
+  R.units = rows * R.groups;
+  R.targets = targets;
+  R.lse = lse;
+  return launch(rows_aligned(m) ? ts_loss_repack_kernel<true> : ts_loss_repack_kernel<false>, (R.units + 7) / 8, 256, 0,
+                R, st);
+}
+
+// The forward pass's workspace for `rows` rows, its copy of w's rows aside.
+int64_t forward_bytes(int64_t rows, int64_t cols, int64_t vocab, bool copy_x) {
+  return (copy_x ? round_up(rows * pitch_of(cols) * 2, 256) : 0) + round_up(rows * 4, 256) +
+         round_up(rows * ((vocab + kHalf - 1) / kHalf) * 8, 256);
+}
+// The backward pass's, d's piece aside, and d's for 256 of the vocabulary.
+int64_t backward_bytes(int64_t rows, int64_t cols, int64_t splits) {
+  return round_up(rows * pitch_of(cols) * 2, 256) + round_up(splits * rows * pitch_of(cols) * 4, 256);
+}
+int64_t piece_bytes(int64_t rows, int64_t cols, bool copy_w) {
+  return kTile * (rows + (copy_w ? pitch_of(cols) : 0)) * 2;
+}
+
+}  // namespace
+
+int64_t vocab_loss_workspace(int64_t rows, int64_t cols, int64_t vocab, bool copy_x, bool copy_w, bool backward,
+                             bool whole) {
+  if (backward)
+    return backward_bytes(rows, cols, 1) + (whole ? tiles(vocab) : 1) * piece_bytes(rows, cols, copy_w);
+  const int64_t r = whole ? rows : std::min<int64_t>(rows, kTile);
+  return forward_bytes(r, cols, vocab, copy_x) + (copy_w ? kTile * pitch_of(cols) * 2 : 0);
+}
+
+cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st) {
+  int pairs = 0;
+  cudaError_t e = resident_pairs(h.device, &pairs);
+  if (e != cudaSuccess) return e;
+  const bool copy_x = !rows_aligned(a.x), copy_w = !rows_aligned(a.w);
+  const int64_t pitch = pitch_of(a.cols), parts = (a.vocab + kHalf - 1) / kHalf;
+  // as many of w's rows at a time as a quarter of the workspace takes
+  int64_t piece = a.vocab, wbytes = 0;
+  if (copy_w) {
+    piece = std::min<int64_t>(tiles(a.vocab), std::max<int64_t>(1, h.ws_bytes / 4 / (kTile * pitch * 2))) * kTile;
+    wbytes = piece * pitch * 2;
+  }
+  // all rows, or as many as leave w's room
+  int64_t block = a.rows;
+  if (forward_bytes(block, a.cols, a.vocab, copy_x) + wbytes > h.ws_bytes) {
+    const int64_t each = forward_bytes(kTile, a.cols, a.vocab, copy_x);
+    block = (h.ws_bytes - wbytes) / each * kTile;
+    if (block < kTile) {   // (room for one tile of each was checked)
+      block = kTile;
+      piece = kTile;
+      wbytes = copy_w ? piece * pitch * 2 : 0;
+    }
+  }
+  uint8_t* wcopy = h.ws + h.ws_bytes - wbytes;
+  if (wbytes) wcopy = h.ws + (h.ws_bytes - wbytes) / 256 * 256;
+  for (int64_t t0 = 0; t0 < a.rows; t0 += block) {
+    const int64_t rows = std::min(block, a.rows - t0);
+    uint8_t* at = h.ws;
+    TsMat x = a.x;
+    x.p = static_cast<const __nv_bfloat16*>(a.x.p) + t0 * a.x.ld;
+    if (copy_x) {
+      e = repack(a.x, t0, rows, a.cols, at, nullptr, nullptr, 0, st);
+      if (e != cudaSuccess) return e;
+      x.p = at;
+      x.ld = pitch;
+      at += round_up(rows * pitch * 2, 256);
+    }
+    JoinKernel J = {};
+    J.tlogit = reinterpret_cast<float*>(at);
+    at += round_up(rows * 4, 256);
+    J.part = reinterpret_cast<float2*>(at);
+    J.targets = a.targets ? a.targets + t0 : nullptr;
+    J.loss = a.loss ? a.loss + t0 : nullptr;
+    J.lse = a.lse ? a.lse + t0 : nullptr;
+    J.vocab = a.vocab;
+    J.rows = (int)rows;
+    J.parts = (int)parts;
+    VocabKernel P = {};
+    P.rows = (int)rows;
+    P.cols = a.cols;
+    P.total = a.vocab;
+    P.tiles_t = (int)tiles(rows);
+    P.tlogit = const_cast<float*>(J.tlogit);
+    P.targets = a.loss ? J.targets : nullptr;
+    P.err = h.err;
+    P.wait_limit_ns = h.wait_limit_ns;
+    P.inject = h.inject;
+    e = make_map(&P.x, x.p, 1, a.cols, rows, x.ld, 64, kHalf);
+    if (e != cudaSuccess) return e;
+    for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
+      const int64_t nv = std::min(piece, a.vocab - v0);
+      TsMat w = a.w;
+      w.p = static_cast<const __nv_bfloat16*>(a.w.p) + v0 * a.w.ld;
+      if (copy_w) {
+        e = repack(a.w, v0, nv, a.cols, wcopy, nullptr, nullptr, 0, st);
+        if (e != cudaSuccess) return e;
+        w.p = wcopy;
+        w.ld = pitch;
+      }
+      e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
+      if (e != cudaSuccess) return e;
+      P.vocab = (int)nv;
+      P.v0 = (int)v0;
+      P.tiles_v = (int)tiles(nv);
+      P.part = const_cast<float2*>(J.part) + v0 / kHalf * rows;
+      const int64_t items = (int64_t)P.tiles_t * P.tiles_v;
+      e = launch(ts_vocab_kernel<kLoss>, 2 * std::min<int64_t>(pairs, items), kThreads, kSmem, P, st);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch(ts_loss_join_kernel, (rows + 31) / 32, 256, 0, J, st);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st) {
+  int pairs = 0;
+  cudaError_t e = resident_pairs(h.device, &pairs);
+  if (e != cudaSuccess) return e;
+  if (!a.dx.p && !a.dw.p) return cudaSuccess;
+  if (a.rows == 0) {
+    if (!a.dw.p || a.accumulate) return cudaSuccess;
+    cudaLaunchConfig_t cfg = pdl_config((int)std::min<int64_t>(a.vocab, 8 * h.nsm), 256, 0, st);
+    cudaLaunchAttribute at[1];
+    pdl_attr(cfg, at);
+    return a.dw.bf16 ? cudaLaunchKernelEx(&cfg, ts_loss_zero_kernel<__nv_bfloat16>,
+                                          static_cast<__nv_bfloat16*>(a.dw.p), a.dw.ld, (int)a.vocab, a.cols)
+                     : cudaLaunchKernelEx(&cfg, ts_loss_zero_kernel<float>, static_cast<float*>(a.dw.p), a.dw.ld,
+                                          (int)a.vocab, a.cols);
+  }
+  const bool copy_w = !rows_aligned(a.w);
+  const int64_t pitch = pitch_of(a.cols), tiles_t = tiles(a.rows), tiles_c = tiles(a.cols), tiles_v = tiles(a.vocab);
+  // dx of few rows is cut along the vocabulary, so that every pair has a part
+  const int64_t one_dx = a.rows * pitch * 4, cost = piece_bytes(a.rows, a.cols, copy_w);
+  int64_t splits = std::min<int64_t>(pairs / (tiles_t * tiles_c), tiles_v / 2);
+  splits = std::min<int64_t>(splits, (h.ws_bytes / 2 - round_up(a.rows * pitch * 2, 256)) / one_dx);
+  while (splits > 1 && backward_bytes(a.rows, a.cols, splits) + cost > h.ws_bytes) --splits;
+  splits = std::max<int64_t>(splits, 1);
+  // equal pieces of the vocabulary, as few as the workspace allows
+  const int64_t most = std::max<int64_t>(1, (h.ws_bytes - backward_bytes(a.rows, a.cols, splits)) / cost);
+  const int64_t pieces = (tiles_v + most - 1) / most, piece = (tiles_v + pieces - 1) / pieces * kTile;
+  __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(h.ws);
+  float* sums = reinterpret_cast<float*>(h.ws + round_up(a.rows * pitch * 2, 256));
+  uint8_t* d = h.ws + backward_bytes(a.rows, a.cols, splits);
+  uint8_t* wcopy = d + a.rows * piece * 2;
+  e = repack(a.x, 0, a.rows, a.cols, x, a.g_lse ? nullptr : a.targets, a.lse, a.vocab, st);
+  if (e != cudaSuccess) return e;
+  VocabKernel P = {};
+  P.rows = (int)a.rows;
+  P.cols = a.cols;
+  P.total = a.vocab;
+  P.tiles_t = (int)tiles_t;
+  P.tiles_c = (int)tiles_c;
+  P.targets = a.targets;
+  P.lse = a.lse;
+  P.g_loss = a.g_loss;
+  P.g_lse = a.g_lse;
+  P.splits = (int)splits;
+  P.accumulate = a.accumulate;
+  P.dw_bf16 = a.dw.bf16;
+  P.lddw = a.dw.ld;
+  P.dw_kind = !rows_aligned(a.dw) || (a.dw.bf16 && a.accumulate) ? 2 : a.dw.bf16 ? 0 : 1;
+  P.err = h.err;
+  P.wait_limit_ns = h.wait_limit_ns;
+  P.inject = h.inject;
+  e = make_map(&P.x, x, 1, a.cols, a.rows, pitch, 64, kHalf);
+  if (e == cudaSuccess) e = make_map(&P.store_dx, sums, 0, a.cols, a.rows, pitch, 32, 32, 3, splits);
+  for (int64_t v0 = 0; v0 < a.vocab && e == cudaSuccess; v0 += piece) {
+    const int64_t nv = std::min(piece, a.vocab - v0), dpitch = tiles(nv) * kTile;
+    TsMat w = a.w;
+    w.p = static_cast<const __nv_bfloat16*>(a.w.p) + v0 * a.w.ld;
+    if (copy_w) {
+      e = repack(a.w, v0, nv, a.cols, wcopy, nullptr, nullptr, 0, st);
+      if (e != cudaSuccess) return e;
+      w.p = wcopy;
+      w.ld = pitch;
+    }
+    P.vocab = (int)nv;
+    P.v0 = (int)v0;
+    P.tiles_v = (int)tiles(nv);
+    P.add_dx = v0 > 0;
+    e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
+    if (e == cudaSuccess) e = make_map(&P.d, d, 1, dpitch, a.rows, dpitch, 64, kHalf);
+    if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
+    if (a.dw.p) {
+      uint8_t* dw = static_cast<uint8_t*>(a.dw.p) + v0 * a.dw.ld * a.dw.elem();
+      P.dw = dw;
+      if (P.dw_kind < 2 && e == cudaSuccess)
+        e = make_map(&P.store_dw, dw, a.dw.bf16, a.cols, nv, a.dw.ld, a.dw.bf16 ? 64 : 32, 32);
+    }
+    if (e != cudaSuccess) return e;
+    e = launch(ts_vocab_kernel<kDlogits>, 2 * std::min<int64_t>(pairs, tiles_t * P.tiles_v), kThreads, kSmem, P, st);
+    if (e != cudaSuccess) return e;
+    P.nx = a.dx.p ? (int)(tiles_t * tiles_c * splits) : 0;
+    P.nw = a.dw.p ? (int)(P.tiles_v * tiles_c) : 0;
+    const int np = std::min(pairs, P.nx + P.nw);
+    // an item of dw takes at least about three blocks of K for its epilogue
+    const int64_t cost_x = (nv + kKB - 1) / kKB / splits, cost_w = std::max<int64_t>(3, (a.rows + kKB - 1) / kKB);
+    P.late = P.nx % np;
+    P.extra = P.late ? (int)((cost_x + cost_w / 2) / cost_w) : 0;
+    e = launch(ts_vocab_kernel<kGrad>, 2 * np, kThreads, kSmem, P, st);
+  }
+  if (e != cudaSuccess || !a.dx.p) return e;
+  DxKernel D = {};
+  D.sums = sums;
+  D.dx = a.dx.p;
+  D.pitch = pitch;
+  D.rows = a.rows;
+  D.ld = a.dx.ld;
+  D.cols = a.cols;
+  D.groups = (a.cols + kGroupCols - 1) / kGroupCols;
+  D.units = a.rows * D.groups;
+  D.splits = (int)splits;
+  const bool vec = rows_aligned(a.dx);
+  auto* kernel = a.dx.bf16 ? vec ? ts_loss_dx_kernel<__nv_bfloat16, true> : ts_loss_dx_kernel<__nv_bfloat16, false>
+                 : vec     ? ts_loss_dx_kernel<float, true>
+                           : ts_loss_dx_kernel<float, false>;
+  return launch(kernel, (D.units + 7) / 8, 256, 0, D, st);
+}
+
+}  // namespace fg

@@ -120,4 +120,40 @@ struct LogprobArgs {
 cudaError_t launch_token_logprobs(const ts_ops& h, const LogprobArgs& a, cudaStream_t st);
 cudaError_t launch_token_logprobs_backward(const ts_ops& h, const LogprobArgs& a, cudaStream_t st);
 
+
+// Embedding and its gradient (embedding_backward_workspace: the least that the
+// sorted tokens take).
+struct EmbedArgs {
+  const int64_t* ids = nullptr;
+  int64_t rows = 0, vocab = 0;
+  int cols = 0;
+  TsMat table, dy;
+  TsOut y, d;
+  float scale = 1.f;
+  int accumulate = 0;
+};
+cudaError_t launch_embedding(const ts_ops& h, const EmbedArgs& a, cudaStream_t st);
+int64_t embedding_backward_workspace(int64_t rows, int64_t vocab);
+cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaStream_t st);
+
+// Cross entropy of x w^T.  The workspace: the least that a pass takes, or what
+// the whole batch (forward) or vocabulary (backward) takes at once; copy_x and
+// copy_w: rows that TMA cannot read.
+struct VocabLossArgs {
+  TsMat x, w;
+  int64_t rows = 0, vocab = 0;
+  int cols = 0;
+  const int64_t* targets = nullptr;
+  float* loss = nullptr;
+  float* lse = nullptr;
+  const float* g_loss = nullptr;
+  const float* g_lse = nullptr;
+  TsOut dx, dw;
+  int accumulate = 0;
+};
+int64_t vocab_loss_workspace(int64_t rows, int64_t cols, int64_t vocab, bool copy_x, bool copy_w, bool backward,
+                             bool whole);
+cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st);
+cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st);
+
 }  // namespace fg

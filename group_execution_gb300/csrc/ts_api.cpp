@@ -13,6 +13,9 @@
 
 using namespace fg;
 
+#define TS_TRY(x) \
+  if (fg_status s_ = (x)) return s_
+
 namespace {
 
 fg_status err(fg_status st, const std::string& msg) { return (fg_status)set_last_error(st, msg.c_str()); }
@@ -67,13 +70,29 @@ fg_status check_in_place(const char* names, const void* out_p, int out_dtype, in
     return err(FG_EINVAL, std::string(names) + " needs the same dtype and row pitch");
   return FG_OK;
 }
+fg_status check_vocab(int64_t vocab) {
+  if (vocab < 1) return err(FG_ESHAPE, "the vocabulary must hold at least 1");
+  if (vocab > kMaxExtent) return err(FG_ESHAPE, "an extent is too large");
+  return FG_OK;
+}
+fg_status check_loss_extent(int64_t rows, int64_t cols, int64_t vocab) {
+  TS_TRY(check_extent(rows, cols));
+  TS_TRY(check_vocab(vocab));
+  constexpr int64_t most = int64_t(1) << 20;
+  if (rows > most || cols > most || vocab > most)
+    return err(FG_EUNSUPPORTED, "more than 2^20 rows, columns or vocabulary");
+  return FG_OK;
+}
+fg_status check_workspace(const ts_ops* h, int64_t needed) {
+  if (needed > h->ws_bytes)
+    return err(FG_EUNSUPPORTED, "the workspace holds " + std::to_string(h->ws_bytes) + " bytes, the call needs " +
+                                    std::to_string(needed));
+  return FG_OK;
+}
 TsMat mat(const void* p, int dtype, int64_t ld) { return TsMat{p, dtype == FG_BF16, ld}; }
 TsOut out(void* p, int dtype, int64_t ld) { return TsOut{p, dtype == FG_BF16, ld}; }
 
 }  // namespace
-
-#define TS_TRY(x) \
-  if (fg_status s_ = (x)) return s_
 
 extern "C" {
 
@@ -130,7 +149,7 @@ fg_status ts_sync_status(ts_ops* h, void* stream) {
   if (flag == 0) return FG_OK;
   e = cudaMemset(h->err, 0, sizeof(int32_t));
   if (e != cudaSuccess) return cuda_err(e, "clearing the device error word");
-  if (flag == DEVERR_TIMEOUT) return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad expired");
+  if (flag == DEVERR_TIMEOUT) return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad or ts_linear_cross_entropy expired");
   return err(FG_EDEVICE, "device error word " + std::to_string(flag));
 }
 
@@ -344,6 +363,121 @@ fg_status ts_token_logprobs_backward(ts_ops* h, const void* logits, fg_dtype dty
   a.dlogits = out(dlogits, d_dtype, ldd);
   return done(launch_token_logprobs_backward(*h, a, static_cast<cudaStream_t>(stream)),
               "ts_token_logprobs_backward launch");
+}
+
+fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* table, fg_dtype table_dtype,
+                       int64_t ld_table, int64_t vocab, int64_t cols, float scale, void* y, fg_dtype y_dtype,
+                       int64_t ldy, void* stream) {
+  TS_TRY(check_handle(h));
+  TS_TRY(check_extent(rows, cols));
+  TS_TRY(check_vocab(vocab));
+  TS_TRY(check_array("ids", ids, rows > 0, 8));
+  TS_TRY(check_matrix("table", table, table_dtype, ld_table, rows > 0 ? vocab : 0, cols));
+  TS_TRY(check_matrix("y", y, y_dtype, ldy, rows, cols));
+  if (rows == 0) return FG_OK;
+  EmbedArgs a;
+  a.ids = ids;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.cols = (int)cols;
+  a.table = mat(table, table_dtype, ld_table);
+  a.y = out(y, y_dtype, ldy);
+  a.scale = scale;
+  return done(launch_embedding(*h, a, static_cast<cudaStream_t>(stream)), "ts_embedding launch");
+}
+
+fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, fg_dtype dy_dtype, int64_t lddy,
+                                int64_t rows, int64_t vocab, int64_t cols, float scale, void* dtable,
+                                fg_dtype d_dtype, int64_t ldd, int32_t accumulate, void* stream) {
+  TS_TRY(check_handle(h));
+  TS_TRY(check_extent(rows, cols));
+  TS_TRY(check_vocab(vocab));
+  TS_TRY(check_array("ids", ids, rows > 0, 8));
+  TS_TRY(check_matrix("dy", dy, dy_dtype, lddy, rows, cols));
+  TS_TRY(check_matrix("dtable", dtable, d_dtype, ldd, vocab, cols));
+  TS_TRY(check_workspace(h, embedding_backward_workspace(rows, vocab)));
+  EmbedArgs a;
+  a.ids = ids;
+  a.rows = rows;
+  a.vocab = vocab;
+  a.cols = (int)cols;
+  a.dy = mat(dy, dy_dtype, lddy);
+  a.d = out(dtable, d_dtype, ldd);
+  a.scale = scale;
+  a.accumulate = accumulate != 0;
+  return done(launch_embedding_backward(*h, a, static_cast<cudaStream_t>(stream)), "ts_embedding_backward launch");
+}
+
+fg_status ts_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* least, int64_t* most) {
+  TS_TRY(check_loss_extent(rows, cols, vocab));
+  auto larger = [&](bool whole) {
+    const int64_t f = vocab_loss_workspace(rows, cols, vocab, true, true, false, whole),
+                  b = vocab_loss_workspace(rows, cols, vocab, true, true, true, whole);
+    return f > b ? f : b;
+  };
+  if (least) *least = larger(false);
+  if (most) *most = larger(true);
+  return FG_OK;
+}
+
+fg_status ts_linear_cross_entropy(ts_ops* h, const void* x, int64_t ldx, const void* w, int64_t ldw, fg_dtype dtype,
+                                  int64_t rows, int64_t cols, int64_t vocab, const int64_t* targets, float* loss,
+                                  float* lse, void* stream) {
+  TS_TRY(check_handle(h));
+  TS_TRY(check_loss_extent(rows, cols, vocab));
+  if (dtype != FG_BF16) return err(FG_EINVAL, "x and w must be bf16 (the tensor cores' operands)");
+  TS_TRY(check_matrix("x", x, dtype, ldx, rows, cols));
+  TS_TRY(check_matrix("w", w, dtype, ldw, rows > 0 ? vocab : 0, cols));
+  TS_TRY(check_array("targets", targets, rows > 0 && loss, 8));
+  TS_TRY(check_array("loss", loss, false));
+  TS_TRY(check_array("lse", lse, false));
+  if (rows == 0) return FG_OK;
+  VocabLossArgs a;
+  a.x = mat(x, dtype, ldx);
+  a.w = mat(w, dtype, ldw);
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.vocab = vocab;
+  a.targets = targets;
+  a.loss = loss;
+  a.lse = lse;
+  TS_TRY(check_workspace(h, vocab_loss_workspace(rows, cols, vocab, !rows_aligned(a.x), !rows_aligned(a.w), false,
+                                                 false)));
+  return done(launch_vocab_loss(*h, a, static_cast<cudaStream_t>(stream)), "ts_linear_cross_entropy launch");
+}
+
+fg_status ts_linear_cross_entropy_backward(ts_ops* h, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                           fg_dtype dtype, int64_t rows, int64_t cols, int64_t vocab,
+                                           const int64_t* targets, const float* lse, const float* g_loss,
+                                           const float* g_lse, void* dx, fg_dtype dx_dtype, int64_t lddx, void* dw,
+                                           fg_dtype dw_dtype, int64_t lddw, int32_t accumulate, void* stream) {
+  TS_TRY(check_handle(h));
+  TS_TRY(check_loss_extent(rows, cols, vocab));
+  if (dtype != FG_BF16) return err(FG_EINVAL, "x and w must be bf16 (the tensor cores' operands)");
+  TS_TRY(check_matrix("x", x, dtype, ldx, rows, cols));
+  TS_TRY(check_matrix("w", w, dtype, ldw, rows > 0 ? vocab : 0, cols));
+  TS_TRY(check_array("targets", targets, rows > 0, 8));
+  TS_TRY(check_array("lse", lse, rows > 0));
+  TS_TRY(check_array("g_loss", g_loss, rows > 0));
+  TS_TRY(check_array("g_lse", g_lse, false));
+  if (dx) TS_TRY(check_matrix("dx", dx, dx_dtype, lddx, rows, cols));
+  if (dw) TS_TRY(check_matrix("dw", dw, dw_dtype, lddw, vocab, cols));
+  VocabLossArgs a;
+  a.x = mat(x, dtype, ldx);
+  a.w = mat(w, dtype, ldw);
+  a.rows = rows;
+  a.cols = (int)cols;
+  a.vocab = vocab;
+  a.targets = targets;
+  a.lse = const_cast<float*>(lse);
+  a.g_loss = g_loss;
+  a.g_lse = g_lse;
+  a.dx = out(dx, dx_dtype, lddx);
+  a.dw = out(dw, dw_dtype, lddw);
+  a.accumulate = accumulate != 0;
+  TS_TRY(check_workspace(h, vocab_loss_workspace(rows, cols, vocab, true, !rows_aligned(a.w), true, false)));
+  return done(launch_vocab_loss_backward(*h, a, static_cast<cudaStream_t>(stream)),
+              "ts_linear_cross_entropy_backward launch");
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 """Training-step operators: layer norm, 8-bit activation checkpoints and the
-gradients that read them, and token log probabilities.
+gradients that read them, token log probabilities, the embedding of tokens, and
+the cross entropy of a linear layer over the vocabulary.
 
 Argument marshalling only, as everywhere in this package: the caller passes
 every tensor, outputs included, and the library's kernels do the work (see
@@ -61,6 +62,16 @@ def checkpoint_layout(rows, cols):
     lib = _lib.load()
     v = [C.c_int64() for _ in range(3)]
     _lib.check(lib.ts_checkpoint_layout(rows, cols, *[C.byref(x) for x in v]))
+    return tuple(x.value for x in v)
+
+
+def linear_cross_entropy_workspace(rows, cols, vocab):
+    """(least, most) workspace bytes of linear_cross_entropy and its gradient:
+    below the first they are refused, with the second they take all rows and
+    the whole vocabulary at once (host only)."""
+    lib = _lib.load()
+    v = [C.c_int64() for _ in range(2)]
+    _lib.check(lib.ts_linear_cross_entropy_workspace(rows, cols, vocab, *[C.byref(x) for x in v]))
     return tuple(x.value for x in v)
 
 
@@ -204,6 +215,64 @@ class TrainingOps:
             _array("lse", lse, (rows,), dev), _array("entropy", entropy, (rows,), dev),
             _array("g_logprob", g_logprob, (rows,), dev), _array("g_entropy", g_entropy, (rows,), dev), pd, td, ldd,
             self._stream(stream)))
+
+    def embedding(self, ids, table, y, scale=1.0, stream=None):
+        """y = scale * table[ids] (ids int64); an id outside the table gives
+        zeros."""
+        dev = self.device
+        rows, cols = y.shape
+        vocab = table.shape[0]
+        pt, tt, ldt = _matrix("table", table, vocab, cols, dev)
+        py, ty, ldy = _matrix("y", y, rows, cols, dev)
+        _lib.check(self.lib.ts_embedding(self.h, _array("ids", ids, (rows,), dev, torch.int64), rows, pt, tt, ldt,
+                                         vocab, cols, scale, py, ty, ldy, self._stream(stream)))
+
+    def embedding_backward(self, ids, dy, dtable, scale=1.0, accumulate=False, stream=None):
+        """The table's gradient: row v is scale times the sum of dy over the
+        tokens of id v, in their order."""
+        dev = self.device
+        rows, cols = dy.shape
+        vocab = dtable.shape[0]
+        pdy, tdy, lddy = _matrix("dy", dy, rows, cols, dev)
+        pd, td, ldd = _matrix("dtable", dtable, vocab, cols, dev)
+        _lib.check(self.lib.ts_embedding_backward(
+            self.h, _array("ids", ids, (rows,), dev, torch.int64), pdy, tdy, lddy, rows, vocab, cols, scale, pd, td,
+            ldd, accumulate, self._stream(stream)))
+
+    def linear_cross_entropy(self, x, w, targets, loss, lse, stream=None):
+        """Cross entropy of the logits x w^T with targets (int64), and their
+        log-sum-exp, by row; the logits are not kept.  Either may be None."""
+        dev = self.device
+        rows, cols = x.shape
+        vocab = w.shape[0]
+        px, pw, ldx, ldw = _operands(x, w, rows, cols, vocab, dev)
+        _lib.check(self.lib.ts_linear_cross_entropy(
+            self.h, px, ldx, pw, ldw, FG_BF16, rows, cols, vocab, _array("targets", targets, (rows,), dev, torch.int64),
+            _array("loss", loss, (rows,), dev), _array("lse", lse, (rows,), dev), self._stream(stream)))
+
+    def linear_cross_entropy_backward(self, x, w, targets, lse, g_loss, dx, dw, g_lse=None, accumulate=False,
+                                      stream=None):
+        """dx and dw (either may be None) from the gradients of loss and (may
+        be None) lse.  accumulate adds to what dw holds."""
+        dev = self.device
+        rows, cols = x.shape
+        vocab = w.shape[0]
+        px, pw, ldx, ldw = _operands(x, w, rows, cols, vocab, dev)
+        pdx, tdx, lddx = (None, FG_BF16, cols) if dx is None else _matrix("dx", dx, rows, cols, dev)
+        pdw, tdw, lddw = (None, FG_BF16, cols) if dw is None else _matrix("dw", dw, vocab, cols, dev)
+        _lib.check(self.lib.ts_linear_cross_entropy_backward(
+            self.h, px, ldx, pw, ldw, FG_BF16, rows, cols, vocab, _array("targets", targets, (rows,), dev, torch.int64),
+            _array("lse", lse, (rows,), dev), _array("g_loss", g_loss, (rows,), dev),
+            _array("g_lse", g_lse, (rows,), dev), pdx, tdx, lddx, pdw, tdw, lddw, accumulate, self._stream(stream)))
+
+
+def _operands(x, w, rows, cols, vocab, device):
+    """The bf16 operands of a product over the vocabulary."""
+    px, tx, ldx = _matrix("x", x, rows, cols, device)
+    pw, tw, ldw = _matrix("w", w, vocab, cols, device)
+    if tx != FG_BF16 or tw != FG_BF16:
+        raise FgError(FG_EINVAL, "x and w: must be bfloat16")
+    return px, pw, ldx, ldw
 
 
 def _buffer(ckpt, device):

@@ -531,7 +531,8 @@ void tf_layout_destroy(tf_layout* l);
 /* ---- training-step operators ------------------------------------------------
  * What a training step runs between its operator groups and the packing of
  * its gradients: layer norm, 8-bit activation checkpoints with the gradients
- * that read them, and the log probabilities of a step's tokens.  The pages
+ * that read them, the log probabilities of a step's tokens, their embedding and
+ * the cross entropy of a linear layer over the vocabulary.  The pages
  * have no counterpart.
  *
  * Matrices are row major, FG_F32 or FG_BF16, with a row pitch in elements (ld
@@ -560,8 +561,9 @@ fg_status ts_create(int64_t workspace_bytes, ts_ops** out);
 fg_status ts_set_wait_limit(ts_ops* h, int64_t wait_limit_ns, int32_t flags);
 
 /* Synchronises the stream, then reads and clears the handle's error word:
- * FG_ETIMEOUT when a bounded wait of a ts_weight_grad kernel expired; that
- * call's results are incomplete. */
+ * FG_ETIMEOUT when a bounded wait of a ts_weight_grad or
+ * ts_linear_cross_entropy(_backward) kernel expired; that call's results are
+ * incomplete. */
 fg_status ts_sync_status(ts_ops* h, void* cuda_stream);
 
 void ts_destroy(ts_ops* h);
@@ -643,6 +645,55 @@ fg_status ts_token_logprobs_backward(ts_ops* h, const void* logits, fg_dtype dty
                                      int64_t vocab, const int64_t* tokens, const float* lse, const float* entropy,
                                      const float* g_logprob, const float* g_entropy, void* dlogits, fg_dtype d_dtype,
                                      int64_t ldd, void* cuda_stream);
+
+/* The embedding of tokens: y [rows, cols] = scale * table[ids], table [vocab,
+ * cols], one rounding to y's type.  An id outside 0 .. vocab - 1 (a padded
+ * place) gives zeros. */
+fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* table, fg_dtype table_dtype,
+                       int64_t ld_table, int64_t vocab, int64_t cols, float scale, void* y, fg_dtype y_dtype,
+                       int64_t ldy, void* cuda_stream);
+
+/* Its gradient: row v of dtable [vocab, cols] is scale times the float32 sum of
+ * dy's rows with id v, and zeros where there are none; accumulate = 1 adds to
+ * what dtable holds and leaves rows without tokens as they are.  Rows of dy
+ * whose id is outside the table are not read.  The sum's order depends on the
+ * ids and the sizes alone.  The workspace holds the tokens in sorted order: 8
+ * bytes a token up to 8192 of them, about 17 for more (FG_EUNSUPPORTED
+ * otherwise). */
+fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, fg_dtype dy_dtype, int64_t lddy,
+                                int64_t rows, int64_t vocab, int64_t cols, float scale, void* dtable,
+                                fg_dtype d_dtype, int64_t ldd, int32_t accumulate, void* cuda_stream);
+
+/* Softmax cross entropy of a linear layer over a vocabulary, whose logits x w^T
+ * [rows, vocab] are never kept: x [rows, cols] and w [vocab, cols] (a row a
+ * token, like an embedding's table), both of type dtype, which must be FG_BF16.
+ * lse = log sum exp of a row's logits, loss = lse - logits[targets[r]]; either
+ * may be NULL (targets too without loss).  A target outside 0 .. vocab - 1
+ * leaves its row unscored: loss 0.  The logits and all sums are float32.  A
+ * -inf logit has probability 0; a row of nothing else has lse -inf and loss
+ * inf; a row with a NaN or +inf logit gives NaN.  rows, cols and vocab are at
+ * most 2^20.
+ *
+ * Its gradient: with d = (g_loss + g_lse) * exp(logits - lse) - g_loss *
+ * onehot(target), from the lse it wrote, dx = d w and dw = d^T x, added to
+ * what dw holds when accumulate = 1.  dx and dw are FG_F32 or FG_BF16, either
+ * may be NULL; g_lse may be NULL.  d is rounded to bf16, as an operand of the
+ * tensor cores; the sums are float32.  An unscored row takes only g_lse's part
+ * (without g_lse it may hold anything), a row of -inf logits none.
+ *
+ * The workspace bounds how many rows (forward) or how much of the vocabulary
+ * (backward) is taken at a time: ts_linear_cross_entropy_workspace gives the
+ * least that any such call needs (FG_EUNSUPPORTED below it) and the most that
+ * it uses.  Host only; either output may be NULL. */
+fg_status ts_linear_cross_entropy_workspace(int64_t rows, int64_t cols, int64_t vocab, int64_t* least, int64_t* most);
+fg_status ts_linear_cross_entropy(ts_ops* h, const void* x, int64_t ldx, const void* w, int64_t ldw, fg_dtype dtype,
+                                  int64_t rows, int64_t cols, int64_t vocab, const int64_t* targets, float* loss,
+                                  float* lse, void* cuda_stream);
+fg_status ts_linear_cross_entropy_backward(ts_ops* h, const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                           fg_dtype dtype, int64_t rows, int64_t cols, int64_t vocab,
+                                           const int64_t* targets, const float* lse, const float* g_loss,
+                                           const float* g_lse, void* dx, fg_dtype dx_dtype, int64_t lddx, void* dw,
+                                           fg_dtype dw_dtype, int64_t lddw, int32_t accumulate, void* cuda_stream);
 
 #ifdef __cplusplus
 }

@@ -122,3 +122,44 @@ def token_logprobs_backward(x, tokens, g_logprob, g_entropy=None):
         if g_entropy is not None:
             out[r] -= g_entropy[r] * np.where(p == 0, 0.0, p * (np.where(p == 0, 0.0, lp) + ent[r]))
     return out
+
+
+def embedding(ids, table, scale=1.0):
+    """Rows of the table, scaled; zeros for an id outside it."""
+    table, ids = np.asarray(table, np.float64), np.asarray(ids)
+    inside = (ids >= 0) & (ids < len(table))
+    return np.where(inside[:, None], table[np.where(inside, ids, 0)] * scale, 0.0)
+
+
+def embedding_backward(ids, dy, vocab, scale=1.0):
+    out = np.zeros((vocab, np.asarray(dy).shape[1]))
+    for t, v in enumerate(ids):
+        if 0 <= v < vocab:
+            out[v] += np.asarray(dy[t], np.float64)
+    return out * scale
+
+
+def linear_cross_entropy(x, w, targets):
+    """(loss, lse) of the logits x w^T."""
+    with np.errstate(all="ignore"):
+        logits = np.asarray(x, np.float64) @ np.asarray(w, np.float64).T
+    logprob, _, lse, _, _ = token_logprobs(logits, targets)
+    scored = np.array([0 <= t < len(w) for t in targets], bool)
+    return np.where(scored, -logprob, 0.0), lse
+
+
+def linear_cross_entropy_backward(x, w, targets, lse, g_loss, g_lse=None):
+    """(dx, dw, d), d the logits' gradient, from lse as it was saved.  Rows that
+    take no gradient count as zeros."""
+    x, w, lse = (np.asarray(a, np.float64) for a in (x, w, lse))
+    scored = np.array([0 <= t < len(w) for t in targets], bool)
+    takes = (scored if g_lse is None else np.ones(len(x), bool)) & (lse != -np.inf)
+    x = np.where(takes[:, None], x, 0.0)
+    with np.errstate(all="ignore"):
+        p = np.exp(x @ w.T - np.where(takes, lse, 0.0)[:, None])
+    g = np.where(scored & takes, np.asarray(g_loss, np.float64), 0.0)
+    coef = g if g_lse is None else g + np.where(takes, np.asarray(g_lse, np.float64), 0.0)
+    d = np.where(takes[:, None], coef[:, None] * p, 0.0)
+    for t in np.flatnonzero(scored):
+        d[t, targets[t]] -= g[t]
+    return d @ w, d.T @ x, d
