@@ -75,6 +75,7 @@ struct VocabKernel {
   int nx, nw, late, extra;   // dx and dw items; see item_of
   int add_dx;                // the piece adds to dx's sums
   int dw_kind;               // 0 bf16 by TMA, 1 float32 by TMA, 2 by threads
+  int cols_whole;            // dw's rows end on 16 bytes
   int dw_bf16, accumulate;
   void* dw;
   int64_t lddw;
@@ -447,65 +448,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else {
         const bool dx = w.kind == 1;
         const int m_end = dx ? P.rows : P.vocab;
-        if (!dx && P.dw_kind == 0) {
-#pragma unroll 1
-          for (int j = 0; j < kHalf; j += 64) {
-            stage_free();
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float v[32];
-              tmem_ld32(acc + j + 32 * k, v);
-              if (j + 64 == kHalf && k == 1) release();
-              stage.put_bf16(lane, k, v);
-            }
-            stage_full();
-            if (lane == 0) {
-              if (r0 < m_end && c0 + j < P.cols) tma_store_2d(&P.store_dw, c0 + j, r0, stage_u32);
-              bulk_commit();
+        // 32 columns of dw as float32 in the stage, to rows that TMA cannot write
+        // or that bf16 values are added to
+        auto by_threads = [&](int j) {
+          __syncwarp();
+          const int col = c0 + j + lane, n = col < P.cols ? min(32, P.vocab - r0) : 0;
+          for (int r = 0; r < n; ++r) {
+            const int64_t at = (int64_t)(r0 + r) * P.lddw + col;
+            const float x = stage.get(r, lane);
+            if (P.dw_bf16) {
+              __nv_bfloat16* d = static_cast<__nv_bfloat16*>(P.dw) + at;
+              *d = __float2bfloat16_rn(P.accumulate ? __bfloat162float(*d) + x : x);
+            } else {
+              float* d = static_cast<float*>(P.dw) + at;
+              *d = P.accumulate ? *d + x : x;
             }
           }
-        } else {
+          __syncwarp();
+        };
 #pragma unroll 1
-          for (int j = 0; j < kHalf; j += 32) {
-            stage_free();
-            float v[32];
-            tmem_ld32(acc + j, v);
-            if (j + 32 == kHalf) release();
-            if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
+        for (int j = 0; j < kHalf; j += 64) {
+          // TMA writes 16 bytes at a time, past the last column too
+          const bool tma = dx || (P.dw_kind < 2 && (c0 + j + 64 <= P.cols || P.cols_whole));
+          const bool half = !dx && tma && P.dw_kind == 0;   // bf16: both 32 columns in one store
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = 0.f;
-            }
-            stage.put_f32(lane, v);
-            if (dx || P.dw_kind == 1) {
-              stage_full();
-              if (lane == 0) {
-                if (r0 < m_end && c0 + j < P.cols) {
-                  if (!dx) {
-                    if (P.accumulate) tma_add_2d(&P.store_dw, c0 + j, r0, stage_u32);
-                    else tma_store_2d(&P.store_dw, c0 + j, r0, stage_u32);
-                  } else {
-                    if (P.add_dx) tma_add_3d(&P.store_dx, c0 + j, r0, w.split, stage_u32);
-                    else tma_store_3d(&P.store_dx, c0 + j, r0, w.split, stage_u32);
-                  }
-                }
-                bulk_commit();
-              }
+          for (int k = 0; k < 2; ++k) {
+            if (!half || k == 0) stage_free();
+            float v[32];
+            tmem_ld32(acc + j + 32 * k, v);
+            if (j + 64 == kHalf && k == 1) release();
+            if (half) {
+              stage.put_bf16(lane, k, v);
+              if (k == 0) continue;
             } else {
-              // rows of dw that TMA cannot write, or that bf16 values are added to
-              __syncwarp();
-              const int col = c0 + j + lane, n = col < P.cols ? min(32, P.vocab - r0) : 0;
-              for (int r = 0; r < n; ++r) {
-                const int64_t at = (int64_t)(r0 + r) * P.lddw + col;
-                const float x = stage.get(r, lane);
-                if (P.dw_bf16) {
-                  __nv_bfloat16* d = static_cast<__nv_bfloat16*>(P.dw) + at;
-                  *d = __float2bfloat16_rn(P.accumulate ? __bfloat162float(*d) + x : x);
+              if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = 0.f;
+              }
+              stage.put_f32(lane, v);
+              if (!tma) {
+                by_threads(j + 32 * k);
+                continue;
+              }
+            }
+            stage_full();
+            const int col = c0 + j + (half ? 0 : 32 * k);
+            if (lane == 0) {
+              if (r0 < m_end && col < P.cols) {
+                if (!dx) {
+                  if (P.accumulate) tma_add_2d(&P.store_dw, col, r0, stage_u32);
+                  else tma_store_2d(&P.store_dw, col, r0, stage_u32);
                 } else {
-                  float* d = static_cast<float*>(P.dw) + at;
-                  *d = P.accumulate ? *d + x : x;
+                  if (P.add_dx) tma_add_3d(&P.store_dx, col, r0, w.split, stage_u32);
+                  else tma_store_3d(&P.store_dx, col, r0, w.split, stage_u32);
                 }
               }
-              __syncwarp();
+              bulk_commit();
             }
           }
         }
@@ -913,6 +911,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   P.dw_bf16 = a.dw.bf16;
   P.lddw = a.dw.ld;
   P.dw_kind = !rows_aligned(a.dw) || (a.dw.bf16 && a.accumulate) ? 2 : a.dw.bf16 ? 0 : 1;
+  P.cols_whole = a.cols * a.dw.elem() % 16 == 0;
   P.err = h.err;
   P.wait_limit_ns = h.wait_limit_ns;
   P.inject = h.inject;
