@@ -13,6 +13,7 @@
 // second kernel adds in order.  Rows of the table that no token uses are zeroed
 // by other blocks of the same launch, which look them up in the sorted list.
 #include <algorithm>
+#include <type_traits>
 
 #include "launch.h"
 #include "ts_device.cuh"
@@ -66,8 +67,10 @@ __global__ void __launch_bounds__(kThreads) ts_embed_kernel(const __grid_constan
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kMaxBits = 9, kMaxBins = 1 << kMaxBits;
 constexpr int kSortAlone = 8192;   // tokens that one block sorts by itself
-constexpr int kTilePer = 4;        // 32-token rounds a warp of a tile of a longer list
-constexpr int kTile = kTilePer * kSortThreads;
+// 32-token rounds that a warp takes of a longer list's tile: a short list is
+// spread over more blocks, a long one has fewer counts that every block adds up.
+constexpr int kShortPer = 2, kLongPer = 8;
+constexpr int64_t kShortList = 1 << 18;
 
 struct SortKernel {
   const int64_t* ids;
@@ -78,8 +81,7 @@ struct SortKernel {
   const uint32_t* idx_in;
   uint32_t* key;
   uint32_t* idx;
-  uint32_t* counts;        // [tiles][bins] of this pass
-  uint32_t* next_counts;   // of the next one, or null
+  uint32_t* counts;         // [tiles][bins]
   int shift, tiles;
 };
 
@@ -113,21 +115,27 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t* warp_s
   return warp_sums[warp] + s - v;
 }
 
-// The ranks of a warp's `per` rounds of 32 keys among the warp's keys of the
-// same digit, in order, and the counts in hist[digit] (a row of this warp's
-// own).  Rounds past `n` keys take no part.
+// The ranks of a warp's rounds of 32 keys among the warp's keys of the same
+// digit, in order, and the counts in hist[digit] (a row of this warp's own).
+// Rounds past `n` keys take no part.  Keys of the same digit find each other by
+// a vote for each bit.
 template <int PER>
-__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[PER], int first, int n, int bins, uint32_t* hist,
+__device__ __forceinline__ void warp_ranks(const uint32_t (&digit)[PER], int first, int n, int bits, uint32_t* hist,
                                            uint32_t (&rank)[PER]) {
   const int lane = threadIdx.x & 31;
-  for (int d = lane; d < bins; d += 32) hist[d] = 0;
+  for (int d = lane; d < 1 << bits; d += 32) hist[d] = 0;
   __syncwarp();
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
     if (first + r * 32 >= n) break;
     const bool in = first + r * 32 + lane < n;
-    const uint32_t d = in ? digit[r] : 0xffffffffu;
-    const uint32_t peers = __match_any_sync(0xffffffffu, d);
+    const uint32_t d = digit[r];
+    uint32_t peers = __ballot_sync(0xffffffffu, in);
+#pragma unroll
+    for (int b = 0; b < kMaxBits; ++b) {
+      const uint32_t set = __ballot_sync(0xffffffffu, d >> b & 1);   // (digits have no bits past `bits`)
+      peers &= d >> b & 1 ? set : ~set;
+    }
     const uint32_t base = in ? hist[d] : 0;
     __syncwarp();
     if (in && (peers & ((1u << lane) - 1)) == 0) hist[d] = base + __popc(peers);
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_alone_kernel(const __
     uint32_t digit[kAlonePer], rank[kAlonePer];
 #pragma unroll
     for (int r = 0; r < kAlonePer; ++r) digit[r] = (key[r] >> (pass * P.bits)) & (bins - 1);
-    warp_ranks(digit, first, n, bins, hist + warp * kMaxBins, rank);
+    warp_ranks(digit, first, n, P.bits, hist + warp * kMaxBins, rank);
     __syncthreads();
     const uint32_t at = block_exclusive(warp_offsets(hist, bins), sums);
     if ((int)threadIdx.x < bins) base[threadIdx.x] = at;
@@ -211,8 +219,8 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_alone_kernel(const __
   }
 }
 
-// Longer lists: the first pass's counts by tile (the later passes' are made by
-// the pass before), and one pass.
+// Longer lists: a pass's counts by tile, and the pass.
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __grid_constant__ SortKernel P) {
   __shared__ uint32_t hist[kMaxBins];
   pdl_launch_dependents();
@@ -221,19 +229,16 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __gri
   if ((int)threadIdx.x < bins) hist[threadIdx.x] = 0;
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kTilePer; ++r) {
-    const int64_t i = (int64_t)blockIdx.x * kTile + r * kSortThreads + threadIdx.x;
-    if (i < P.rows) atomicAdd(&hist[id_key(P.ids[i], P.vocab) & (bins - 1)], 1u);
+  for (int r = 0; r < PER; ++r) {
+    const int64_t i = ((int64_t)blockIdx.x * PER + r) * kSortThreads + threadIdx.x;
+    if (i < P.rows)
+      atomicAdd(&hist[(P.key_in ? P.key_in[i] : id_key(P.ids[i], P.vocab)) >> P.shift & (bins - 1)], 1u);
   }
   __syncthreads();
-  if ((int)threadIdx.x < bins) {
-    P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
-    // the later passes' counts start at zero
-    for (int p = 1; p < P.passes; ++p)
-      P.counts[((int64_t)p * P.tiles + blockIdx.x) * bins + threadIdx.x] = 0;
-  }
+  if ((int)threadIdx.x < bins) P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
 }
 
+template <int PER>
 __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid_constant__ SortKernel P) {
   extern __shared__ uint32_t smem[];
   uint32_t* hist = smem;
@@ -242,11 +247,11 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
-  const int tile0 = blockIdx.x * kTile, first = warp * kTilePer * 32;
-  const int n = min(P.rows - tile0, first + kTilePer * 32);
-  uint32_t key[kTilePer], idx[kTilePer], digit[kTilePer], rank[kTilePer];
+  const int tile0 = blockIdx.x * PER * kSortThreads, first = warp * PER * 32;
+  const int n = min(P.rows - tile0, first + PER * 32);
+  uint32_t key[PER], idx[PER], digit[PER], rank[PER];
 #pragma unroll
-  for (int r = 0; r < kTilePer; ++r) {
+  for (int r = 0; r < PER; ++r) {
     const int i = first + r * 32 + lane;
     key[r] = idx[r] = 0;
     if (i < n) {
@@ -255,9 +260,6 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
     }
     digit[r] = (key[r] >> P.shift) & (bins - 1);
   }
-  warp_ranks(digit, first, n, bins, hist + warp * kMaxBins, rank);
-  __syncthreads();
-  warp_offsets(hist, bins);
   uint32_t before = 0, total = 0;
   if ((int)threadIdx.x < bins) {
     const uint32_t* c = P.counts + threadIdx.x;
@@ -268,17 +270,18 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
       if (b < (int)blockIdx.x) before += v;
     }
   }
+  warp_ranks(digit, first, n, P.bits, hist + warp * kMaxBins, rank);
+  __syncthreads();
+  warp_offsets(hist, bins);
   const uint32_t at = block_exclusive(total, sums);
   if ((int)threadIdx.x < bins) base[threadIdx.x] = at + before;
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kTilePer; ++r) {
+  for (int r = 0; r < PER; ++r) {
     if (first + r * 32 + lane < n) {
       const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
       P.key[pos] = key[r];
       P.idx[pos] = idx[r];
-      if (P.next_counts)
-        atomicAdd(&P.next_counts[(int64_t)(pos / kTile) * bins + ((key[r] >> (P.shift + P.bits)) & (bins - 1))], 1u);
     }
   }
 }
@@ -302,11 +305,44 @@ __device__ __forceinline__ float* part_at(const EmbedBackKernel& P, int chunk, i
   return P.part + ((int64_t)chunk * 2 + slot) * P.part_cols + group * kGroupCols + lane * 8;
 }
 
-// old + scale * sum, or scale * sum
-template <bool ACC>
-__device__ __forceinline__ void finish(float scale, const float (&acc)[8], const float (&old)[8], float (&v)[8]) {
+// Whether the sum is added in memory: float32 rows, each value by one reduction
+// of one launch, so that it does not matter when.  (Reading them first took
+// 65536 x 1003 into 50001 131 us in place of XX.)
+template <class U, bool ACC>
+constexpr bool kAddInMemory = ACC && std::is_same<U, float>::value;
+
+// Adds the group's values to a float32 row.
+template <bool VEC>
+__device__ __forceinline__ void add_group(float* p, int c0, int cols, int lane, const float (&v)[8]) {
+  if (VEC && c0 + lane * 8 + 8 <= cols) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = ACC ? fmaf(scale, acc[j], old[j]) : scale * acc[j];
+    for (int k = 0; k < 8; k += 4)
+      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + c0 + lane * 8 + k), "f"(v[k]),
+                   "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = c0 + group_col<VEC>(lane, j);
+      if (c < cols) atomicAdd(p + c, v[j]);
+    }
+  }
+}
+
+// scale * sum, or (ACC, in 16 bits) old + scale * sum, into a row.
+template <bool VEC, bool ACC, class U>
+__device__ __forceinline__ void finish(U* row, float scale, const float (&acc)[8], const float (&old)[8], int c0,
+                                       int cols, int lane) {
+  float v[8];
+  if constexpr (kAddInMemory<U, ACC>) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = scale * acc[j];
+    add_group<VEC>(row, c0, cols, lane, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = ACC ? fmaf(scale, acc[j], old[j]) : scale * acc[j];
+    store_group<VEC>(row, c0, cols, lane, v);
+  }
 }
 
 // T: dy's type, U: dtable's; ACC adds to what dtable holds.
@@ -345,7 +381,8 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
   const uint32_t vocab = (uint32_t)P.vocab;
   bool open = p0 > 0 && P.key[p0 - 1] == P.key[p0];   // the first id has tokens in the chunk before
   float acc[8] = {};
-  constexpr int kU = ACC ? 4 : 8;   // rows in flight
+  constexpr bool kOld = ACC && !kAddInMemory<U, ACC>;   // what dtable holds is read
+  constexpr int kU = kOld ? 4 : 8;                       // rows in flight
   for (int q = p0; q < p1; q += 32) {
     const int at = q + lane;
     const uint32_t k = at < p1 ? P.key[at] : vocab, ix = at < p1 ? P.idx[at] : 0;
@@ -353,13 +390,13 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
     const int n = min(32, p1 - q);
     for (int j = 0; j < n; j += kU) {
       RawGroup<T, VEC> raw[kU];
-      RawGroup<U, VEC> old[ACC ? kU : 1];
+      RawGroup<U, VEC> old[kOld ? kU : 1];
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
         const uint32_t ki = __shfl_sync(0xffffffffu, k, (j + i) & 31), xi = __shfl_sync(0xffffffffu, ix, (j + i) & 31);
         const bool in = j + i < n && ki < vocab;
         raw[i].load(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
-        if constexpr (ACC) {
+        if constexpr (kOld) {
           const uint32_t ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
           const bool ends = in && ni != ki;
           old[i].load(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
@@ -382,9 +419,8 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
           reinterpret_cast<float4*>(o)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         } else {
           float was[8] = {};
-          if constexpr (ACC) old[i].get(was);
-          finish<ACC>(P.scale, acc, was, v);
-          store_group<VEC>(d + (int64_t)ki * P.ldd, c0, P.cols, lane, v);
+          if constexpr (kOld) old[i].get(was);
+          finish<VEC, ACC>(d + (int64_t)ki * P.ldd, P.scale, acc, was, c0, P.cols, lane);
         }
         open = false;
 #pragma unroll
@@ -394,47 +430,65 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
   }
 }
 
-// An id whose tokens begin in this warp's chunk and end in a later one.
+// An id whose tokens begin in a chunk and end in a later one: the block's warps
+// share the later chunks, each its own in order, and their sums are added in
+// order.  (An id of 6000 tokens of 65536 has 190 chunks: one warp for them all
+// took 28 us, the block XX.)
 template <class U, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_constant__ EmbedBackKernel P) {
+  __shared__ __align__(16) float sums[kWarps][kGroupCols];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= P.units) return;
-  const int chunk = (int)(u / P.groups), group = (int)(u - (int64_t)chunk * P.groups), c0 = group * kGroupCols;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunk = (int)(blockIdx.x / P.groups), group = (int)(blockIdx.x - (int64_t)chunk * P.groups);
+  const int c0 = group * kGroupCols;
   const int64_t p0 = (int64_t)chunk * P.chunk, p1 = p0 + P.chunk;
   if (p1 >= P.rows) return;
   const uint32_t k = P.key[p1 - 1];
   if (k >= (uint32_t)P.vocab || P.key[p1] != k) return;
   if (p0 > 0 && P.key[p0 - 1] == k) return;   // it began before
-  U* row = static_cast<U*>(P.d) + (int64_t)k * P.ldd;
-  float acc[8], was[8] = {}, v[8];
-  load8(part_at(P, chunk, 1, group, lane), acc);
-  if constexpr (ACC) load_group<VEC>(row, c0, P.cols, lane, was);
+  // the chunks after this one that have a part
+  int parts = 0;
   for (int64_t e = chunk + 1;; e += 32) {
     // lane i: whether the id goes on past chunk e + i
     const int64_t after = (e + lane + 1) * P.chunk;
     const uint32_t stops = __ballot_sync(0xffffffffu, !(after < P.rows && P.key[after] == k));
-    const int n = stops ? __ffs(stops) : 32;
-    for (int j = 0; j < n; j += 4) {
-      float x[4][8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (j + i < n) load8(part_at(P, (int)e + j + i, 0, group, lane), x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (j + i < n) {
-#pragma unroll
-          for (int m = 0; m < 8; ++m) acc[m] += x[i][m];
-        }
-      }
-    }
+    parts += stops ? __ffs(stops) : 32;
     if (stops) break;
   }
-  finish<ACC>(P.scale, acc, was, v);
-  store_group<VEC>(row, c0, P.cols, lane, v);
+  float acc[8] = {};
+  if (warp == 0) load8(part_at(P, chunk, 1, group, lane), acc);
+  const int used = min(kWarps, (parts + 3) / 4);   // warps at work
+  const int from = chunk + 1 + (int)((int64_t)parts * warp / used), to = chunk + 1 + (int)((int64_t)parts * (warp + 1) / used);
+  for (int j = from; warp < used && j < to; j += 8) {
+    float x[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (j + i < to) load8(part_at(P, j + i, 0, group, lane), x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (j + i < to) {
+#pragma unroll
+        for (int m = 0; m < 8; ++m) acc[m] += x[i][m];
+      }
+    }
+  }
+  if (used > 1) {
+    store8<true>(&sums[warp][lane * 8], acc);   // (shared memory)
+    __syncthreads();
+  }
+  if (warp) return;
+  for (int w = 1; w < used; ++w) {
+    float x[8];
+    load8(&sums[w][lane * 8], x);
+#pragma unroll
+    for (int m = 0; m < 8; ++m) acc[m] += x[m];
+  }
+  U* row = static_cast<U*>(P.d) + (int64_t)k * P.ldd;
+  float was[8] = {};
+  if constexpr (ACC && !kAddInMemory<U, ACC>) load_group<VEC>(row, c0, P.cols, lane, was);
+  finish<VEC, ACC>(row, P.scale, acc, was, c0, P.cols, lane);
 }
 
 template <class K, class A>
@@ -500,11 +554,20 @@ SortPlan sort_plan(int64_t rows, int64_t vocab) {
   while (key_bits < 32 && (vocab >> key_bits)) ++key_bits;   // (the key of a padded place is `vocab`)
   s.passes = (key_bits + kMaxBits - 1) / kMaxBits;
   s.bits = (key_bits + s.passes - 1) / s.passes;
-  s.tiles = (int)((rows + kTile - 1) / kTile);
+  const int64_t tile = (rows <= kShortList ? kShortPer : kLongPer) * kSortThreads;
+  s.tiles = (int)((rows + tile - 1) / tile);
   const bool alone = rows <= kSortAlone;
-  s.counts_bytes = alone ? 0 : ((int64_t)s.passes * s.tiles << s.bits) * 4;
+  s.counts_bytes = alone ? 0 : ((int64_t)s.tiles << s.bits) * 4;
   s.bytes = (rows * 4 + 255) / 256 * 256 * (alone ? 2 : 4) + (s.counts_bytes + 255) / 256 * 256;
   return s;
+}
+template <int PER>
+cudaError_t sort_pass(const SortKernel& S, cudaStream_t st) {
+  constexpr int smem = (kSortWarps * kMaxBins + kMaxBins + 32) * 4;
+  cudaError_t e = cudaFuncSetAttribute(ts_sort_pass_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = launch(ts_sort_count_kernel<PER>, S.tiles, kSortThreads, 0, S, st);
+  if (e == cudaSuccess) e = launch(ts_sort_pass_kernel<PER>, S.tiles, kSortThreads, smem, S, st);
+  return e;
 }
 }  // namespace
 
@@ -532,12 +595,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
       if (e != cudaSuccess) return e;
       e = launch(ts_sort_alone_kernel, 1, kSortThreads, kAloneSmem, S, st);
     } else {
-      constexpr int smem = (kSortWarps * kMaxBins + kMaxBins + 32) * 4;
-      uint32_t* counts = reinterpret_cast<uint32_t*>(h.ws + 4 * list);
-      e = cudaFuncSetAttribute(ts_sort_pass_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (e != cudaSuccess) return e;
-      S.counts = counts;
-      e = launch(ts_sort_count_kernel, s.tiles, kSortThreads, 0, S, st);
+      S.counts = reinterpret_cast<uint32_t*>(h.ws + 4 * list);
       for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
         // the last pass ends in the first list
         const int out = (s.passes - 1 - p) & 1 ? 2 : 0;
@@ -546,9 +604,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
         S.key_in = p ? at[2 - out] : nullptr;
         S.idx_in = p ? at[3 - out] : nullptr;
         S.shift = p * s.bits;
-        S.counts = counts + ((int64_t)p * s.tiles << s.bits);
-        S.next_counts = p + 1 < s.passes ? counts + ((int64_t)(p + 1) * s.tiles << s.bits) : nullptr;
-        e = launch(ts_sort_pass_kernel, s.tiles, kSortThreads, smem, S, st);
+        e = a.rows <= kShortList ? sort_pass<kShortPer>(S, st) : sort_pass<kLongPer>(S, st);
       }
     }
     if (e != cudaSuccess) return e;
@@ -579,7 +635,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
     P.unit_blocks = (P.units + kWarps - 1) / kWarps;
   }
   const int64_t fill = a.accumulate ? 0 : (a.vocab + kWarps * kFillRows - 1) / (kWarps * kFillRows);
-  if (P.unit_blocks + fill > kMaxGrid) return cudaErrorInvalidConfiguration;
+  if (P.unit_blocks + fill > kMaxGrid || P.units > kMaxGrid) return cudaErrorInvalidConfiguration;
   if (P.unit_blocks + fill == 0) return cudaSuccess;
   return by_type(a.dy, a.d, [&](auto t, auto u, auto vec) {
     using T = decltype(t);
@@ -588,7 +644,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
     cudaError_t e = launch(a.accumulate ? ts_embed_sum_kernel<T, U, V, true> : ts_embed_sum_kernel<T, U, V, false>,
                            P.unit_blocks + fill, kThreads, 0, P, st);
     if (e != cudaSuccess || P.chunks < 2) return e;
-    return launch(a.accumulate ? ts_embed_join_kernel<U, V, true> : ts_embed_join_kernel<U, V, false>, P.unit_blocks,
+    return launch(a.accumulate ? ts_embed_join_kernel<U, V, true> : ts_embed_join_kernel<U, V, false>, P.units,
                   kThreads, 0, P, st);
   });
 }

@@ -84,6 +84,17 @@ struct VocabKernel {
   int inject;
 };
 
+// A float32 accumulator of 4096 products is 2e-6 off, one of 1024 5e-7: the
+// tensor core truncates as it adds.  The loss is a float32 result, so its sums
+// run over at most kChain blocks of K; the epilogue's threads add what they came
+// to in registers, during the next one's MMAs.  (The gradients' sums are of
+// operands rounded to bf16.)
+constexpr int kChain = 8;
+template <int MODE>
+__device__ __forceinline__ int chain_end(int kb0, int kb1) {
+  return MODE == kLoss && kb1 - kb0 > kChain ? kb0 + kChain : kb1;
+}
+
 // What a pair works on: a tile at (m0, n0) of a product, over blocks [kb0, kb1)
 // of kKB.
 struct Item {
@@ -151,6 +162,19 @@ __device__ __forceinline__ float exp2_approx(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+// 16 consecutive f32 columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, int x, int y, int z, uint32_t src) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
@@ -287,15 +311,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, i = 0;
       uint32_t ph = 0;
       bool ok = true;
-      for (; ok; ++i) {
-        const Item w = item_of<MODE>(P, pair, npair, i);
+      for (int k = 0; ok; ++k) {
+        const Item w = item_of<MODE>(P, pair, npair, k);
         if (w.kind < 0) break;
-        const int b = i & 1;
-        if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, P.wait_limit_ns, &abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
         // MN-major: atoms of 64 columns x 8 of K, the second 64 columns one box
         // on, 16 of K 2 KB on.  K-major: atoms of 8 rows x 64 of K, 16 of K 32
         // bytes on, the second 64 of K one box on.
@@ -305,27 +323,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                        bd0 = smem_desc_sw128(base + kOperandBytes, b_mn ? kBoxBytes : 16, 1024);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
         const uint32_t a_half = (a_mn ? 4 * 2048 : kBoxBytes) >> 4, b_half = (b_mn ? 4 * 2048 : kBoxBytes) >> 4;
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!wait_bar(full0 + 8 * s, ph, P.wait_limit_ns, &abort_flag)) {
+        int s0 = w.kb0;
+        do {
+          const int s1 = chain_end<MODE>(s0, w.kb1), b = i & 1;
+          if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t so = (uint32_t)(s * kSlotBytes) >> 4;
-          const int left = w.K - kb * kKB;   // (past K both operands are zeros)
+          for (int kb = s0; kb < s1; ++kb) {
+            if (!wait_bar(full0 + 8 * s, ph, P.wait_limit_ns, &abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t so = (uint32_t)(s * kSlotBytes) >> 4;
+            const int left = w.K - kb * kKB;   // (past K both operands are zeros)
 #pragma unroll
-          for (int kk = 0; kk < kKB / 16; ++kk) {
-            if (kk * 16 >= left) break;
-            tc_mma_bf16<2>(tmem + b * kTile, ad0 + so + (kk >> 2) * a_half + (kk & 3) * a_step,
-                           bd0 + so + (kk >> 2) * b_half + (kk & 3) * b_step, idesc, kb != w.kb0 || kk != 0);
+            for (int kk = 0; kk < kKB / 16; ++kk) {
+              if (kk * 16 >= left) break;
+              tc_mma_bf16<2>(tmem + b * kTile, ad0 + so + (kk >> 2) * a_half + (kk & 3) * a_step,
+                             bd0 + so + (kk >> 2) * b_half + (kk & 3) * b_step, idesc, kb != s0 || kk != 0);
+            }
+            tc_commit_mask(empty0 + 8 * s, pair_mask);
+            if (++s == kSlots) {
+              s = 0;
+              ph ^= 1;
+            }
           }
-          tc_commit_mask(empty0 + 8 * s, pair_mask);
-          if (++s == kSlots) {
-            s = 0;
-            ph ^= 1;
-          }
-        }
-        if (ok) tc_commit_mask(tfull0 + 8 * b, pair_mask);
+          if (ok) tc_commit_mask(tfull0 + 8 * b, pair_mask);
+          s0 = s1;
+          ++i;
+        } while (ok && s0 < w.kb1);
       }
       if (!ok) {
         abort_flag = 1;
@@ -341,10 +370,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const Stage stage = {ring + kSlots * kSlotBytes + (warp - 4) * kStageBytes};
     const uint32_t stage_u32 = smem_u32(stage.p);
     bool ok = true;
-    for (int i = 0;; ++i) {
-      const Item w = item_of<MODE>(P, pair, npair, i);
+    int i = 0;   // accumulators so far
+    for (int k = 0; ok; ++k) {
+      const Item w = item_of<MODE>(P, pair, npair, k);
       if (w.kind < 0) break;
-      const int b = i & 1, r0 = w.m0 + h * kHalf + q * 32, row = r0 + lane;
+      const int r0 = w.m0 + h * kHalf + q * 32, row = r0 + lane;
       const int c0 = w.n0 + set * kHalf;   // this warp's first column
       float lse2 = 0.f, coef = 0.f, g = 0.f;
       int target = -1;   // the target's column of the piece
@@ -362,15 +392,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, P.wait_limit_ns, &abort_flag));
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + b * kTile + set * kHalf;
+      uint32_t acc = 0;
+      auto next_acc = [&]() {
+        const int b = i & 1;
+        ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, P.wait_limit_ns, &abort_flag));
+        tc_fence_after();
+        acc = tmem + ((uint32_t)(q * 32) << 16) + b * kTile + set * kHalf;
+        return ok;
+      };
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * b, 0));
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * (i & 1), 0));
+        ++i;
       };
+      if constexpr (MODE != kLoss) {
+        if (!next_acc()) break;
+      }
       // before the stage is written again, its last store has read it
       auto stage_free = [&]() {
         if (lane == 0) bulk_wait_read<0>();
@@ -381,40 +419,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         __syncwarp();
       };
       if constexpr (MODE == kLoss) {
-        // the sums' reference is the largest logit so far, in log2
-        float m2 = -INFINITY, sum = 0.f;
-#pragma unroll 1
-        for (int j = 0; j < kHalf; j += 32) {
-          float v[32];
-          tmem_ld32(acc + j, v);
-          if (j + 32 == kHalf) release();
-          const int left = P.vocab - c0 - j;   // columns of the vocabulary from here on
-          if (left <= 0) continue;
-          const int at = target - c0 - j;
-          if (at >= 0 && at < 32) {
-            float l = 0.f;
+        float v[4][32];
+        for (int s0 = w.kb0; s0 < w.kb1;) {
+          if (!next_acc()) break;
+          if (s0 == w.kb0) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) l = c == at ? v[c] : l;
-            P.tlogit[row] = l;
+            for (int j = 0; j < 4; ++j) tmem_ld32(acc + 32 * j, v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float o[16];
+              tmem_ld16(acc + 16 * j, o);
+#pragma unroll
+              for (int c = 0; c < 16; ++c) v[j / 2][j % 2 * 16 + c] += o[c];
+            }
           }
-          if (left < 32) {
+          release();
+          s0 = chain_end<MODE>(s0, w.kb1);
+        }
+        if (!ok) break;
+        // the sum's reference is the largest logit, in log2
+        const int left = P.vocab - c0, at = target - c0;
+        if (left < kHalf) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
 #pragma unroll
             for (int c = 0; c < 32; ++c)
-              if (c >= left) v[c] = -INFINITY;
-          }
-          float top = v[0];
-#pragma unroll
-          for (int c = 1; c < 32; ++c) top = fmaxf(top, v[c]);
-          const float next = fmaxf(m2, top * kLog2e);
-          const float ref = next == -INFINITY ? 0.f : next;
-          float s[4] = {};
-#pragma unroll
-          for (int c = 0; c < 32; ++c) s[c & 3] += exp2_approx(fmaf(v[c], kLog2e, -ref));
-          sum = sum * exp2_approx(m2 - ref) + ((s[0] + s[1]) + (s[2] + s[3]));
-          m2 = next;
+              if (32 * j + c >= left) v[j][c] = -INFINITY;
         }
-        if (row < P.rows && c0 < P.vocab)
-          P.part[(int64_t)(c0 / kHalf) * P.rows + row] = make_float2(m2, sum);
+        if (at >= 0 && at < kHalf) {
+          float l = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int c = 0; c < 32; ++c) l = 32 * j + c == at ? v[j][c] : l;
+          P.tlogit[row] = l;
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], v[j][c]);
+        const float m2 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
+        const float ref = m2 == -INFINITY ? 0.f : m2;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx(fmaf(v[j][c], kLog2e, -ref));
+        if (row < P.rows && left > 0)
+          P.part[(int64_t)(c0 / kHalf) * P.rows + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
 #pragma unroll 1
         for (int j = 0; j < kHalf; j += 64) {
@@ -553,12 +606,16 @@ struct JoinKernel {
   int rows, parts;
 };
 
-// The parts of 32 rows: lane = row, eight warps share the parts.
-__global__ void __launch_bounds__(256) ts_loss_join_kernel(const __grid_constant__ JoinKernel P) {
-  __shared__ float2 sm[8][32];
+// The parts of 32 rows: lane = row, the block's warps share the parts.  (With 8
+// warps a block 16 rows of 250 parts took 9 us, a chain of loads.)
+constexpr int kJoinWarps = 32;
+
+__global__ void __launch_bounds__(kJoinWarps * 32) ts_loss_join_kernel(const __grid_constant__ JoinKernel P) {
+  __shared__ float2 sm[kJoinWarps][33];
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = blockIdx.x * 32 + lane;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
   auto add = [&](float2 v) {
     const float next = fmaxf(m, v.x), ref = next == -INFINITY ? 0.f : next;
@@ -566,20 +623,29 @@ __global__ void __launch_bounds__(256) ts_loss_join_kernel(const __grid_constant
     m = next;
   };
   if (row < P.rows) {
-    int p = warp;
-    for (; p + 24 < P.parts; p += 32) {
-      float2 v[4];
+    const float2* p = P.part + row;
+    for (int k0 = warp; k0 < P.parts; k0 += 8 * kJoinWarps) {
+      float2 v[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = P.part[(int64_t)(p + 8 * k) * P.rows + row];
+      for (int k = 0; k < 8; ++k) {
+        const int at = k0 + k * kJoinWarps;
+        v[k] = at < P.parts ? p[(int64_t)at * P.rows] : make_float2(-INFINITY, 0.f);
+      }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) add(v[k]);
+      for (int k = 0; k < 8; ++k) add(v[k]);
     }
-    for (; p < P.parts; p += 8) add(P.part[(int64_t)p * P.rows + row]);
   }
-  sm[warp][lane] = make_float2(m, s);
+  sm[lane][warp] = make_float2(m, s);
   __syncthreads();
-  if (warp || row >= P.rows) return;
-  for (int k = 1; k < 8; ++k) add(sm[k][lane]);
+  // warp w now joins row w's sums, one a lane
+  row = blockIdx.x * 32 + warp;
+  const float2 v = sm[warp][lane];
+  m = v.x;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ref = m == -INFINITY ? 0.f : m;
+  s = warp_sum(v.y * exp2_approx(v.x - ref));
+  if (lane || row >= P.rows) return;
   // the reference is a rounded log2, the sum relative to it as rounded
   const float lse = s == 0.f ? -INFINITY : (m + log2f(s)) * kLn2;
   if (P.lse) P.lse[row] = lse;
@@ -645,11 +711,17 @@ __global__ void __launch_bounds__(256) ts_loss_dx_kernel(const __grid_constant__
   const int c0 = (int)(u - r * P.groups) * kGroupCols;
   float v[8];
   load_group<VEC>(P.sums + r * P.pitch, c0, P.cols, lane, v);
-  for (int s = 1; s < P.splits; ++s) {
-    float x[8];
-    load_group<VEC>(P.sums + ((int64_t)s * P.rows + r) * P.pitch, c0, P.cols, lane, x);
+  for (int s = 1; s < P.splits; s += 4) {
+    float x[4][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] += x[j];
+    for (int k = 0; k < 4; ++k)
+      if (s + k < P.splits) load_group<VEC>(P.sums + ((int64_t)(s + k) * P.rows + r) * P.pitch, c0, P.cols, lane, x[k]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (s + k < P.splits) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] += x[k][j];
+      }
   }
   store_group<VEC>(static_cast<T*>(P.dx) + r * P.ld, c0, P.cols, lane, v);
 }
@@ -858,7 +930,7 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
       e = launch(ts_vocab_kernel<kLoss>, 2 * std::min<int64_t>(pairs, items), kThreads, kSmem, P, st);
       if (e != cudaSuccess) return e;
     }
-    e = launch(ts_loss_join_kernel, (rows + 31) / 32, 256, 0, J, st);
+    e = launch(ts_loss_join_kernel, (rows + 31) / 32, kJoinWarps * 32, 0, J, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
