@@ -76,12 +76,11 @@ struct SortKernel {
   const int64_t* ids;
   int64_t vocab;
   int rows, passes, bits;
+  uint2* out;            // (key, token) sorted by key, tokens of a key in order
+  uint32_t* joins;       // set to 0; see EmbedBackKernel
   // one pass over a longer list
-  const uint32_t* key_in;   // null: from the ids
-  const uint32_t* idx_in;
-  uint32_t* key;
-  uint32_t* idx;
-  uint32_t* counts;         // [tiles][bins]
+  const uint2* in;       // null: the ids
+  uint32_t* counts;      // [tiles][bins]
   int shift, tiles;
 };
 
@@ -158,65 +157,53 @@ __device__ __forceinline__ uint32_t warp_offsets(uint32_t* hist, int bins) {
   return sum;
 }
 
-// Up to kSortAlone tokens in one block: every pass between two halves of shared
-// memory, the last one to the workspace.
+// Up to kSortAlone tokens in one block, every pass through shared memory (a last
+// pass that scatters to global memory took 12 of 22 us for 8192 tokens).
 constexpr int kAlonePer = kSortAlone / kSortThreads;
-constexpr int kAloneSmem = (kSortWarps * kMaxBins + kMaxBins + 32 + 4 * kSortAlone) * 4;
+constexpr int kAloneSmem = (kSortWarps * kMaxBins + kMaxBins + 32 + 2 * kSortAlone) * 4;
 
 __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_alone_kernel(const __grid_constant__ SortKernel P) {
-  extern __shared__ uint32_t smem[];
-  uint32_t* hist = smem;
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint2* buf = reinterpret_cast<uint2*>(smem);
+  uint32_t* hist = smem + 2 * kSortAlone;
   uint32_t* base = hist + kSortWarps * kMaxBins;
   uint32_t* sums = base + kMaxBins;
-  uint32_t* buf = sums + 32;   // key, idx, key, idx
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
   const int per = (P.rows + kSortThreads - 1) / kSortThreads, first = warp * per * 32;
   // a warp's rounds follow each other in the list, so that ranks keep its order
-  uint32_t key[kAlonePer], idx[kAlonePer];
+  uint2 e[kAlonePer];
 #pragma unroll
   for (int r = 0; r < kAlonePer; ++r) {
     const int i = first + r * 32 + lane;
-    idx[r] = i;
-    key[r] = r < per && i < P.rows ? id_key(P.ids[i], P.vocab) : 0;
+    e[r] = make_uint2(r < per && i < P.rows ? id_key(P.ids[i], P.vocab) : 0, i);
   }
+  if (threadIdx.x == 0) *P.joins = 0;
   const int n = min(P.rows, first + per * 32);
   for (int pass = 0; pass < P.passes; ++pass) {
-    uint32_t* out = buf + (pass & 1) * 2 * kSortAlone;
     uint32_t digit[kAlonePer], rank[kAlonePer];
 #pragma unroll
-    for (int r = 0; r < kAlonePer; ++r) digit[r] = (key[r] >> (pass * P.bits)) & (bins - 1);
+    for (int r = 0; r < kAlonePer; ++r) digit[r] = (e[r].x >> (pass * P.bits)) & (bins - 1);
     warp_ranks(digit, first, n, P.bits, hist + warp * kMaxBins, rank);
     __syncthreads();
     const uint32_t at = block_exclusive(warp_offsets(hist, bins), sums);
     if ((int)threadIdx.x < bins) base[threadIdx.x] = at;
     __syncthreads();
-    const bool last = pass + 1 == P.passes;
 #pragma unroll
-    for (int r = 0; r < kAlonePer; ++r) {
-      if (r < per && first + r * 32 + lane < n) {
-        const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
-        if (last) {
-          P.key[pos] = key[r];
-          P.idx[pos] = idx[r];
-        } else {
-          out[pos] = key[r];
-          out[kSortAlone + pos] = idx[r];
-        }
-      }
-    }
-    if (last) break;
+    for (int r = 0; r < kAlonePer; ++r)
+      if (r < per && first + r * 32 + lane < n)
+        buf[base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r]] = e[r];
     __syncthreads();
+    if (pass + 1 < P.passes) {
 #pragma unroll
-    for (int r = 0; r < kAlonePer; ++r) {
-      const int i = first + r * 32 + lane;
-      if (r < per && i < n) {
-        key[r] = out[i];
-        idx[r] = out[kSortAlone + i];
+      for (int r = 0; r < kAlonePer; ++r) {
+        const int i = first + r * 32 + lane;
+        if (r < per && i < n) e[r] = buf[i];
       }
     }
   }
+  for (int i = threadIdx.x; i < P.rows; i += kSortThreads) P.out[i] = buf[i];
 }
 
 // Longer lists: a pass's counts by tile, and the pass.
@@ -232,8 +219,9 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __gri
   for (int r = 0; r < PER; ++r) {
     const int64_t i = ((int64_t)blockIdx.x * PER + r) * kSortThreads + threadIdx.x;
     if (i < P.rows)
-      atomicAdd(&hist[(P.key_in ? P.key_in[i] : id_key(P.ids[i], P.vocab)) >> P.shift & (bins - 1)], 1u);
+      atomicAdd(&hist[(P.in ? P.in[i].x : id_key(P.ids[i], P.vocab)) >> P.shift & (bins - 1)], 1u);
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *P.joins = 0;
   __syncthreads();
   if ((int)threadIdx.x < bins) P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
 }
@@ -249,16 +237,14 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
   const int tile0 = blockIdx.x * PER * kSortThreads, first = warp * PER * 32;
   const int n = min(P.rows - tile0, first + PER * 32);
-  uint32_t key[PER], idx[PER], digit[PER], rank[PER];
+  uint2 e[PER];
+  uint32_t digit[PER], rank[PER];
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
     const int i = first + r * 32 + lane;
-    key[r] = idx[r] = 0;
-    if (i < n) {
-      key[r] = P.key_in ? P.key_in[tile0 + i] : id_key(P.ids[tile0 + i], P.vocab);
-      idx[r] = P.key_in ? P.idx_in[tile0 + i] : tile0 + i;
-    }
-    digit[r] = (key[r] >> P.shift) & (bins - 1);
+    e[r] = make_uint2(0, 0);
+    if (i < n) e[r] = P.in ? P.in[tile0 + i] : make_uint2(id_key(P.ids[tile0 + i], P.vocab), tile0 + i);
+    digit[r] = (e[r].x >> P.shift) & (bins - 1);
   }
   uint32_t before = 0, total = 0;
   if ((int)threadIdx.x < bins) {
@@ -278,22 +264,18 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
-    if (first + r * 32 + lane < n) {
-      const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
-      P.key[pos] = key[r];
-      P.idx[pos] = idx[r];
-    }
+    if (first + r * 32 + lane < n) P.out[base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r]] = e[r];
   }
 }
 
 // ---- sums of the sorted tokens' rows ------------------------------------------------
 
 struct EmbedBackKernel {
-  const uint32_t* key;   // sorted
-  const uint32_t* idx;
+  const uint2* list;     // (key, token), sorted
   const void* dy;
   void* d;
   float* part;           // [chunks][2][part_cols]: a chunk's first id's, its last id's
+  uint32_t* joins;       // how many ids lie in more than one chunk, and the chunks where they begin
   int64_t lddy, ldd, part_cols, units, unit_blocks, vocab;
   int rows, cols, groups, chunk, chunks;
   float scale;
@@ -347,7 +329,7 @@ __device__ __forceinline__ void finish(U* row, float scale, const float (&acc)[8
 
 // T: dy's type, U: dtable's; ACC adds to what dtable holds.
 template <class T, class U, bool VEC, bool ACC>
-__global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_constant__ EmbedBackKernel P) {
+__global__ void __launch_bounds__(kThreads, 2) ts_embed_sum_kernel(const __grid_constant__ EmbedBackKernel P) {
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -361,10 +343,10 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
       int lo = 0, hi = P.rows;
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if ((int64_t)P.key[mid] < v) lo = mid + 1;
+        if ((int64_t)P.list[mid].x < v) lo = mid + 1;
         else hi = mid;
       }
-      absent = !(lo < P.rows && (int64_t)P.key[lo] == v);
+      absent = !(lo < P.rows && (int64_t)P.list[lo].x == v);
     }
     const float zero[8] = {};
     for (uint32_t m = __ballot_sync(0xffffffffu, absent); m; m &= m - 1) {
@@ -379,116 +361,121 @@ __global__ void __launch_bounds__(kThreads) ts_embed_sum_kernel(const __grid_con
   const int p0 = chunk * P.chunk, p1 = min(P.rows, p0 + P.chunk);
   const T* dy = static_cast<const T*>(P.dy);
   const uint32_t vocab = (uint32_t)P.vocab;
-  bool open = p0 > 0 && P.key[p0 - 1] == P.key[p0];   // the first id has tokens in the chunk before
-  float acc[8] = {};
   constexpr bool kOld = ACC && !kAddInMemory<U, ACC>;   // what dtable holds is read
-  constexpr int kU = kOld ? 4 : 8;                       // rows in flight
+  // rows of a batch; one is loaded while one is added
+  constexpr int kU = kOld ? 2 : sizeof(T) == 2 ? 8 : 4;
+  struct Batch {
+    RawGroup<T, VEC> raw[kU];
+    RawGroup<U, VEC> old[kOld ? kU : 1];
+  };
+  bool open = false;
+  float acc[8] = {};
   for (int q = p0; q < p1; q += 32) {
-    const int at = q + lane;
-    const uint32_t k = at < p1 ? P.key[at] : vocab, ix = at < p1 ? P.idx[at] : 0;
-    const uint32_t next = at + 1 < P.rows && at < p1 ? P.key[at + 1] : 0xffffffffu;
-    const int n = min(32, p1 - q);
-    for (int j = 0; j < n; j += kU) {
-      RawGroup<T, VEC> raw[kU];
-      RawGroup<U, VEC> old[kOld ? kU : 1];
+    const int at = q + lane, n = min(32, p1 - q);
+    const uint2 e = at < p1 ? P.list[at] : make_uint2(vocab, 0);
+    const uint32_t next = at + 1 < P.rows && at < p1 ? P.list[at + 1].x : 0xffffffffu;
+    // the first id may have tokens in the chunk before
+    if (q == p0) open = p0 > 0 && P.list[p0 - 1].x == __shfl_sync(0xffffffffu, e.x, 0);
+    auto load = [&](Batch& b, int j) {
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const uint32_t ki = __shfl_sync(0xffffffffu, k, (j + i) & 31), xi = __shfl_sync(0xffffffffu, ix, (j + i) & 31);
+        const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), xi = __shfl_sync(0xffffffffu, e.y, (j + i) & 31);
         const bool in = j + i < n && ki < vocab;
-        raw[i].load(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
+        b.raw[i].load(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
         if constexpr (kOld) {
           const uint32_t ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
           const bool ends = in && ni != ki;
-          old[i].load(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
+          b.old[i].load(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
         }
       }
+    };
+    auto add = [&](const Batch& b, int j) {
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const uint32_t ki = __shfl_sync(0xffffffffu, k, (j + i) & 31), ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
-        if (j + i >= n) break;
-        if (ki >= vocab) return;   // (padded places sort last)
+        const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
+        if (j + i >= n || ki >= vocab) return;   // (padded places sort last)
         float v[8];
-        raw[i].get(v);
+        b.raw[i].get(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] += v[e];
+        for (int m = 0; m < 8; ++m) acc[m] += v[m];
         const bool ends = ni != ki;
         if (!ends && q + j + i + 1 < p1) continue;
         if (open || !ends) {
           float* o = part_at(P, chunk, open ? 0 : 1, group, lane);
           reinterpret_cast<float4*>(o)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
           reinterpret_cast<float4*>(o)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+          if (!open && group == 0 && lane == 0) P.joins[1 + atomicAdd(P.joins, 1u)] = chunk;
         } else {
           float was[8] = {};
-          if constexpr (kOld) old[i].get(was);
+          if constexpr (kOld) b.old[i].get(was);
           finish<VEC, ACC>(d + (int64_t)ki * P.ldd, P.scale, acc, was, c0, P.cols, lane);
         }
         open = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int m = 0; m < 8; ++m) acc[m] = 0.f;
       }
+    };
+    Batch b0, b1;
+    load(b0, 0);
+    for (int j = 0; j < n; j += 2 * kU) {
+      load(b1, j + kU);
+      add(b0, j);
+      load(b0, j + 2 * kU);
+      add(b1, j + kU);
     }
   }
 }
 
-// An id whose tokens begin in a chunk and end in a later one: the block's warps
-// share the later chunks, each its own in order, and their sums are added in
-// order.  (An id of 6000 tokens of 65536 has 190 chunks: one warp for them all
-// took 28 us, the block XX.)
+// The ids whose tokens lie in more than one chunk, as the kernel before has
+// noted them (in any order: each is summed by itself, its chunks in order).  A
+// warp takes 64 columns, so that an id of many chunks has many warps: at 65536
+// tokens the most frequent id has 190 chunks.
+constexpr int kJoinCols = 64;
+
 template <class U, bool VEC, bool ACC>
 __global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_constant__ EmbedBackKernel P) {
-  __shared__ __align__(16) float sums[kWarps][kGroupCols];
   pdl_launch_dependents();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int chunk = (int)(blockIdx.x / P.groups), group = (int)(blockIdx.x - (int64_t)chunk * P.groups);
-  const int c0 = group * kGroupCols;
-  const int64_t p0 = (int64_t)chunk * P.chunk, p1 = p0 + P.chunk;
-  if (p1 >= P.rows) return;
-  const uint32_t k = P.key[p1 - 1];
-  if (k >= (uint32_t)P.vocab || P.key[p1] != k) return;
-  if (p0 > 0 && P.key[p0 - 1] == k) return;   // it began before
-  // the chunks after this one that have a part
-  int parts = 0;
-  for (int64_t e = chunk + 1;; e += 32) {
-    // lane i: whether the id goes on past chunk e + i
-    const int64_t after = (e + lane + 1) * P.chunk;
-    const uint32_t stops = __ballot_sync(0xffffffffu, !(after < P.rows && P.key[after] == k));
-    parts += stops ? __ffs(stops) : 32;
-    if (stops) break;
-  }
-  float acc[8] = {};
-  if (warp == 0) load8(part_at(P, chunk, 1, group, lane), acc);
-  const int used = min(kWarps, (parts + 3) / 4);   // warps at work
-  const int from = chunk + 1 + (int)((int64_t)parts * warp / used), to = chunk + 1 + (int)((int64_t)parts * (warp + 1) / used);
-  for (int j = from; warp < used && j < to; j += 8) {
-    float x[8][8];
+  const int lane = threadIdx.x & 31, pieces = (int)(P.part_cols / kJoinCols);
+  const int64_t items = (int64_t)*P.joins * pieces;
+  for (int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); u < items; u += (int64_t)gridDim.x * kWarps) {
+    const int piece = (int)(u % pieces), chunk = (int)P.joins[1 + u / pieces];
+    const int64_t p1 = (int64_t)(chunk + 1) * P.chunk;
+    const uint32_t k = P.list[p1].x;
+    // a lane's two places among a group's, and their columns
+    const int pos = piece * kJoinCols % kGroupCols + lane * 2;
+    const float* part = part_at(P, chunk, 0, piece * kJoinCols / kGroupCols, 0) + pos;
+    const int64_t step = 2 * P.part_cols;   // to the next chunk's
+    float2 acc = *reinterpret_cast<const float2*>(part + P.part_cols);
+    for (int64_t e = chunk + 1;; e += 32) {
+      // lane i: whether the id goes on past chunk e + i
+      const int64_t after = (e + lane + 1) * P.chunk;
+      const uint32_t stops = __ballot_sync(0xffffffffu, !(after < P.rows && P.list[after].x == k));
+      const int n = stops ? __ffs(stops) : 32;
+      const float* o = part + (e - chunk) * step;
+      for (int j = 0; j < n; j += 16) {
+        float2 x[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (j + i < to) load8(part_at(P, j + i, 0, group, lane), x[i]);
-    }
+        for (int i = 0; i < 16; ++i)
+          if (j + i < n) x[i] = *reinterpret_cast<const float2*>(o + (j + i) * step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (j + i < to) {
-#pragma unroll
-        for (int m = 0; m < 8; ++m) acc[m] += x[i][m];
+        for (int i = 0; i < 16; ++i) {
+          if (j + i < n) {
+            acc.x += x[i].x;
+            acc.y += x[i].y;
+          }
+        }
       }
+      if (stops) break;
+    }
+    U* row = static_cast<U*>(P.d) + (int64_t)k * P.ldd;
+    const float v[2] = {acc.x, acc.y};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = piece * kJoinCols / kGroupCols * kGroupCols + group_col<VEC>((pos + i) / 8, (pos + i) % 8);
+      if (c < P.cols) row[c] = from_f32<U>(ACC ? fmaf(P.scale, v[i], to_f32(row[c])) : P.scale * v[i]);
     }
   }
-  if (used > 1) {
-    store8<true>(&sums[warp][lane * 8], acc);   // (shared memory)
-    __syncthreads();
-  }
-  if (warp) return;
-  for (int w = 1; w < used; ++w) {
-    float x[8];
-    load8(&sums[w][lane * 8], x);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) acc[m] += x[m];
-  }
-  U* row = static_cast<U*>(P.d) + (int64_t)k * P.ldd;
-  float was[8] = {};
-  if constexpr (ACC && !kAddInMemory<U, ACC>) load_group<VEC>(row, c0, P.cols, lane, was);
-  finish<VEC, ACC>(row, P.scale, acc, was, c0, P.cols, lane);
 }
 
 template <class K, class A>
@@ -558,7 +545,7 @@ SortPlan sort_plan(int64_t rows, int64_t vocab) {
   s.tiles = (int)((rows + tile - 1) / tile);
   const bool alone = rows <= kSortAlone;
   s.counts_bytes = alone ? 0 : ((int64_t)s.tiles << s.bits) * 4;
-  s.bytes = (rows * 4 + 255) / 256 * 256 * (alone ? 2 : 4) + (s.counts_bytes + 255) / 256 * 256;
+  s.bytes = (rows * 8 + 255) / 256 * 256 * (alone ? 1 : 2) + (s.counts_bytes + 255) / 256 * 256;
   return s;
 }
 template <int PER>
@@ -571,16 +558,15 @@ cudaError_t sort_pass(const SortKernel& S, cudaStream_t st) {
 }
 }  // namespace
 
-int64_t embedding_backward_workspace(int64_t rows, int64_t vocab) { return sort_plan(rows, vocab).bytes; }
+int64_t embedding_backward_workspace(int64_t rows, int64_t vocab) { return sort_plan(rows, vocab).bytes + 512; }
 
 cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaStream_t st) {
   EmbedBackKernel P = {};
   const SortPlan s = sort_plan(a.rows, a.vocab);
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) {
-    const int64_t list = (a.rows * 4 + 255) / 256 * 256;
-    uint32_t* at[4];
-    for (int i = 0; i < 4; ++i) at[i] = reinterpret_cast<uint32_t*>(h.ws + i * list);
+    const int64_t list = (a.rows * 8 + 255) / 256 * 256;
+    uint2* at[2] = {reinterpret_cast<uint2*>(h.ws), reinterpret_cast<uint2*>(h.ws + list)};
     SortKernel S = {};
     S.ids = a.ids;
     S.vocab = a.vocab;
@@ -588,28 +574,25 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
     S.passes = s.passes;
     S.bits = s.bits;
     S.tiles = s.tiles;
-    S.key = at[0];
-    S.idx = at[1];
+    S.out = at[0];
+    S.joins = reinterpret_cast<uint32_t*>(h.ws + s.bytes);
     if (a.rows <= kSortAlone) {
       e = cudaFuncSetAttribute(ts_sort_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAloneSmem);
       if (e != cudaSuccess) return e;
       e = launch(ts_sort_alone_kernel, 1, kSortThreads, kAloneSmem, S, st);
     } else {
-      S.counts = reinterpret_cast<uint32_t*>(h.ws + 4 * list);
+      S.counts = reinterpret_cast<uint32_t*>(h.ws + 2 * list);
       for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
-        // the last pass ends in the first list
-        const int out = (s.passes - 1 - p) & 1 ? 2 : 0;
-        S.key = at[out];
-        S.idx = at[out + 1];
-        S.key_in = p ? at[2 - out] : nullptr;
-        S.idx_in = p ? at[3 - out] : nullptr;
+        const int out = (s.passes - 1 - p) & 1;   // the last pass ends in the first list
+        S.out = at[out];
+        S.in = p ? at[1 - out] : nullptr;
         S.shift = p * s.bits;
         e = a.rows <= kShortList ? sort_pass<kShortPer>(S, st) : sort_pass<kLongPer>(S, st);
       }
     }
     if (e != cudaSuccess) return e;
-    P.key = at[0];
-    P.idx = at[1];
+    P.list = at[0];
+    P.joins = S.joins;
   }
   P.dy = a.dy.p;
   P.d = a.d.p;
@@ -621,21 +604,21 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   P.scale = a.scale;
   P.groups = (a.cols + kGroupCols - 1) / kGroupCols;
   P.part_cols = (int64_t)P.groups * kGroupCols;
-  P.part = reinterpret_cast<float*>(h.ws + s.bytes);
   if (a.rows > 0) {
     // as many chunks as give every SM some warps, of 4 to 32 tokens, and as the
     // workspace has room for partials
     const int64_t want = a.rows * P.groups / ((int64_t)h.nsm * 16);
-    const int64_t room = (h.ws_bytes - s.bytes) / (P.part_cols * 8);
+    const int64_t room = (h.ws_bytes - s.bytes - 512) / (P.part_cols * 8 + 4);
     P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
     if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))
       P.chunk = room < 2 ? (int)a.rows : (int)((a.rows + room - 1) / room);
     P.chunks = (int)((a.rows + P.chunk - 1) / P.chunk);
+    P.part = reinterpret_cast<float*>(h.ws + s.bytes + ((int64_t)P.chunks * 4 + 4 + 255) / 256 * 256);
     P.units = (int64_t)P.chunks * P.groups;
     P.unit_blocks = (P.units + kWarps - 1) / kWarps;
   }
   const int64_t fill = a.accumulate ? 0 : (a.vocab + kWarps * kFillRows - 1) / (kWarps * kFillRows);
-  if (P.unit_blocks + fill > kMaxGrid || P.units > kMaxGrid) return cudaErrorInvalidConfiguration;
+  if (P.unit_blocks + fill > kMaxGrid) return cudaErrorInvalidConfiguration;
   if (P.unit_blocks + fill == 0) return cudaSuccess;
   return by_type(a.dy, a.d, [&](auto t, auto u, auto vec) {
     using T = decltype(t);
@@ -644,8 +627,9 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
     cudaError_t e = launch(a.accumulate ? ts_embed_sum_kernel<T, U, V, true> : ts_embed_sum_kernel<T, U, V, false>,
                            P.unit_blocks + fill, kThreads, 0, P, st);
     if (e != cudaSuccess || P.chunks < 2) return e;
-    return launch(a.accumulate ? ts_embed_join_kernel<U, V, true> : ts_embed_join_kernel<U, V, false>, P.units,
-                  kThreads, 0, P, st);
+    return launch(a.accumulate ? ts_embed_join_kernel<U, V, true> : ts_embed_join_kernel<U, V, false>,
+                  std::min<int64_t>(4 * h.nsm, (P.chunks * (P.part_cols / kJoinCols) + kWarps - 1) / kWarps), kThreads,
+                  0, P, st);
   });
 }
 
