@@ -13,6 +13,7 @@
 // second kernel adds in order.  Rows of the table that no token uses are zeroed
 // by other blocks of the same launch, which look them up in the sorted list.
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "launch.h"
@@ -66,8 +67,10 @@ __global__ void __launch_bounds__(kThreads) ts_embed_kernel(const __grid_constan
 
 constexpr int kSortThreads = 1024, kSortWarps = 32;
 constexpr int kMaxBits = 9, kMaxBins = 1 << kMaxBits;
-constexpr int kSortAlone = 8192;   // tokens that one block sorts by itself
-// 32-token rounds that a warp takes of a longer list's tile: a short list is
+// Lists that one cluster sorts in one launch, every CTA holding a part of it.
+constexpr int kClusterCtas = 8, kClusterPer = 2;   // CTAs, and 32-token rounds a warp, at most
+constexpr int kClusterList = kClusterCtas * kClusterPer * kSortThreads;
+// 32-token rounds that a warp takes of a longer list's tile: a shorter one is
 // spread over more blocks, a long one has fewer counts that every block adds up.
 constexpr int kShortPer = 2, kLongPer = 8;
 constexpr int64_t kShortList = 1 << 18;
@@ -157,53 +160,80 @@ __device__ __forceinline__ uint32_t warp_offsets(uint32_t* hist, int bins) {
   return sum;
 }
 
-// Up to kSortAlone tokens in one block, every pass through shared memory (a last
-// pass that scatters to global memory took 12 of 22 us for 8192 tokens).
-constexpr int kAlonePer = kSortAlone / kSortThreads;
-constexpr int kAloneSmem = (kSortWarps * kMaxBins + kMaxBins + 32 + 2 * kSortAlone) * 4;
+// Up to kClusterList tokens in one launch: the list lies in the shared memory of
+// a cluster's CTAs, PER * 1024 tokens each, and every pass scatters it there.
+// One CTA by itself took 18 us for 8192 tokens, 16 of it instruction issue, this
+// 10.  65536 tokens in eight CTAs took 29 us; passes in launches of their own (a
+// count and a scatter each, below) 21.
+template <int PER>
+constexpr int kClusterSmem = (2 * PER * kSortThreads + kSortWarps * kMaxBins + 2 * kMaxBins + 32) * 4;
 
-__global__ void __launch_bounds__(kSortThreads, 1) ts_sort_alone_kernel(const __grid_constant__ SortKernel P) {
+template <int PER>
+__global__ void __launch_bounds__(kSortThreads, 1) ts_sort_cluster_kernel(const __grid_constant__ SortKernel P) {
   extern __shared__ __align__(16) uint32_t smem[];
+  constexpr int kPart = PER * kSortThreads;
   uint2* buf = reinterpret_cast<uint2*>(smem);
-  uint32_t* hist = smem + 2 * kSortAlone;
+  uint32_t* hist = smem + 2 * kPart;
   uint32_t* base = hist + kSortWarps * kMaxBins;
-  uint32_t* sums = base + kMaxBins;
+  uint32_t* totals = base + kMaxBins;
+  uint32_t* sums = totals + kMaxBins;
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
-  const int per = (P.rows + kSortThreads - 1) / kSortThreads, first = warp * per * 32;
+  const int cta = (int)cluster_ctarank(), ctas = gridDim.x;
   // a warp's rounds follow each other in the list, so that ranks keep its order
-  uint2 e[kAlonePer];
+  const int part0 = cta * kPart, first = warp * PER * 32, n = min(P.rows - part0, first + PER * 32);
+  uint2 e[PER];
 #pragma unroll
-  for (int r = 0; r < kAlonePer; ++r) {
+  for (int r = 0; r < PER; ++r) {
     const int i = first + r * 32 + lane;
-    e[r] = make_uint2(r < per && i < P.rows ? id_key(P.ids[i], P.vocab) : 0, i);
+    e[r] = make_uint2(i < n ? id_key(P.ids[part0 + i], P.vocab) : 0, part0 + i);
   }
-  if (threadIdx.x == 0) *P.joins = 0;
-  const int n = min(P.rows, first + per * 32);
+  if (cta == 0 && threadIdx.x == 0) *P.joins = 0;
   for (int pass = 0; pass < P.passes; ++pass) {
-    uint32_t digit[kAlonePer], rank[kAlonePer];
+    uint32_t digit[PER], rank[PER];
 #pragma unroll
-    for (int r = 0; r < kAlonePer; ++r) digit[r] = (e[r].x >> (pass * P.bits)) & (bins - 1);
+    for (int r = 0; r < PER; ++r) digit[r] = (e[r].x >> (pass * P.bits)) & (bins - 1);
     warp_ranks(digit, first, n, P.bits, hist + warp * kMaxBins, rank);
     __syncthreads();
-    const uint32_t at = block_exclusive(warp_offsets(hist, bins), sums);
-    if ((int)threadIdx.x < bins) base[threadIdx.x] = at;
+    const uint32_t mine = warp_offsets(hist, bins);
+    if ((int)threadIdx.x < bins) totals[threadIdx.x] = mine;
+    cluster_sync();   // (every CTA has its tokens in registers now)
+    uint32_t before = 0, total = 0;
+    if ((int)threadIdx.x < bins) {
+      const uint32_t at = smem_u32(totals + threadIdx.x);
+#pragma unroll
+      for (int c = 0; c < kClusterCtas; ++c) {
+        if (c >= ctas) break;
+        uint32_t v;
+        asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(at, c)) : "memory");
+        total += v;
+        if (c < cta) before += v;
+      }
+    }
+    const uint32_t at = block_exclusive(total, sums);
+    if ((int)threadIdx.x < bins) base[threadIdx.x] = at + before;
     __syncthreads();
 #pragma unroll
-    for (int r = 0; r < kAlonePer; ++r)
-      if (r < per && first + r * 32 + lane < n)
-        buf[base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r]] = e[r];
-    __syncthreads();
+    for (int r = 0; r < PER; ++r) {
+      if (first + r * 32 + lane < n) {
+        const uint32_t pos = base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r];
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(
+                         cluster_addr(smem_u32(buf + pos % kPart), pos / kPart)),
+                     "r"(e[r].x), "r"(e[r].y)
+                     : "memory");
+      }
+    }
+    cluster_sync();
     if (pass + 1 < P.passes) {
 #pragma unroll
-      for (int r = 0; r < kAlonePer; ++r) {
+      for (int r = 0; r < PER; ++r) {
         const int i = first + r * 32 + lane;
-        if (r < per && i < n) e[r] = buf[i];
+        if (i < n) e[r] = buf[i];
       }
     }
   }
-  for (int i = threadIdx.x; i < P.rows; i += kSortThreads) P.out[i] = buf[i];
+  for (int i = threadIdx.x; i < min(P.rows - part0, kPart); i += kSortThreads) P.out[part0 + i] = buf[i];
 }
 
 // Longer lists: a pass's counts by tile, and the pass.
@@ -363,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_embed_sum_kernel(const __grid_
   const uint32_t vocab = (uint32_t)P.vocab;
   constexpr bool kOld = ACC && !kAddInMemory<U, ACC>;   // what dtable holds is read
   // rows of a batch; one is loaded while one is added
-  constexpr int kU = kOld ? 2 : sizeof(T) == 2 ? 8 : 4;
+  constexpr int kU = kOld ? 2 : VEC && sizeof(T) == 2 ? 8 : 4;
   struct Batch {
     RawGroup<T, VEC> raw[kU];
     RawGroup<U, VEC> old[kOld ? kU : 1];
@@ -500,6 +530,16 @@ cudaError_t by_type(const A& a, const B& b, F f) {
 
 constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
 
+// Allows a kernel its shared memory, once a device.
+template <auto Kernel>
+cudaError_t opt_in(int device, int smem) {
+  static std::atomic<uint64_t> done;
+  if (device < 64 && done.load(std::memory_order_acquire) >> device & 1) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess && device < 64) done.fetch_or(uint64_t(1) << device, std::memory_order_release);
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_embedding(const ts_ops& h, const EmbedArgs& a, cudaStream_t st) {
@@ -543,15 +583,30 @@ SortPlan sort_plan(int64_t rows, int64_t vocab) {
   s.bits = (key_bits + s.passes - 1) / s.passes;
   const int64_t tile = (rows <= kShortList ? kShortPer : kLongPer) * kSortThreads;
   s.tiles = (int)((rows + tile - 1) / tile);
-  const bool alone = rows <= kSortAlone;
+  const bool alone = rows <= kClusterList;
   s.counts_bytes = alone ? 0 : ((int64_t)s.tiles << s.bits) * 4;
   s.bytes = (rows * 8 + 255) / 256 * 256 * (alone ? 1 : 2) + (s.counts_bytes + 255) / 256 * 256;
   return s;
 }
 template <int PER>
-cudaError_t sort_pass(const SortKernel& S, cudaStream_t st) {
+cudaError_t sort_cluster(const ts_ops& h, const SortKernel& S, int ctas, cudaStream_t st) {
+  cudaError_t e = opt_in<ts_sort_cluster_kernel<PER>>(h.device, kClusterSmem<PER>);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = pdl_config(ctas, kSortThreads, kClusterSmem<PER>, st);
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = ctas;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, ts_sort_cluster_kernel<PER>, S);
+}
+template <int PER>
+cudaError_t sort_pass(const ts_ops& h, const SortKernel& S, cudaStream_t st) {
   constexpr int smem = (kSortWarps * kMaxBins + kMaxBins + 32) * 4;
-  cudaError_t e = cudaFuncSetAttribute(ts_sort_pass_kernel<PER>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = opt_in<ts_sort_pass_kernel<PER>>(h.device, smem);
   if (e == cudaSuccess) e = launch(ts_sort_count_kernel<PER>, S.tiles, kSortThreads, 0, S, st);
   if (e == cudaSuccess) e = launch(ts_sort_pass_kernel<PER>, S.tiles, kSortThreads, smem, S, st);
   return e;
@@ -576,10 +631,11 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
     S.tiles = s.tiles;
     S.out = at[0];
     S.joins = reinterpret_cast<uint32_t*>(h.ws + s.bytes);
-    if (a.rows <= kSortAlone) {
-      e = cudaFuncSetAttribute(ts_sort_alone_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAloneSmem);
-      if (e != cudaSuccess) return e;
-      e = launch(ts_sort_alone_kernel, 1, kSortThreads, kAloneSmem, S, st);
+    if (a.rows <= kClusterList) {
+      // (one CTA up to 1024 tokens, then eight of one or two rounds a warp)
+      e = a.rows <= kSortThreads                  ? sort_cluster<1>(h, S, 1, st)
+          : a.rows <= kClusterCtas * kSortThreads ? sort_cluster<1>(h, S, kClusterCtas, st)
+                                                  : sort_cluster<kClusterPer>(h, S, kClusterCtas, st);
     } else {
       S.counts = reinterpret_cast<uint32_t*>(h.ws + 2 * list);
       for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
@@ -587,7 +643,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
         S.out = at[out];
         S.in = p ? at[1 - out] : nullptr;
         S.shift = p * s.bits;
-        e = a.rows <= kShortList ? sort_pass<kShortPer>(S, st) : sort_pass<kLongPer>(S, st);
+        e = a.rows <= kShortList ? sort_pass<kShortPer>(h, S, st) : sort_pass<kLongPer>(h, S, st);
       }
     }
     if (e != cudaSuccess) return e;

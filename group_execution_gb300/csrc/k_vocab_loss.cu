@@ -54,17 +54,39 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kLoss, kDlogits, kGrad };
 
+// Rows of bf16 that are copied to a pitch that TMA can read.  Rows that take no
+// gradient (without a target, or of an lse of -inf) have d = 0 and may hold
+// anything: where targets or lse are given, the copy has them as zeros.
+struct CopyRows {
+  const __nv_bfloat16* src;
+  __nv_bfloat16* dst;
+  int64_t ld, pitch, rows, vocab, units;   // a unit: eight columns of a row
+  int cols;
+  const int64_t* targets;
+  const float* lse;
+};
+
+// Where a gradient goes.
+struct Out {
+  CUtensorMap map;   // [depth, rows, cols]
+  void* p;
+  int64_t ld;
+  int bf16, tma;     // by TMA, or by threads
+  int whole;         // rows end on 16 bytes, the unit that TMA writes
+  int add;           // to what it holds
+};
+
 struct VocabKernel {
   CUtensorMap x, w, d;       // loads: x [rows, cols], w's piece [vocab, cols], d [rows, dpitch]
   CUtensorMap store_d;       // d, in boxes of 64 x 32
-  CUtensorMap store_dx;      // dx's sums [splits, rows, cols] float32
-  CUtensorMap store_dw;      // dw's piece
+  Out out[2];                // dx (its sums [splits, rows, cols] float32, or itself), dw's piece
+  CopyRows copy;             // x for dw, copied beside the first piece's logits
   int rows, cols, vocab;     // vocab: of the piece
   int v0;                    // its first row of w
   int64_t total;             // the whole vocabulary's size
   int tiles_t, tiles_v, tiles_c;
   // forward
-  float2* part;              // [128-column parts][rows]: reference (log2) and sum
+  float2* part;              // [column parts][rows]: reference (log2) and sum
   float* tlogit;             // the target's logit
   const int64_t* targets;
   // backward
@@ -73,12 +95,6 @@ struct VocabKernel {
   const float* g_lse;
   int splits;                // of dx's K
   int nx, nw, late, extra;   // dx and dw items; see item_of
-  int add_dx;                // the piece adds to dx's sums
-  int dw_kind;               // 0 bf16 by TMA, 1 float32 by TMA, 2 by threads
-  int cols_whole;            // dw's rows end on 16 bytes
-  int dw_bf16, accumulate;
-  void* dw;
-  int64_t lddw;
   int32_t* err;
   int64_t wait_limit_ns;
   int inject;
@@ -188,11 +204,62 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, int x, int y, i
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
 }
-__device__ __forceinline__ void tma_add_2d(const CUtensorMap* m, int x, int y, uint32_t src) {
-  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                   reinterpret_cast<uint64_t>(m)),
-               "r"(x), "r"(y), "r"(src)
-               : "memory");
+// Eight elements of a row from column j on, zeros past `cols`: out of the two
+// aligned pieces of 16 bytes that hold them, or one by one where those would
+// reach past the row's ends.
+__device__ __forceinline__ uint4 row_piece(const __nv_bfloat16* row, int j, int cols) {
+  const __nv_bfloat16* s = row + j;
+  const int off = (int)(reinterpret_cast<uintptr_t>(s) % 16 / 2);   // the same for all of a row
+  if (off == 0 && j + 8 <= cols) return __ldcs(reinterpret_cast<const uint4*>(s));
+  if (j < off || j - off + 16 > cols) {
+    __align__(16) __nv_bfloat16 e[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) e[k] = j + k < cols ? s[k] : from_f32<__nv_bfloat16>(0.f);
+    return *reinterpret_cast<const uint4*>(e);
+  }
+  const uint4* q = reinterpret_cast<const uint4*>(s - off);
+  const uint4 a = __ldcs(q), b = __ldcs(q + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  // the elements before the first one drop out: four, two and one of them
+  if (off & 4) {
+#pragma unroll
+    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+  }
+  if (off & 2) {
+#pragma unroll
+    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+  }
+  if (off & 1) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// Copies the rows, 16 bytes a thread: thread `t` of `n`, U pieces in flight.
+template <int U>
+__device__ __forceinline__ void copy_rows(const CopyRows& C, int64_t t, int64_t n) {
+  const int per = (int)(C.pitch / 8);
+  for (int64_t u0 = t; u0 < C.units; u0 += U * n) {
+    uint4 v[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = u0 + k * n, r = u / per;
+      if (u >= C.units) break;
+      bool keep = true;
+      if (C.targets) {
+        const int64_t i = C.targets[r];
+        keep = i >= 0 && i < C.vocab;
+      }
+      if (C.lse && C.lse[r] == -INFINITY) keep = false;
+      v[k] = row_piece(C.src + r * C.ld, (int)(u - r * per) * 8, keep ? C.cols : 0);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t u = u0 + k * n;
+      if (u >= C.units) break;
+      reinterpret_cast<uint4*>(C.dst)[u] = v[k];   // (the copy's rows lie together)
+    }
+  }
 }
 
 // An epilogue warp's 32 rows x 128 bytes on their way out, 128-byte swizzled.
@@ -220,6 +287,24 @@ struct Stage {
                                         bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7])));
   }
 };
+
+// A lane's column of the stage's first n rows, to rows `ld` apart.
+template <class T>
+__device__ __forceinline__ void to_rows(const Stage& stage, T* d, int64_t ld, int n, bool add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r = 0; r < 32; r += 8, d += 8 * ld) {
+    float old[8] = {};
+    if (add) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (r + i < n) old[i] = to_f32(d[i * ld]);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (r + i < n) d[i * ld] = from_f32<T>(old[i] + stage.get(r + i, lane));
+  }
+}
 
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -364,6 +449,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_commit_mask(done_bar, pair_mask);
       mbar_wait(done_bar, 0, kDrainLimitNs);
     }
+  } else if (warp == 3) {
+    if constexpr (MODE == kDlogits) {
+      // ---- x for dw: rows that take no gradient as zeros ----
+      copy_rows<4>(P.copy, blockIdx.x * 32 + lane, gridDim.x * 32);
+    }
   } else if (warp >= 4) {
     // ---- epilogue ----
     const int q = warp & 3, set = (warp - 4) >> 2;   // the TMEM lane quarter this warp may access, its column half
@@ -439,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // the sum's reference is the largest logit, in log2
-        const int left = P.vocab - c0, at = target - c0;
+        const int left = min(kHalf, P.vocab - c0), at = target - c0;
         if (left < kHalf) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -447,7 +537,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c)
               if (32 * j + c >= left) v[j][c] = -INFINITY;
         }
-        if (at >= 0 && at < kHalf) {
+        if (at >= 0 && at < left) {
           float l = 0.f;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -466,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx(fmaf(v[j][c], kLog2e, -ref));
-        if (row < P.rows && left > 0)
+        if (row < P.rows)
           P.part[(int64_t)(c0 / kHalf) * P.rows + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
 #pragma unroll 1
@@ -499,45 +589,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       } else {
-        const bool dx = w.kind == 1;
-        const int m_end = dx ? P.rows : P.vocab;
-        // 32 columns of dw as float32 in the stage, to rows that TMA cannot write
-        // or that bf16 values are added to
+        const Out& out = P.out[w.kind - 1];
+        const int m_end = w.kind == 1 ? P.rows : P.vocab;
+        // 32 columns as float32 in the stage, to rows that TMA cannot write or that
+        // bf16 values are added to
         auto by_threads = [&](int j) {
           __syncwarp();
-          const int col = c0 + j + lane, n = col < P.cols ? min(32, P.vocab - r0) : 0;
-          for (int r = 0; r < n; ++r) {
-            const int64_t at = (int64_t)(r0 + r) * P.lddw + col;
-            const float x = stage.get(r, lane);
-            if (P.dw_bf16) {
-              __nv_bfloat16* d = static_cast<__nv_bfloat16*>(P.dw) + at;
-              *d = __float2bfloat16_rn(P.accumulate ? __bfloat162float(*d) + x : x);
-            } else {
-              float* d = static_cast<float*>(P.dw) + at;
-              *d = P.accumulate ? *d + x : x;
-            }
-          }
+          const int col = c0 + j + lane, n = col < P.cols ? min(32, m_end - r0) : 0;
+          const int64_t at = (int64_t)r0 * out.ld + col;
+          if (out.bf16) to_rows(stage, static_cast<__nv_bfloat16*>(out.p) + at, out.ld, n, out.add);
+          else to_rows(stage, static_cast<float*>(out.p) + at, out.ld, n, out.add);
           __syncwarp();
         };
 #pragma unroll 1
         for (int j = 0; j < kHalf; j += 64) {
-          // TMA writes 16 bytes at a time, past the last column too
-          const bool tma = dx || (P.dw_kind < 2 && (c0 + j + 64 <= P.cols || P.cols_whole));
-          const bool half = !dx && tma && P.dw_kind == 0;   // bf16: both 32 columns in one store
+          const bool tma = out.tma && (out.whole || c0 + j + 64 <= P.cols);
+          const bool both = tma && out.bf16;   // both 32 columns in one store
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (!half || k == 0) stage_free();
+            if (!both || k == 0) stage_free();
             float v[32];
             tmem_ld32(acc + j + 32 * k, v);
             if (j + 64 == kHalf && k == 1) release();
-            if (half) {
+            if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
+#pragma unroll
+              for (int c = 0; c < 32; ++c) v[c] = 0.f;
+            }
+            if (both) {
               stage.put_bf16(lane, k, v);
               if (k == 0) continue;
             } else {
-              if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = 0.f;
-              }
               stage.put_f32(lane, v);
               if (!tma) {
                 by_threads(j + 32 * k);
@@ -545,16 +626,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
             }
             stage_full();
-            const int col = c0 + j + (half ? 0 : 32 * k);
+            const int col = c0 + j + (both ? 0 : 32 * k);
             if (lane == 0) {
               if (r0 < m_end && col < P.cols) {
-                if (!dx) {
-                  if (P.accumulate) tma_add_2d(&P.store_dw, col, r0, stage_u32);
-                  else tma_store_2d(&P.store_dw, col, r0, stage_u32);
-                } else {
-                  if (P.add_dx) tma_add_3d(&P.store_dx, col, r0, w.split, stage_u32);
-                  else tma_store_3d(&P.store_dx, col, r0, w.split, stage_u32);
-                }
+                if (out.add) tma_add_3d(&out.map, col, r0, w.split, stage_u32);
+                else tma_store_3d(&out.map, col, r0, w.split, stage_u32);
               }
               bulk_commit();
             }
@@ -655,42 +731,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ts_loss_join_kernel(const __g
   }
 }
 
-struct RepackKernel {
-  const __nv_bfloat16* src;
-  __nv_bfloat16* dst;
-  int64_t ld, pitch, rows, vocab, units;
-  int cols, groups;
-  const int64_t* targets;   // if not null, rows without a target are zeros
-  const float* lse;         // if not null, rows whose lse is -inf are zeros
-};
-
-// bf16 rows at a pitch that TMA can read.  A row that takes no gradient has d = 0,
-// and may hold anything: dw takes it as zeros.
-template <bool VEC>
-__global__ void __launch_bounds__(256) ts_loss_repack_kernel(const __grid_constant__ RepackKernel P) {
+__global__ void __launch_bounds__(256) ts_loss_copy_kernel(const __grid_constant__ CopyRows C) {
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t u = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (u >= P.units) return;
-  const int64_t r = u / P.groups;
-  const int c0 = (int)(u - r * P.groups) * kGroupCols;
-  bool keep = true;
-  if (P.targets) {
-    const int64_t t = P.targets[r];
-    keep = t >= 0 && t < P.vocab;
-  }
-  if (P.lse && P.lse[r] == -INFINITY) keep = false;
-  __nv_bfloat16* dst = P.dst + r * P.pitch;
-  RawGroup<__nv_bfloat16, VEC> raw;
-  raw.load(P.src + r * P.ld, c0, keep ? P.cols : 0, lane);
-  if constexpr (VEC) {
-    if (c0 + lane * 8 < P.pitch) *reinterpret_cast<uint4*>(dst + c0 + lane * 8) = raw.q[0];
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (c0 + j * 32 + lane < P.pitch) dst[c0 + j * 32 + lane] = raw.e[j];
-  }
+  copy_rows<2>(C, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
 struct DxKernel {
@@ -809,29 +853,33 @@ int64_t round_up(int64_t n, int64_t m) { return (n + m - 1) / m * m; }
 int64_t tiles(int64_t n) { return (n + kTile - 1) / kTile; }
 int64_t pitch_of(int64_t cols) { return round_up(cols, 8); }
 
-// Copies rows of a bf16 matrix to dst at pitch_of(cols); see the kernel.
-cudaError_t repack(const TsMat& m, int64_t row0, int64_t rows, int cols, void* dst, const int64_t* targets,
-                   const float* lse, int64_t vocab, cudaStream_t st) {
-  RepackKernel R = {};
-  R.src = static_cast<const __nv_bfloat16*>(m.p) + row0 * m.ld;
-  R.dst = static_cast<__nv_bfloat16*>(dst);
-  R.ld = m.ld;
-  R.pitch = pitch_of(cols);
-  R.rows = rows;
-  R.vocab = vocab;
-  R.cols = cols;
-  R.groups = (cols + kGroupCols - 1) / kGroupCols;
-  R.units = rows * R.groups;
-  R.targets = targets;
-  R.lse = lse;
-  return launch(rows_aligned(m) ? ts_loss_repack_kernel<true> : ts_loss_repack_kernel<false>, (R.units + 7) / 8, 256, 0,
-                R, st);
+CopyRows copy_of(const TsMat& m, int64_t rows, int cols, void* dst) {
+  CopyRows C = {};
+  C.src = static_cast<const __nv_bfloat16*>(m.p);
+  C.dst = static_cast<__nv_bfloat16*>(dst);
+  C.ld = m.ld;
+  C.pitch = pitch_of(cols);
+  C.rows = rows;
+  C.cols = cols;
+  C.units = rows * (C.pitch / 8);
+  return C;
+}
+cudaError_t launch_copy(const CopyRows& C, cudaStream_t st) {
+  return launch(ts_loss_copy_kernel, (C.units + 511) / 512, 256, 0, C, st);
+}
+// Copies the matrix to `at` and describes the copy.
+cudaError_t copy_aligned(TsMat& m, int64_t rows, int cols, void* at, cudaStream_t st) {
+  const cudaError_t e = launch_copy(copy_of(m, rows, cols, at), st);
+  m.p = at;
+  m.ld = pitch_of(cols);
+  return e;
 }
 
-// The forward pass's workspace for `rows` rows, its copy of w's rows aside.
+// The forward pass's workspace for `rows` rows, its copy of w's rows aside: two
+// parts a tile.
 int64_t forward_bytes(int64_t rows, int64_t cols, int64_t vocab, bool copy_x) {
   return (copy_x ? round_up(rows * pitch_of(cols) * 2, 256) : 0) + round_up(rows * 4, 256) +
-         round_up(rows * ((vocab + kHalf - 1) / kHalf) * 8, 256);
+         round_up(rows * 2 * tiles(vocab) * 8, 256);
 }
 // The backward pass's, d's piece aside, and d's for 256 of the vocabulary.
 int64_t backward_bytes(int64_t rows, int64_t cols, int64_t splits) {
@@ -847,8 +895,10 @@ int64_t vocab_loss_workspace(int64_t rows, int64_t cols, int64_t vocab, bool cop
                              bool whole) {
   if (backward)
     return backward_bytes(rows, cols, 1) + (whole ? tiles(vocab) : 1) * piece_bytes(rows, cols, copy_w);
-  const int64_t r = whole ? rows : std::min<int64_t>(rows, kTile);
-  return forward_bytes(r, cols, vocab, copy_x) + (copy_w ? kTile * pitch_of(cols) * 2 : 0);
+  if (whole)
+    return forward_bytes(rows, cols, vocab, copy_x) + (copy_w ? tiles(vocab) * kTile * pitch_of(cols) * 2 : 0);
+  return forward_bytes(std::min<int64_t>(rows, kTile), cols, vocab, copy_x) +
+         (copy_w ? kTile * pitch_of(cols) * 2 : 0);
 }
 
 cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st) {
@@ -856,36 +906,32 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
   cudaError_t e = resident_pairs(h.device, &pairs);
   if (e != cudaSuccess) return e;
   const bool copy_x = !rows_aligned(a.x), copy_w = !rows_aligned(a.w);
-  const int64_t pitch = pitch_of(a.cols), parts = (a.vocab + kHalf - 1) / kHalf;
-  // as many of w's rows at a time as a quarter of the workspace takes
+  const int64_t pitch = pitch_of(a.cols);
+  // w's rows are copied whole, or as many at a time as half of the workspace takes
   int64_t piece = a.vocab, wbytes = 0;
   if (copy_w) {
-    piece = std::min<int64_t>(tiles(a.vocab), std::max<int64_t>(1, h.ws_bytes / 4 / (kTile * pitch * 2))) * kTile;
+    piece = std::min<int64_t>(tiles(a.vocab), std::max<int64_t>(1, h.ws_bytes / 2 / (kTile * pitch * 2))) * kTile;
     wbytes = piece * pitch * 2;
   }
-  // all rows, or as many as leave w's room
+  // all rows at once, or as many as leave w's room
   int64_t block = a.rows;
   if (forward_bytes(block, a.cols, a.vocab, copy_x) + wbytes > h.ws_bytes) {
-    const int64_t each = forward_bytes(kTile, a.cols, a.vocab, copy_x);
-    block = (h.ws_bytes - wbytes) / each * kTile;
+    block = std::max<int64_t>(0, h.ws_bytes - wbytes) / forward_bytes(kTile, a.cols, a.vocab, copy_x) * kTile;
     if (block < kTile) {   // (room for one tile of each was checked)
       block = kTile;
       piece = kTile;
       wbytes = copy_w ? piece * pitch * 2 : 0;
     }
   }
-  uint8_t* wcopy = h.ws + h.ws_bytes - wbytes;
-  if (wbytes) wcopy = h.ws + (h.ws_bytes - wbytes) / 256 * 256;
+  uint8_t* wcopy = h.ws + h.ws_bytes - wbytes;   // (all of these are multiples of 256)
   for (int64_t t0 = 0; t0 < a.rows; t0 += block) {
     const int64_t rows = std::min(block, a.rows - t0);
     uint8_t* at = h.ws;
     TsMat x = a.x;
     x.p = static_cast<const __nv_bfloat16*>(a.x.p) + t0 * a.x.ld;
     if (copy_x) {
-      e = repack(a.x, t0, rows, a.cols, at, nullptr, nullptr, 0, st);
+      e = copy_aligned(x, rows, a.cols, at, st);
       if (e != cudaSuccess) return e;
-      x.p = at;
-      x.ld = pitch;
       at += round_up(rows * pitch * 2, 256);
     }
     JoinKernel J = {};
@@ -897,7 +943,6 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
     J.lse = a.lse ? a.lse + t0 : nullptr;
     J.vocab = a.vocab;
     J.rows = (int)rows;
-    J.parts = (int)parts;
     VocabKernel P = {};
     P.rows = (int)rows;
     P.cols = a.cols;
@@ -915,17 +960,16 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
       TsMat w = a.w;
       w.p = static_cast<const __nv_bfloat16*>(a.w.p) + v0 * a.w.ld;
       if (copy_w) {
-        e = repack(a.w, v0, nv, a.cols, wcopy, nullptr, nullptr, 0, st);
+        e = copy_aligned(w, nv, a.cols, wcopy, st);
         if (e != cudaSuccess) return e;
-        w.p = wcopy;
-        w.ld = pitch;
       }
       e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
       if (e != cudaSuccess) return e;
       P.vocab = (int)nv;
       P.v0 = (int)v0;
       P.tiles_v = (int)tiles(nv);
-      P.part = const_cast<float2*>(J.part) + v0 / kHalf * rows;
+      P.part = const_cast<float2*>(J.part) + J.parts * rows;
+      J.parts += 2 * P.tiles_v;
       const int64_t items = (int64_t)P.tiles_t * P.tiles_v;
       e = launch(ts_vocab_kernel<kLoss>, 2 * std::min<int64_t>(pairs, items), kThreads, kSmem, P, st);
       if (e != cudaSuccess) return e;
@@ -951,23 +995,22 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
                      : cudaLaunchKernelEx(&cfg, ts_loss_zero_kernel<float>, static_cast<float*>(a.dw.p), a.dw.ld,
                                           (int)a.vocab, a.cols);
   }
-  const bool copy_w = !rows_aligned(a.w);
+  const bool copy_x = !rows_aligned(a.x), copy_w = !rows_aligned(a.w);
   const int64_t pitch = pitch_of(a.cols), tiles_t = tiles(a.rows), tiles_c = tiles(a.cols), tiles_v = tiles(a.vocab);
-  // dx of few rows is cut along the vocabulary, so that every pair has a part
+  // dx of few rows is cut along the vocabulary, so that every pair has a part,
+  // where that saves more blocks of K than the sums' own kernel costs
   const int64_t one_dx = a.rows * pitch * 4, cost = piece_bytes(a.rows, a.cols, copy_w);
   int64_t splits = std::min<int64_t>(pairs / (tiles_t * tiles_c), tiles_v / 2);
   splits = std::min<int64_t>(splits, (h.ws_bytes / 2 - round_up(a.rows * pitch * 2, 256)) / one_dx);
   while (splits > 1 && backward_bytes(a.rows, a.cols, splits) + cost > h.ws_bytes) --splits;
-  splits = std::max<int64_t>(splits, 1);
+  if (splits < 2 || 2 * tiles_v - 2 * tiles_v / splits < 6) splits = 1;
   // equal pieces of the vocabulary, as few as the workspace allows
   const int64_t most = std::max<int64_t>(1, (h.ws_bytes - backward_bytes(a.rows, a.cols, splits)) / cost);
   const int64_t pieces = (tiles_v + most - 1) / most, piece = (tiles_v + pieces - 1) / pieces * kTile;
-  __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(h.ws);
+  uint8_t* xcopy = h.ws;
   float* sums = reinterpret_cast<float*>(h.ws + round_up(a.rows * pitch * 2, 256));
   uint8_t* d = h.ws + backward_bytes(a.rows, a.cols, splits);
   uint8_t* wcopy = d + a.rows * piece * 2;
-  e = repack(a.x, 0, a.rows, a.cols, x, a.g_lse ? nullptr : a.targets, a.lse, a.vocab, st);
-  if (e != cudaSuccess) return e;
   VocabKernel P = {};
   P.rows = (int)a.rows;
   P.cols = a.cols;
@@ -979,41 +1022,68 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   P.g_loss = a.g_loss;
   P.g_lse = a.g_lse;
   P.splits = (int)splits;
-  P.accumulate = a.accumulate;
-  P.dw_bf16 = a.dw.bf16;
-  P.lddw = a.dw.ld;
-  P.dw_kind = !rows_aligned(a.dw) || (a.dw.bf16 && a.accumulate) ? 2 : a.dw.bf16 ? 0 : 1;
-  P.cols_whole = a.cols * a.dw.elem() % 16 == 0;
   P.err = h.err;
   P.wait_limit_ns = h.wait_limit_ns;
   P.inject = h.inject;
-  e = make_map(&P.x, x, 1, a.cols, a.rows, pitch, 64, kHalf);
-  if (e == cudaSuccess) e = make_map(&P.store_dx, sums, 0, a.cols, a.rows, pitch, 32, 32, 3, splits);
+  // dw's copy of x: beside the first piece's logits, or before them where TMA
+  // cannot read x itself
+  TsMat x = a.x;
+  CopyRows C = copy_of(a.x, a.rows, a.cols, xcopy);
+  C.targets = a.g_lse ? nullptr : a.targets;
+  C.lse = a.lse;
+  C.vocab = a.vocab;
+  if (copy_x) {
+    e = launch_copy(C, st);
+    if (e != cudaSuccess) return e;
+    x.p = xcopy;
+    x.ld = pitch;
+  } else if (a.dw.p) {
+    P.copy = C;
+  }
+  auto describe = [](Out& o, const TsOut& m, int64_t rows, int cols, bool add) {
+    o.p = m.p;
+    o.ld = m.ld;
+    o.bf16 = m.bf16;
+    o.add = add;
+    o.tma = rows_aligned(m) && !(m.bf16 && add);
+    o.whole = cols * m.elem() % 16 == 0;
+    return o.tma ? make_map(&o.map, m.p, m.bf16, cols, rows, m.ld, m.bf16 ? 64 : 32, 32, 3) : cudaSuccess;
+  };
+  // one piece that is not cut is dx itself
+  const bool direct = splits == 1 && pieces == 1;
+  if (a.dx.p) {
+    if (direct) {
+      e = describe(P.out[0], a.dx, a.rows, a.cols, false);
+    } else {
+      P.out[0].tma = P.out[0].whole = 1;
+      e = make_map(&P.out[0].map, sums, 0, a.cols, a.rows, pitch, 32, 32, 3, splits);
+    }
+  }
   for (int64_t v0 = 0; v0 < a.vocab && e == cudaSuccess; v0 += piece) {
     const int64_t nv = std::min(piece, a.vocab - v0), dpitch = tiles(nv) * kTile;
     TsMat w = a.w;
     w.p = static_cast<const __nv_bfloat16*>(a.w.p) + v0 * a.w.ld;
     if (copy_w) {
-      e = repack(a.w, v0, nv, a.cols, wcopy, nullptr, nullptr, 0, st);
+      e = copy_aligned(w, nv, a.cols, wcopy, st);
       if (e != cudaSuccess) return e;
-      w.p = wcopy;
-      w.ld = pitch;
     }
     P.vocab = (int)nv;
     P.v0 = (int)v0;
+    P.out[0].add = v0 > 0;
     P.tiles_v = (int)tiles(nv);
-    P.add_dx = v0 > 0;
-    e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
-    if (e == cudaSuccess) e = make_map(&P.d, d, 1, dpitch, a.rows, dpitch, 64, kHalf);
+    e = make_map(&P.x, x.p, 1, a.cols, a.rows, x.ld, 64, kHalf);
+    if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
     if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
-    if (a.dw.p) {
-      uint8_t* dw = static_cast<uint8_t*>(a.dw.p) + v0 * a.dw.ld * a.dw.elem();
-      P.dw = dw;
-      if (P.dw_kind < 2 && e == cudaSuccess)
-        e = make_map(&P.store_dw, dw, a.dw.bf16, a.cols, nv, a.dw.ld, a.dw.bf16 ? 64 : 32, 32);
-    }
     if (e != cudaSuccess) return e;
     e = launch(ts_vocab_kernel<kDlogits>, 2 * std::min<int64_t>(pairs, tiles_t * P.tiles_v), kThreads, kSmem, P, st);
+    P.copy.units = 0;
+    if (e == cudaSuccess && a.dw.p) {
+      TsOut dw = a.dw;
+      dw.p = static_cast<uint8_t*>(a.dw.p) + v0 * a.dw.ld * a.dw.elem();
+      e = describe(P.out[1], dw, nv, a.cols, a.accumulate);
+      if (e == cudaSuccess) e = make_map(&P.x, xcopy, 1, a.cols, a.rows, pitch, 64, kHalf);
+    }
+    if (e == cudaSuccess) e = make_map(&P.d, d, 1, dpitch, a.rows, dpitch, 64, kHalf);
     if (e != cudaSuccess) return e;
     P.nx = a.dx.p ? (int)(tiles_t * tiles_c * splits) : 0;
     P.nw = a.dw.p ? (int)(P.tiles_v * tiles_c) : 0;
@@ -1024,6 +1094,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
     P.extra = P.late ? (int)((cost_x + cost_w / 2) / cost_w) : 0;
     e = launch(ts_vocab_kernel<kGrad>, 2 * np, kThreads, kSmem, P, st);
   }
+  if (direct) return e;
   if (e != cudaSuccess || !a.dx.p) return e;
   DxKernel D = {};
   D.sums = sums;

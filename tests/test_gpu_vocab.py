@@ -106,7 +106,8 @@ def test_embedding_row_of_no_finite_value_stays_where_it_is(ops):
 BACK = [(1, 1, 1, "plain"), (1, 300, 5, "none"), (7, 17, 3, "mixed"), (64, 256, 100, "mixed"), (512, 256, 4000, "plain"),
         (1025, 33, 600, "mixed"), (1000, 1003, 70, "mixed"), (5000, 264, 50001, "mixed"), (8192, 40, 131072, "plain"),
         (8193, 64, 300, "mixed"), (20000, 72, 131072, "mixed"), (30001, 40, 1000000, "mixed"), (3000, 520, 9, "one"),
-        (40000, 32, 100, "one"), (9000, 24, 77, "none"), (700, 5003, 513, "plain"), (3, 70001, 4, "mixed")]
+        (40000, 32, 100, "one"), (9000, 24, 77, "none"),
+        (65536, 16, 50001, "mixed"), (65537, 16, 70000, "mixed"), (300001, 8, 131072, "mixed"), (300000, 8, 400, "plain"), (700, 5003, 513, "plain"), (3, 70001, 4, "mixed")]
 
 
 @pytest.mark.parametrize("accumulate", [False, True])
