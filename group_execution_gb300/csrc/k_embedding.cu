@@ -661,9 +661,12 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   P.groups = (a.cols + kGroupCols - 1) / kGroupCols;
   P.part_cols = (int64_t)P.groups * kGroupCols;
   if (a.rows > 0) {
-    // as many chunks as give every SM some warps, of 4 to 32 tokens, and as the
-    // workspace has room for partials
-    const int64_t want = a.rows * P.groups / ((int64_t)h.nsm * 16);
+    // as many warps as are resident at once (two blocks an SM), or that many
+    // several times over, so that no SM idles at the end: 4 to 32 tokens a chunk;
+    // fewer, longer ones where the workspace has no room for so many partials
+    const int64_t all = a.rows * P.groups, resident = (int64_t)h.nsm * 2 * kWarps;
+    const int64_t times = std::max<int64_t>(1, (all + resident * 32 - 1) / (resident * 32));
+    const int64_t want = (all + resident * times - 1) / (resident * times);
     const int64_t room = (h.ws_bytes - s.bytes - 512) / (P.part_cols * 8 + 4);
     P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
     if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))

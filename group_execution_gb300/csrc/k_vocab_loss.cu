@@ -36,6 +36,7 @@
 
 #include "launch.h"
 #include "ts_device.cuh"
+#include "vocab.cuh"
 
 namespace fg {
 namespace {
@@ -50,21 +51,8 @@ constexpr int kSlots = 3;
 constexpr int kStageBytes = 32 * 128;            // an epilogue warp's rows on their way out
 constexpr int kThreads = 12 * 32;
 constexpr int kSmem = kSlots * kSlotBytes + 8 * kStageBytes + 1024;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 enum Mode { kLoss, kDlogits, kGrad };
-
-// Rows of bf16 that are copied to a pitch that TMA can read.  Rows that take no
-// gradient (without a target, or of an lse of -inf) have d = 0 and may hold
-// anything: where targets or lse are given, the copy has them as zeros.
-struct CopyRows {
-  const __nv_bfloat16* src;
-  __nv_bfloat16* dst;
-  int64_t ld, pitch, rows, vocab, units;   // a unit: eight columns of a row
-  int cols;
-  const int64_t* targets;
-  const float* lse;
-};
 
 // Where a gradient goes.
 struct Out {
@@ -84,6 +72,8 @@ struct VocabKernel {
   int rows, cols, vocab;     // vocab: of the piece
   int v0;                    // its first row of w
   int64_t total;             // the whole vocabulary's size
+  int tile_n;                // columns of a tile of the logits
+  int box_rows;              // rows of x's and d's boxes: 128, or as many 16s as there are rows
   int tiles_t, tiles_v, tiles_c;
   // forward
   float2* part;              // [column parts][rows]: reference (log2) and sum
@@ -94,7 +84,8 @@ struct VocabKernel {
   const float* g_loss;
   const float* g_lse;
   int splits;                // of dx's K
-  int nx, nw, late, extra;   // dx and dw items; see item_of
+  int nx, nw;                // dx and dw items
+  int dw_first, late, extra; // which are longer, and how the others follow; see item_of
   int32_t* err;
   int64_t wait_limit_ns;
   int inject;
@@ -129,17 +120,26 @@ __device__ __forceinline__ Item item_of(const VocabKernel& P, int pair, int npai
     const int per = kRowGroup * P.tiles_v, g = (int)(x / per), r = (int)(x - (int64_t)g * per);
     const int gm = min(kRowGroup, P.tiles_t - g * kRowGroup);
     w.m0 = (g * kRowGroup + r % gm) * kTile;
-    w.n0 = r / gm * kTile;
+    w.n0 = r / gm * P.tile_n;
     w.K = P.cols;
     w.kb1 = (P.cols + kKB - 1) / kKB;
     return w;
   } else {
-    // dx's long items first, one after the other over all pairs; where their
-    // last round leaves pairs free, those take `extra` items of dw before the
-    // others join them
-    const int mine = pair < P.nx ? (P.nx - pair + npair - 1) / npair : 0;
-    if (k < mine) {
-      const int x = pair + k * npair, per = P.tiles_t * P.tiles_c, r = x % per;
+    // the longer kind's items first, one after the other over all pairs; where
+    // their last round leaves pairs free, those take `extra` items of the other
+    // kind before the rest join them
+    const int n1 = P.dw_first ? P.nw : P.nx, n2 = P.dw_first ? P.nx : P.nw;
+    const int mine = pair < n1 ? (n1 - pair + npair - 1) / npair : 0;
+    const bool second = k >= mine;
+    int x = pair + k * npair;
+    if (second) {
+      const int j = k - mine, early = npair - P.late;
+      if (pair >= P.late && j < P.extra) x = pair - P.late + j * early;
+      else x = P.extra * early + pair + (pair >= P.late ? j - P.extra : j) * npair;
+      if (x >= n2) return Item{-1};
+    }
+    if (second == (P.dw_first != 0)) {
+      const int per = P.tiles_t * P.tiles_c, r = x % per;
       w.kind = 1;
       w.split = x / per;
       w.m0 = r / P.tiles_c * kTile;
@@ -150,11 +150,6 @@ __device__ __forceinline__ Item item_of(const VocabKernel& P, int pair, int npai
       w.K = P.vocab;
       return w;
     }
-    const int j = k - mine, early = npair - P.late;
-    int x;
-    if (pair >= P.late && j < P.extra) x = pair - P.late + j * early;
-    else x = P.extra * early + pair + (pair >= P.late ? j - P.extra : j) * npair;
-    if (x >= P.nw) return Item{-1};
     w.kind = 2;
     w.m0 = x / P.tiles_c * kTile;
     w.n0 = x % P.tiles_c * kTile;
@@ -173,11 +168,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, int64_t 
 }
 __device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ float exp2_approx(float v) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-  return r;
 }
 // 16 consecutive f32 columns of this warp's 32 lanes of tensor memory.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
@@ -204,64 +194,6 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, int x, int y, i
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
 }
-// Eight elements of a row from column j on, zeros past `cols`: out of the two
-// aligned pieces of 16 bytes that hold them, or one by one where those would
-// reach past the row's ends.
-__device__ __forceinline__ uint4 row_piece(const __nv_bfloat16* row, int j, int cols) {
-  const __nv_bfloat16* s = row + j;
-  const int off = (int)(reinterpret_cast<uintptr_t>(s) % 16 / 2);   // the same for all of a row
-  if (off == 0 && j + 8 <= cols) return __ldcs(reinterpret_cast<const uint4*>(s));
-  if (j < off || j - off + 16 > cols) {
-    __align__(16) __nv_bfloat16 e[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) e[k] = j + k < cols ? s[k] : from_f32<__nv_bfloat16>(0.f);
-    return *reinterpret_cast<const uint4*>(e);
-  }
-  const uint4* q = reinterpret_cast<const uint4*>(s - off);
-  const uint4 a = __ldcs(q), b = __ldcs(q + 1);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  // the elements before the first one drop out: four, two and one of them
-  if (off & 4) {
-#pragma unroll
-    for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
-  }
-  if (off & 2) {
-#pragma unroll
-    for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
-  }
-  if (off & 1) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-// Copies the rows, 16 bytes a thread: thread `t` of `n`, U pieces in flight.
-template <int U>
-__device__ __forceinline__ void copy_rows(const CopyRows& C, int64_t t, int64_t n) {
-  const int per = (int)(C.pitch / 8);
-  for (int64_t u0 = t; u0 < C.units; u0 += U * n) {
-    uint4 v[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int64_t u = u0 + k * n, r = u / per;
-      if (u >= C.units) break;
-      bool keep = true;
-      if (C.targets) {
-        const int64_t i = C.targets[r];
-        keep = i >= 0 && i < C.vocab;
-      }
-      if (C.lse && C.lse[r] == -INFINITY) keep = false;
-      v[k] = row_piece(C.src + r * C.ld, (int)(u - r * per) * 8, keep ? C.cols : 0);
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int64_t u = u0 + k * n;
-      if (u >= C.units) break;
-      reinterpret_cast<uint4*>(C.dst)[u] = v[k];   // (the copy's rows lie together)
-    }
-  }
-}
-
 // An epilogue warp's 32 rows x 128 bytes on their way out, 128-byte swizzled.
 struct Stage {
   uint8_t* p;
@@ -322,6 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const bool leader = h == 0;
   const uint16_t pair_mask = 3u;
   const int npair = gridDim.x / 2, pair = blockIdx.x / 2;
+  const int half_n = MODE == kGrad ? kHalf : P.tile_n / 2;   // columns of B that a CTA stages, and of an epilogue set
   if (threadIdx.x == 0) {
     abort_flag = issued[0] = issued[1] = 0;
     for (int s = 0; s < kSlots; ++s) {
@@ -366,13 +299,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           map = isA ? &P.x : &P.w;
           mn = false;
         }
-        const int o = (isA ? w.m0 : w.n0) + h * kHalf;
+        const int o = isA ? w.m0 + h * kHalf : w.n0 + h * half_n;
+        // a slot's rows: x's or d's boxes, and w's
+        const int slot_rows = MODE != kGrad ? P.box_rows + half_n : w.kind == 1 ? P.box_rows + kHalf : 2 * P.box_rows;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
           }
-          if (leader && isA) mbar_expect_tx(full0 + 8 * s, 2 * kSlotBytes);
+          if (leader && isA) mbar_expect_tx(full0 + 8 * s, 2 * slot_rows * 256);
           const uint32_t dst = dst0 + s * kSlotBytes, cbar = cbar0 + 8 * s;
           tma_load_2d_pair(dst, map, mn ? o : kb * kKB, mn ? kb * kKB : o, cbar, keep);
           tma_load_2d_pair(dst + kBoxBytes, map, (mn ? o : kb * kKB) + 64, mn ? kb * kKB : o, cbar, keep);
@@ -403,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // on, 16 of K 2 KB on.  K-major: atoms of 8 rows x 64 of K, 16 of K 32
         // bytes on, the second 64 of K one box on.
         const bool a_mn = MODE == kGrad && w.kind == 2, b_mn = MODE == kGrad;
-        const uint32_t idesc = idesc_bf16_f32(kTile, kTile, a_mn, b_mn);
+        const uint32_t idesc = idesc_bf16_f32(kTile, 2 * half_n, a_mn, b_mn);
         const uint64_t ad0 = smem_desc_sw128(base, a_mn ? kBoxBytes : 16, 1024),
                        bd0 = smem_desc_sw128(base + kOperandBytes, b_mn ? kBoxBytes : 16, 1024);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
@@ -465,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const Item w = item_of<MODE>(P, pair, npair, k);
       if (w.kind < 0) break;
       const int r0 = w.m0 + h * kHalf + q * 32, row = r0 + lane;
-      const int c0 = w.n0 + set * kHalf;   // this warp's first column
+      const int c0 = w.n0 + set * half_n;   // this warp's first column
       float lse2 = 0.f, coef = 0.f, g = 0.f;
       int target = -1;   // the target's column of the piece
       if constexpr (MODE != kGrad) {
@@ -487,7 +422,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int b = i & 1;
         ok = __all_sync(0xffffffffu, wait_bar(tfull0 + 8 * b, (i >> 1) & 1, P.wait_limit_ns, &abort_flag));
         tc_fence_after();
-        acc = tmem + ((uint32_t)(q * 32) << 16) + b * kTile + set * kHalf;
+        acc = tmem + ((uint32_t)(q * 32) << 16) + b * kTile + set * half_n;
         return ok;
       };
       auto release = [&]() {
@@ -529,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
         // the sum's reference is the largest logit, in log2
-        const int left = min(kHalf, P.vocab - c0), at = target - c0;
+        const int left = min(half_n, P.vocab - c0), at = target - c0;
         if (left < kHalf) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -557,16 +492,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx(fmaf(v[j][c], kLog2e, -ref));
         if (row < P.rows)
-          P.part[(int64_t)(c0 / kHalf) * P.rows + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
 #pragma unroll 1
-        for (int j = 0; j < kHalf; j += 64) {
+        for (int j = 0; j < half_n; j += 64) {
           stage_free();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float v[32];
             tmem_ld32(acc + j + 32 * k, v);
-            if (j + 64 == kHalf && k == 1) release();
+            if (j + 64 == half_n && k == 1) release();
             const int cc = c0 + j + 32 * k, left = P.vocab - cc, at = target - cc;
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = coef * exp2_approx(fmaf(v[c], kLog2e, -lse2));
@@ -875,11 +810,50 @@ cudaError_t copy_aligned(TsMat& m, int64_t rows, int cols, void* at, cudaStream_
   return e;
 }
 
+// The logits' tiles are half as wide where that still leaves a pair without one.
+// (512 x 1024 x 4000, backward: 28 us, with the wider tiles 33.)
+int logits_width(int64_t tiles_t, int64_t vocab, int pairs) {
+  return tiles_t * ((vocab + kHalf - 1) / kHalf) <= pairs ? kHalf : kTile;
+}
+// Rows of the boxes of x and d: past the last row TMA would fill with zeros,
+// which takes as long as reading.
+int box_rows(int64_t rows) { return (int)std::min<int64_t>(kHalf, round_up(rows, 16)); }
+
+// An item of dw takes at least about three blocks of K for its epilogue.
+int64_t dw_blocks(int64_t rows) { return std::max<int64_t>(3, (rows + kKB - 1) / kKB); }
+
+// How nx items of dx of cx blocks of K each and nw of dw of cw share `pairs`
+// pairs (see item_of), and how many blocks the last one ends after, an item's
+// start and end being about one.
+struct Schedule {
+  int dw_first, late, extra;
+  int64_t blocks;
+};
+Schedule schedule(int64_t nx, int64_t cx, int64_t nw, int64_t cw, int pairs) {
+  Schedule s = {};
+  ++cx;
+  ++cw;
+  s.dw_first = cw > cx;
+  if (s.dw_first) {
+    std::swap(nx, nw);
+    std::swap(cx, cw);
+  }
+  s.late = (int)(nx % pairs);
+  s.extra = s.late ? (int)((cx + cw / 2) / cw) : 0;
+  const int64_t rounds = nx / pairs, early = pairs - s.late, ahead = std::min<int64_t>(nw, early * s.extra);
+  const int64_t both = (nw - ahead) / pairs, rest = (nw - ahead) % pairs;   // items of all pairs
+  // a late pair's, and an early one's: the pairs that come first take the rest
+  const int64_t late = s.late ? rounds * cx + cx + (both + (rest > 0)) * cw : 0;
+  const int64_t first = rounds * cx + ((ahead + early - 1) / early + both + (rest > s.late)) * cw;
+  s.blocks = std::max(late, first);
+  return s;
+}
+
 // The forward pass's workspace for `rows` rows, its copy of w's rows aside: two
-// parts a tile.
+// parts a tile, and tiles of half the width.
 int64_t forward_bytes(int64_t rows, int64_t cols, int64_t vocab, bool copy_x) {
   return (copy_x ? round_up(rows * pitch_of(cols) * 2, 256) : 0) + round_up(rows * 4, 256) +
-         round_up(rows * 2 * tiles(vocab) * 8, 256);
+         round_up(rows * 4 * tiles(vocab) * 8, 256);
 }
 // The backward pass's, d's piece aside, and d's for 256 of the vocabulary.
 int64_t backward_bytes(int64_t rows, int64_t cols, int64_t splits) {
@@ -902,6 +876,7 @@ int64_t vocab_loss_workspace(int64_t rows, int64_t cols, int64_t vocab, bool cop
 }
 
 cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStream_t st) {
+  if (few_rows(a)) return launch_few_loss(h, a, st);
   int pairs = 0;
   cudaError_t e = resident_pairs(h.device, &pairs);
   if (e != cudaSuccess) return e;
@@ -948,12 +923,13 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
     P.cols = a.cols;
     P.total = a.vocab;
     P.tiles_t = (int)tiles(rows);
+    P.box_rows = box_rows(rows);
     P.tlogit = const_cast<float*>(J.tlogit);
     P.targets = a.loss ? J.targets : nullptr;
     P.err = h.err;
     P.wait_limit_ns = h.wait_limit_ns;
     P.inject = h.inject;
-    e = make_map(&P.x, x.p, 1, a.cols, rows, x.ld, 64, kHalf);
+    e = make_map(&P.x, x.p, 1, a.cols, rows, x.ld, 64, P.box_rows);
     if (e != cudaSuccess) return e;
     for (int64_t v0 = 0; v0 < a.vocab; v0 += piece) {
       const int64_t nv = std::min(piece, a.vocab - v0);
@@ -963,11 +939,12 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
         e = copy_aligned(w, nv, a.cols, wcopy, st);
         if (e != cudaSuccess) return e;
       }
-      e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
-      if (e != cudaSuccess) return e;
       P.vocab = (int)nv;
       P.v0 = (int)v0;
-      P.tiles_v = (int)tiles(nv);
+      P.tile_n = logits_width(P.tiles_t, nv, pairs);
+      P.tiles_v = (int)((nv + P.tile_n - 1) / P.tile_n);
+      e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, P.tile_n / 2);
+      if (e != cudaSuccess) return e;
       P.part = const_cast<float2*>(J.part) + J.parts * rows;
       J.parts += 2 * P.tiles_v;
       const int64_t items = (int64_t)P.tiles_t * P.tiles_v;
@@ -995,15 +972,26 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
                      : cudaLaunchKernelEx(&cfg, ts_loss_zero_kernel<float>, static_cast<float*>(a.dw.p), a.dw.ld,
                                           (int)a.vocab, a.cols);
   }
-  const bool copy_x = !rows_aligned(a.x), copy_w = !rows_aligned(a.w);
+  bool copy_x = !rows_aligned(a.x);
+  const bool copy_w = !rows_aligned(a.w);
   const int64_t pitch = pitch_of(a.cols), tiles_t = tiles(a.rows), tiles_c = tiles(a.cols), tiles_v = tiles(a.vocab);
-  // dx of few rows is cut along the vocabulary, so that every pair has a part,
-  // where that saves more blocks of K than the sums' own kernel costs
+  // dx's items are cut along the vocabulary where that shortens the gradients'
+  // launch by more than the sums' own kernel costs (about six blocks of K)
   const int64_t one_dx = a.rows * pitch * 4, cost = piece_bytes(a.rows, a.cols, copy_w);
-  int64_t splits = std::min<int64_t>(pairs / (tiles_t * tiles_c), tiles_v / 2);
-  splits = std::min<int64_t>(splits, (h.ws_bytes / 2 - round_up(a.rows * pitch * 2, 256)) / one_dx);
-  while (splits > 1 && backward_bytes(a.rows, a.cols, splits) + cost > h.ws_bytes) --splits;
-  if (splits < 2 || 2 * tiles_v - 2 * tiles_v / splits < 6) splits = 1;
+  // (as if dw were wanted too: dx does not depend on whether it is)
+  const int64_t nkb = (a.vocab + kKB - 1) / kKB, nw = tiles_v * tiles_c;
+  int64_t splits = 1, least = INT64_MAX;
+  for (int64_t n = 1; n <= std::min<int64_t>(64, std::max<int64_t>(1, tiles_v / 2)); ++n) {
+    if (n > 1 && (round_up(a.rows * pitch * 2, 256) + n * one_dx > h.ws_bytes / 2 ||
+                  backward_bytes(a.rows, a.cols, n) + cost > h.ws_bytes))
+      break;
+    const Schedule s = schedule(tiles_t * tiles_c * n, (nkb + n - 1) / n, nw, dw_blocks(a.rows), pairs);
+    const int64_t t = s.blocks + (n > 1 ? 6 + one_dx * n / (int64_t(4) << 20) : 0);
+    if (t < least) {
+      least = t;
+      splits = n;
+    }
+  }
   // equal pieces of the vocabulary, as few as the workspace allows
   const int64_t most = std::max<int64_t>(1, (h.ws_bytes - backward_bytes(a.rows, a.cols, splits)) / cost);
   const int64_t pieces = (tiles_v + most - 1) / most, piece = (tiles_v + pieces - 1) / pieces * kTile;
@@ -1017,6 +1005,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   P.total = a.vocab;
   P.tiles_t = (int)tiles_t;
   P.tiles_c = (int)tiles_c;
+  P.box_rows = box_rows(a.rows);
   P.targets = a.targets;
   P.lse = a.lse;
   P.g_loss = a.g_loss;
@@ -1032,7 +1021,11 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   C.targets = a.g_lse ? nullptr : a.targets;
   C.lse = a.lse;
   C.vocab = a.vocab;
-  if (copy_x) {
+  const bool few = few_rows(a) && pieces == 1;   // (their logits take rows as they lie)
+  if (few) {
+    copy_x = false;
+    if (!a.dw.p) C.units = 0;
+  } else if (copy_x) {
     e = launch_copy(C, st);
     if (e != cudaSuccess) return e;
     x.p = xcopy;
@@ -1070,28 +1063,35 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
     P.vocab = (int)nv;
     P.v0 = (int)v0;
     P.out[0].add = v0 > 0;
-    P.tiles_v = (int)tiles(nv);
-    e = make_map(&P.x, x.p, 1, a.cols, a.rows, x.ld, 64, kHalf);
-    if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
-    if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
-    if (e != cudaSuccess) return e;
-    e = launch(ts_vocab_kernel<kDlogits>, 2 * std::min<int64_t>(pairs, tiles_t * P.tiles_v), kThreads, kSmem, P, st);
-    P.copy.units = 0;
+    if (few) {
+      e = launch_few_dlogits(h, a, C, reinterpret_cast<__nv_bfloat16*>(d), dpitch, st);
+    } else {
+      P.tile_n = logits_width(tiles_t, nv, pairs);
+      P.tiles_v = (int)((nv + P.tile_n - 1) / P.tile_n);
+      e = make_map(&P.x, x.p, 1, a.cols, a.rows, x.ld, 64, P.box_rows);
+      if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, P.tile_n / 2);
+      if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
+      if (e != cudaSuccess) return e;
+      e = launch(ts_vocab_kernel<kDlogits>, 2 * std::min<int64_t>(pairs, tiles_t * P.tiles_v), kThreads, kSmem, P, st);
+      P.copy.units = 0;
+    }
     if (e == cudaSuccess && a.dw.p) {
       TsOut dw = a.dw;
       dw.p = static_cast<uint8_t*>(a.dw.p) + v0 * a.dw.ld * a.dw.elem();
       e = describe(P.out[1], dw, nv, a.cols, a.accumulate);
-      if (e == cudaSuccess) e = make_map(&P.x, xcopy, 1, a.cols, a.rows, pitch, 64, kHalf);
+      if (e == cudaSuccess) e = make_map(&P.x, xcopy, 1, a.cols, a.rows, pitch, 64, P.box_rows);
     }
-    if (e == cudaSuccess) e = make_map(&P.d, d, 1, dpitch, a.rows, dpitch, 64, kHalf);
+    if (e == cudaSuccess) e = make_map(&P.d, d, 1, dpitch, a.rows, dpitch, 64, P.box_rows);
+    if (e == cudaSuccess && P.tile_n != kTile && a.dx.p) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, kHalf);
     if (e != cudaSuccess) return e;
+    P.tiles_v = (int)tiles(nv);
     P.nx = a.dx.p ? (int)(tiles_t * tiles_c * splits) : 0;
     P.nw = a.dw.p ? (int)(P.tiles_v * tiles_c) : 0;
     const int np = std::min(pairs, P.nx + P.nw);
-    // an item of dw takes at least about three blocks of K for its epilogue
-    const int64_t cost_x = (nv + kKB - 1) / kKB / splits, cost_w = std::max<int64_t>(3, (a.rows + kKB - 1) / kKB);
-    P.late = P.nx % np;
-    P.extra = P.late ? (int)((cost_x + cost_w / 2) / cost_w) : 0;
+    const Schedule s = schedule(P.nx, (nv + kKB - 1) / kKB / splits, P.nw, dw_blocks(a.rows), np);
+    P.dw_first = s.dw_first;
+    P.late = s.late;
+    P.extra = s.extra;
     e = launch(ts_vocab_kernel<kGrad>, 2 * np, kThreads, kSmem, P, st);
   }
   if (direct) return e;
