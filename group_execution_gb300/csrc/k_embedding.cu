@@ -4,8 +4,8 @@
 // The lookup is bound by memory: a warp takes 256 columns of a token's row at
 // a time, four such pieces in flight where there are enough of them.
 //
-// The gradient sums in token order, so that it is the same every time and no
-// atomics touch a sum: the tokens are sorted by id (a stable radix sort, up to
+// The gradient sums in token order, so that it is the same every time: the tokens
+// are sorted by id (a stable radix sort, up to
 // 9 bits a pass), and the sorted list is cut into chunks of equal length,
 // however often a token occurs.  A warp sums one chunk's rows over 256 columns
 // in registers and writes each id's row once.  An id whose tokens lie in more
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_cluster_kernel(const 
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
-  const int cta = (int)cluster_ctarank(), ctas = gridDim.x;
+  const int cta = (int)cluster_ctarank();
   // a warp's rounds follow each other in the list, so that ranks keep its order
   const int part0 = cta * kPart, first = warp * PER * 32, n = min(P.rows - part0, first + PER * 32);
   uint2 e[PER];
@@ -204,7 +204,6 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_cluster_kernel(const 
       const uint32_t at = smem_u32(totals + threadIdx.x);
 #pragma unroll
       for (int c = 0; c < kClusterCtas; ++c) {
-        if (c >= ctas) break;
         uint32_t v;
         asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(at, c)) : "memory");
         total += v;
@@ -508,6 +507,168 @@ __global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_co
   }
 }
 
+// ---- few tokens ------------------------------------------------------------------------
+
+// Up to kFewTokens tokens in one launch.  Every block sorts the tokens for itself
+// (one a thread) and then takes 64 columns of all of them, its warps a part of the
+// sorted list each; the parts of an id meet in shared memory.  Later blocks zero
+// the rows that no token uses.  (512 tokens of 256 columns: XX us, by the kernels
+// below, one after the other, 11.7.)
+constexpr int kFewTokens = kSortThreads;
+constexpr int kFewCols = 64;
+constexpr int kFewSmem =
+    (kSortWarps * kMaxBins + kMaxBins + 32 + 2 * kFewTokens + kSortWarps * 2 * kFewCols) * 4;
+
+struct EmbedFewKernel {
+  const int64_t* ids;
+  const void* dy;
+  void* d;
+  int64_t vocab, lddy, ldd;
+  int rows, cols, passes, bits, pieces;   // pieces of kFewCols columns, a block each
+  int fill;                               // rows of the table that a later block's warp looks up
+  float scale;
+};
+
+// A lane's two columns of 64: side by side (VEC: rows on 16 bytes), or 32 apart.
+template <bool VEC>
+__device__ __forceinline__ int few_col(int lane, int i) {
+  return VEC ? 2 * lane + i : lane + 32 * i;
+}
+template <bool VEC, class T>
+__device__ __forceinline__ float2 load_pair(const T* p, int c0, int cols, int lane) {
+  if (VEC && c0 + 2 * lane + 2 <= cols) {
+    if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2*>(p + c0 + 2 * lane);
+    else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p + c0 + 2 * lane));
+  }
+  float2 v = make_float2(0.f, 0.f);
+  if (c0 + few_col<VEC>(lane, 0) < cols) v.x = to_f32(p[c0 + few_col<VEC>(lane, 0)]);
+  if (c0 + few_col<VEC>(lane, 1) < cols) v.y = to_f32(p[c0 + few_col<VEC>(lane, 1)]);
+  return v;
+}
+template <bool VEC, class T>
+__device__ __forceinline__ void store_pair(T* p, int c0, int cols, int lane, float2 v) {
+  if (VEC && c0 + 2 * lane + 2 <= cols) {
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(p + c0 + 2 * lane) = v;
+    else *reinterpret_cast<__nv_bfloat162*>(p + c0 + 2 * lane) = __floats2bfloat162_rn(v.x, v.y);
+    return;
+  }
+  if (c0 + few_col<VEC>(lane, 0) < cols) p[c0 + few_col<VEC>(lane, 0)] = from_f32<T>(v.x);
+  if (c0 + few_col<VEC>(lane, 1) < cols) p[c0 + few_col<VEC>(lane, 1)] = from_f32<T>(v.y);
+}
+
+template <class T, class U, bool VEC, bool ACC>
+__global__ void __launch_bounds__(kSortThreads) ts_embed_few_kernel(const __grid_constant__ EmbedFewKernel P) {
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint2* list = reinterpret_cast<uint2*>(smem);
+  float2* part = reinterpret_cast<float2*>(smem + 2 * kFewTokens);   // [warps][2][32]
+  uint32_t* hist = smem + 2 * kFewTokens + kSortWarps * 2 * kFewCols;
+  uint32_t* base = hist + kSortWarps * kMaxBins;
+  uint32_t* sums = base + kMaxBins;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, bins = 1 << P.bits;
+  const uint32_t vocab = (uint32_t)P.vocab;
+  {
+    const int i = threadIdx.x;
+    uint2 e = make_uint2(i < P.rows ? id_key(P.ids[i], P.vocab) : 0, i);
+    for (int pass = 0; pass < P.passes; ++pass) {
+      const uint32_t digit[1] = {(e.x >> (pass * P.bits)) & (bins - 1)};
+      uint32_t rank[1];
+      warp_ranks(digit, warp * 32, P.rows, P.bits, hist + warp * kMaxBins, rank);
+      __syncthreads();
+      const uint32_t at = block_exclusive(warp_offsets(hist, bins), sums);
+      if ((int)threadIdx.x < bins) base[threadIdx.x] = at;
+      __syncthreads();
+      if (i < P.rows) list[base[digit[0]] + hist[warp * kMaxBins + digit[0]] + rank[0]] = e;
+      __syncthreads();
+      if (i < P.rows) e = list[i];
+      __syncthreads();
+    }
+  }
+  U* d = static_cast<U*>(P.d);
+  if ((int)blockIdx.x >= P.pieces) {
+    // rows that no token uses
+    const int64_t r0 = ((int64_t)(blockIdx.x - P.pieces) * kSortWarps + warp) * P.fill, v = r0 + lane;
+    bool absent = lane < P.fill && v < P.vocab;
+    if (absent) {
+      int lo = 0, hi = P.rows;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)list[mid].x < v) lo = mid + 1;
+        else hi = mid;
+      }
+      absent = !(lo < P.rows && (int64_t)list[lo].x == v);
+    }
+    const float zero[8] = {};
+    for (uint32_t m = __ballot_sync(0xffffffffu, absent); m; m &= m - 1) {
+      U* row = d + (r0 + __ffs(m) - 1) * P.ldd;
+      for (int c = 0; c < P.cols; c += kGroupCols) store_group<VEC>(row, c, P.cols, lane, zero);
+    }
+    return;
+  }
+  const int c0 = blockIdx.x * kFewCols, per = (P.rows + kSortWarps - 1) / kSortWarps;   // tokens a warp, at most 32
+  const int p0 = warp * per, n = max(0, min(P.rows - p0, per));
+  const T* dy = static_cast<const T*>(P.dy);
+  // lane j: token j of the warp's part, and the id after it
+  const uint2 e = lane < n ? list[p0 + lane] : make_uint2(vocab, 0);
+  const uint32_t next = lane < n && p0 + lane + 1 < P.rows ? list[p0 + lane + 1].x : 0xffffffffu;
+  const uint32_t first = __shfl_sync(0xffffffffu, e.x, 0);
+  bool open = n > 0 && p0 > 0 && list[p0 - 1].x == first;   // the first id has tokens in the part before
+  bool goes_on = false;                                       // an id that begins here has some in the next
+  auto out = [&](uint32_t k, float2 acc, float2 old) {
+    acc.x = ACC ? fmaf(P.scale, acc.x, old.x) : P.scale * acc.x;
+    acc.y = ACC ? fmaf(P.scale, acc.y, old.y) : P.scale * acc.y;
+    store_pair<VEC>(d + (int64_t)k * P.ldd, c0, P.cols, lane, acc);
+  };
+  constexpr int kU = 8;   // rows in flight
+  float2 acc = make_float2(0.f, 0.f);
+  for (int j = 0; j < n; j += kU) {
+    float2 x[kU], old[ACC ? kU : 1];
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), xi = __shfl_sync(0xffffffffu, e.y, (j + i) & 31);
+      const bool in = j + i < n && ki < vocab;
+      x[i] = load_pair<VEC>(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
+      if constexpr (ACC) {
+        const bool ends = in && __shfl_sync(0xffffffffu, next, (j + i) & 31) != ki;
+        old[i] = load_pair<VEC>(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kU; ++i) {
+      const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
+      if (j + i >= n || ki >= vocab) break;   // (padded places sort last)
+      acc.x += x[i].x;
+      acc.y += x[i].y;
+      const bool ends = ni != ki;
+      if (!ends && j + i + 1 < n) continue;
+      if (open || !ends) {
+        part[(warp * 2 + !open) * 32 + lane] = acc;
+        goes_on = !open;
+      } else {
+        out(ki, acc, old[ACC ? i : 0]);
+      }
+      open = false;
+      acc = make_float2(0.f, 0.f);
+    }
+  }
+  __syncthreads();
+  if (!goes_on) return;
+  // the id of this part's last token: the parts after it, in order
+  const uint32_t k = __shfl_sync(0xffffffffu, e.x, n - 1);
+  float2 old = make_float2(0.f, 0.f);
+  if constexpr (ACC) old = load_pair<VEC>(d + (int64_t)k * P.ldd, c0, P.cols, lane);
+  acc = part[(warp * 2 + 1) * 32 + lane];
+  for (int w = warp + 1;; ++w) {
+    const float2 v = part[w * 2 * 32 + lane];
+    acc.x += v.x;
+    acc.y += v.y;
+    const int after = (w + 1) * per;
+    if (after >= P.rows || list[after].x != k) break;
+  }
+  out(k, acc, old);
+}
+
 template <class K, class A>
 cudaError_t launch(K kernel, int64_t grid, int block, int smem, const A& args, cudaStream_t st) {
   cudaLaunchConfig_t cfg = pdl_config((int)grid, block, smem, st);
@@ -589,15 +750,15 @@ SortPlan sort_plan(int64_t rows, int64_t vocab) {
   return s;
 }
 template <int PER>
-cudaError_t sort_cluster(const ts_ops& h, const SortKernel& S, int ctas, cudaStream_t st) {
+cudaError_t sort_cluster(const ts_ops& h, const SortKernel& S, cudaStream_t st) {
   cudaError_t e = opt_in<ts_sort_cluster_kernel<PER>>(h.device, kClusterSmem<PER>);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = pdl_config(ctas, kSortThreads, kClusterSmem<PER>, st);
+  cudaLaunchConfig_t cfg = pdl_config(kClusterCtas, kSortThreads, kClusterSmem<PER>, st);
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = ctas;
+  at[1].val.clusterDim.x = kClusterCtas;
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 2;
@@ -613,43 +774,74 @@ cudaError_t sort_pass(const ts_ops& h, const SortKernel& S, cudaStream_t st) {
 }
 }  // namespace
 
-int64_t embedding_backward_workspace(int64_t rows, int64_t vocab) { return sort_plan(rows, vocab).bytes + 512; }
+namespace {
+cudaError_t launch_few(const ts_ops& h, const EmbedArgs& a, const SortPlan& s, cudaStream_t st) {
+  EmbedFewKernel P = {};
+  P.ids = a.ids;
+  P.dy = a.dy.p;
+  P.d = a.d.p;
+  P.vocab = a.vocab;
+  P.lddy = a.dy.ld;
+  P.ldd = a.d.ld;
+  P.rows = (int)a.rows;
+  P.cols = a.cols;
+  P.passes = s.passes;
+  P.bits = s.bits;
+  P.pieces = a.rows ? (a.cols + kFewCols - 1) / kFewCols : 0;
+  P.scale = a.scale;
+  // (a block an SM, or several: each sorts first)
+  P.fill = (int)std::min<int64_t>(kFillRows, std::max<int64_t>(1, a.vocab / (h.nsm * kSortWarps)));
+  const int64_t fill = a.accumulate ? 0 : (a.vocab + kSortWarps * P.fill - 1) / (kSortWarps * P.fill);
+  if (P.pieces + fill > kMaxGrid) return cudaErrorInvalidConfiguration;
+  if (P.pieces + fill == 0) return cudaSuccess;
+  return by_type(a.dy, a.d, [&](auto t, auto u, auto vec) {
+    using T = decltype(t);
+    using U = decltype(u);
+    constexpr bool V = decltype(vec)::value;
+    cudaError_t e = a.accumulate ? opt_in<ts_embed_few_kernel<T, U, V, true>>(h.device, kFewSmem)
+                                 : opt_in<ts_embed_few_kernel<T, U, V, false>>(h.device, kFewSmem);
+    if (e != cudaSuccess) return e;
+    return launch(a.accumulate ? ts_embed_few_kernel<T, U, V, true> : ts_embed_few_kernel<T, U, V, false>,
+                  P.pieces + fill, kSortThreads, kFewSmem, P, st);
+  });
+}
+}  // namespace
+
+int64_t embedding_backward_workspace(int64_t rows, int64_t vocab) {
+  return rows <= kFewTokens ? 0 : sort_plan(rows, vocab).bytes + 512;
+}
 
 cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaStream_t st) {
   EmbedBackKernel P = {};
   const SortPlan s = sort_plan(a.rows, a.vocab);
+  if (a.rows <= kFewTokens) return launch_few(h, a, s, st);
+  const int64_t list = (a.rows * 8 + 255) / 256 * 256;
+  uint2* at[2] = {reinterpret_cast<uint2*>(h.ws), reinterpret_cast<uint2*>(h.ws + list)};
+  SortKernel S = {};
+  S.ids = a.ids;
+  S.vocab = a.vocab;
+  S.rows = (int)a.rows;
+  S.passes = s.passes;
+  S.bits = s.bits;
+  S.tiles = s.tiles;
+  S.out = at[0];
+  S.joins = reinterpret_cast<uint32_t*>(h.ws + s.bytes);
   cudaError_t e = cudaSuccess;
-  if (a.rows > 0) {
-    const int64_t list = (a.rows * 8 + 255) / 256 * 256;
-    uint2* at[2] = {reinterpret_cast<uint2*>(h.ws), reinterpret_cast<uint2*>(h.ws + list)};
-    SortKernel S = {};
-    S.ids = a.ids;
-    S.vocab = a.vocab;
-    S.rows = (int)a.rows;
-    S.passes = s.passes;
-    S.bits = s.bits;
-    S.tiles = s.tiles;
-    S.out = at[0];
-    S.joins = reinterpret_cast<uint32_t*>(h.ws + s.bytes);
-    if (a.rows <= kClusterList) {
-      // (one CTA up to 1024 tokens, then eight of one or two rounds a warp)
-      e = a.rows <= kSortThreads                  ? sort_cluster<1>(h, S, 1, st)
-          : a.rows <= kClusterCtas * kSortThreads ? sort_cluster<1>(h, S, kClusterCtas, st)
-                                                  : sort_cluster<kClusterPer>(h, S, kClusterCtas, st);
-    } else {
-      S.counts = reinterpret_cast<uint32_t*>(h.ws + 2 * list);
-      for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
-        const int out = (s.passes - 1 - p) & 1;   // the last pass ends in the first list
-        S.out = at[out];
-        S.in = p ? at[1 - out] : nullptr;
-        S.shift = p * s.bits;
-        e = a.rows <= kShortList ? sort_pass<kShortPer>(h, S, st) : sort_pass<kLongPer>(h, S, st);
-      }
+  if (a.rows <= kClusterList) {
+    e = a.rows <= kClusterCtas * kSortThreads ? sort_cluster<1>(h, S, st) : sort_cluster<kClusterPer>(h, S, st);
+  } else {
+    S.counts = reinterpret_cast<uint32_t*>(h.ws + 2 * list);
+    for (int p = 0; p < s.passes && e == cudaSuccess; ++p) {
+      const int out = (s.passes - 1 - p) & 1;   // the last pass ends in the first list
+      S.out = at[out];
+      S.in = p ? at[1 - out] : nullptr;
+      S.shift = p * s.bits;
+      e = a.rows <= kShortList ? sort_pass<kShortPer>(h, S, st) : sort_pass<kLongPer>(h, S, st);
     }
-    if (e != cudaSuccess) return e;
-    P.list = at[0];
-    P.joins = S.joins;
   }
+  if (e != cudaSuccess) return e;
+  P.list = at[0];
+  P.joins = S.joins;
   P.dy = a.dy.p;
   P.d = a.d.p;
   P.lddy = a.dy.ld;
@@ -660,25 +852,22 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   P.scale = a.scale;
   P.groups = (a.cols + kGroupCols - 1) / kGroupCols;
   P.part_cols = (int64_t)P.groups * kGroupCols;
-  if (a.rows > 0) {
-    // as many warps as are resident at once (two blocks an SM), or that many
-    // several times over, so that no SM idles at the end: 4 to 32 tokens a chunk;
-    // fewer, longer ones where the workspace has no room for so many partials
-    const int64_t all = a.rows * P.groups, resident = (int64_t)h.nsm * 2 * kWarps;
-    const int64_t times = std::max<int64_t>(1, (all + resident * 32 - 1) / (resident * 32));
-    const int64_t want = (all + resident * times - 1) / (resident * times);
-    const int64_t room = (h.ws_bytes - s.bytes - 512) / (P.part_cols * 8 + 4);
-    P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
-    if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))
-      P.chunk = room < 2 ? (int)a.rows : (int)((a.rows + room - 1) / room);
-    P.chunks = (int)((a.rows + P.chunk - 1) / P.chunk);
-    P.part = reinterpret_cast<float*>(h.ws + s.bytes + ((int64_t)P.chunks * 4 + 4 + 255) / 256 * 256);
-    P.units = (int64_t)P.chunks * P.groups;
-    P.unit_blocks = (P.units + kWarps - 1) / kWarps;
-  }
+  // as many warps as are resident at once (two blocks an SM), or that many several
+  // times over, so that no SM idles at the end: 4 to 32 tokens a chunk; fewer,
+  // longer ones where the workspace has no room for so many partials
+  const int64_t all = a.rows * P.groups, resident = (int64_t)h.nsm * 2 * kWarps;
+  const int64_t times = (all + resident * 32 - 1) / (resident * 32);
+  const int64_t want = (all + resident * times - 1) / (resident * times);
+  const int64_t room = (h.ws_bytes - s.bytes - 512) / (P.part_cols * 8 + 4);
+  P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
+  if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))
+    P.chunk = room < 2 ? (int)a.rows : (int)((a.rows + room - 1) / room);
+  P.chunks = (int)((a.rows + P.chunk - 1) / P.chunk);
+  P.part = reinterpret_cast<float*>(h.ws + s.bytes + ((int64_t)P.chunks * 4 + 4 + 255) / 256 * 256);
+  P.units = (int64_t)P.chunks * P.groups;
+  P.unit_blocks = (P.units + kWarps - 1) / kWarps;
   const int64_t fill = a.accumulate ? 0 : (a.vocab + kWarps * kFillRows - 1) / (kWarps * kFillRows);
   if (P.unit_blocks + fill > kMaxGrid) return cudaErrorInvalidConfiguration;
-  if (P.unit_blocks + fill == 0) return cudaSuccess;
   return by_type(a.dy, a.d, [&](auto t, auto u, auto vec) {
     using T = decltype(t);
     using U = decltype(u);

@@ -44,13 +44,12 @@ namespace {
 constexpr int kTile = 256;                       // rows and columns of a pair's tile
 constexpr int kHalf = kTile / 2;                 // ... and one CTA stages of each operand
 constexpr int kKB = 128;                         // of K in a ring slot
-constexpr int kBoxBytes = 64 * kHalf * 2;        // one TMA box
-constexpr int kOperandBytes = 2 * kBoxBytes;     // 32 KB
-constexpr int kSlotBytes = 2 * kOperandBytes;
-constexpr int kSlots = 3;
+constexpr int kRowBytes = 64 * 2;                // a TMA box is 64 columns wide
+constexpr int kRingBytes = 192 << 10;
+constexpr int kMaxSlots = 8;                     // (three of 128 rows of each operand)
 constexpr int kStageBytes = 32 * 128;            // an epilogue warp's rows on their way out
 constexpr int kThreads = 12 * 32;
-constexpr int kSmem = kSlots * kSlotBytes + 8 * kStageBytes + 1024;
+constexpr int kSmem = kRingBytes + 8 * kStageBytes + 1024;
 
 enum Mode { kLoss, kDlogits, kGrad };
 
@@ -74,6 +73,7 @@ struct VocabKernel {
   int64_t total;             // the whole vocabulary's size
   int tile_n;                // columns of a tile of the logits
   int box_rows;              // rows of x's and d's boxes: 128, or as many 16s as there are rows
+  int slots, slot_bytes;     // of the ring
   int tiles_t, tiles_v, tiles_c;
   // forward
   float2* part;              // [column parts][rows]: reference (log2) and sum
@@ -242,12 +242,12 @@ template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_vocab_kernel(const __grid_constant__ VocabKernel P) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_mem[2 * kSlots + 5];
+  __shared__ __align__(8) uint64_t bar_mem[2 * kMaxSlots + 5];
   __shared__ int abort_flag, issued[2];         // slots that either producer has issued copies for
   __shared__ int peer_gave_up, peer_issued;     // written by the pair's other CTA
   __shared__ uint32_t tmem_slot;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kSlots, tfull0 = empty0 + 8 * kSlots,
+  const uint32_t full0 = smem_u32(bar_mem), empty0 = full0 + 8 * kMaxSlots, tfull0 = empty0 + 8 * kMaxSlots,
                  tempty0 = tfull0 + 16, done_bar = tempty0 + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int h = (int)cluster_ctarank();
@@ -257,7 +257,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int half_n = MODE == kGrad ? kHalf : P.tile_n / 2;   // columns of B that a CTA stages, and of an epilogue set
   if (threadIdx.x == 0) {
     abort_flag = issued[0] = issued[1] = 0;
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < P.slots; ++s) {
       mbar_init(full0 + 8 * s, 1);   // the even CTA's expect_tx
       mbar_init(empty0 + 8 * s, 1);
     }
@@ -282,7 +282,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (lane == 0 && !P.inject) {
       const bool isA = warp == 0;
       const uint64_t keep = l2_evict_last();
-      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + (isA ? 0 : kOperandBytes);
+      const uint32_t cbar0 = cluster_addr(full0, 0), dst0 = smem_u32(ring) + (isA ? 0 : 2 * P.box_rows * kRowBytes);
       int it = 0, s = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -300,19 +300,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mn = false;
         }
         const int o = isA ? w.m0 + h * kHalf : w.n0 + h * half_n;
-        // a slot's rows: x's or d's boxes, and w's
-        const int slot_rows = MODE != kGrad ? P.box_rows + half_n : w.kind == 1 ? P.box_rows + kHalf : 2 * P.box_rows;
+        // two boxes of each operand; B's rows are columns of the logits, or of K
+        const int b_rows = MODE != kGrad ? half_n : w.kind == 1 ? kHalf : P.box_rows;
+        const uint32_t box_bytes = (isA ? P.box_rows : b_rows) * kRowBytes;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (it >= kSlots && !wait_bar(empty0 + 8 * s, ph ^ 1, P.wait_limit_ns, &abort_flag)) {
+          if (it >= P.slots && !wait_bar(empty0 + 8 * s, ph ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
           }
-          if (leader && isA) mbar_expect_tx(full0 + 8 * s, 2 * slot_rows * 256);
-          const uint32_t dst = dst0 + s * kSlotBytes, cbar = cbar0 + 8 * s;
+          if (leader && isA) mbar_expect_tx(full0 + 8 * s, 4 * (P.box_rows + b_rows) * kRowBytes);
+          const uint32_t dst = dst0 + s * P.slot_bytes, cbar = cbar0 + 8 * s;
           tma_load_2d_pair(dst, map, mn ? o : kb * kKB, mn ? kb * kKB : o, cbar, keep);
-          tma_load_2d_pair(dst + kBoxBytes, map, (mn ? o : kb * kKB) + 64, mn ? kb * kKB : o, cbar, keep);
+          tma_load_2d_pair(dst + box_bytes, map, (mn ? o : kb * kKB) + 64, mn ? kb * kKB : o, cbar, keep);
           ++it;
-          if (++s == kSlots) {
+          if (++s == P.slots) {
             s = 0;
             ph ^= 1;
           }
@@ -339,10 +340,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // bytes on, the second 64 of K one box on.
         const bool a_mn = MODE == kGrad && w.kind == 2, b_mn = MODE == kGrad;
         const uint32_t idesc = idesc_bf16_f32(kTile, 2 * half_n, a_mn, b_mn);
-        const uint64_t ad0 = smem_desc_sw128(base, a_mn ? kBoxBytes : 16, 1024),
-                       bd0 = smem_desc_sw128(base + kOperandBytes, b_mn ? kBoxBytes : 16, 1024);
+        const uint32_t a_box = P.box_rows * kRowBytes,
+                       b_box = (MODE != kGrad ? half_n : w.kind == 1 ? kHalf : P.box_rows) * kRowBytes;
+        const uint64_t ad0 = smem_desc_sw128(base, a_mn ? a_box : 16, 1024),
+                       bd0 = smem_desc_sw128(base + 2 * a_box, b_mn ? b_box : 16, 1024);
         const uint32_t a_step = (a_mn ? 2048 : 32) >> 4, b_step = (b_mn ? 2048 : 32) >> 4;
-        const uint32_t a_half = (a_mn ? 4 * 2048 : kBoxBytes) >> 4, b_half = (b_mn ? 4 * 2048 : kBoxBytes) >> 4;
+        const uint32_t a_half = (a_mn ? 4 * 2048 : a_box) >> 4, b_half = (b_mn ? 4 * 2048 : b_box) >> 4;
         int s0 = w.kb0;
         do {
           const int s1 = chain_end<MODE>(s0, w.kb1), b = i & 1;
@@ -357,7 +360,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
-            const uint32_t so = (uint32_t)(s * kSlotBytes) >> 4;
+            const uint32_t so = (uint32_t)(s * P.slot_bytes) >> 4;
             const int left = w.K - kb * kKB;   // (past K both operands are zeros)
 #pragma unroll
             for (int kk = 0; kk < kKB / 16; ++kk) {
@@ -366,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                              bd0 + so + (kk >> 2) * b_half + (kk & 3) * b_step, idesc, kb != s0 || kk != 0);
             }
             tc_commit_mask(empty0 + 8 * s, pair_mask);
-            if (++s == kSlots) {
+            if (++s == P.slots) {
               s = 0;
               ph ^= 1;
             }
@@ -392,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ---- epilogue ----
     const int q = warp & 3, set = (warp - 4) >> 2;   // the TMEM lane quarter this warp may access, its column half
-    const Stage stage = {ring + kSlots * kSlotBytes + (warp - 4) * kStageBytes};
+    const Stage stage = {ring + kRingBytes + (warp - 4) * kStageBytes};
     const uint32_t stage_u32 = smem_u32(stage.p);
     bool ok = true;
     int i = 0;   // accumulators so far
@@ -496,7 +499,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       } else if constexpr (MODE == kDlogits) {
 #pragma unroll 1
         for (int j = 0; j < half_n; j += 64) {
-          stage_free();
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             float v[32];
@@ -515,6 +517,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 32; ++c)
                 if (c >= left || (coef == 0.f && g == 0.f)) v[c] = 0.f;
             }
+            if (k == 0) stage_free();
             stage.put_bf16(lane, k, v);
           }
           stage_full();
@@ -542,10 +545,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const bool both = tma && out.bf16;   // both 32 columns in one store
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            if (!both || k == 0) stage_free();
             float v[32];
             tmem_ld32(acc + j + 32 * k, v);
             if (j + 64 == kHalf && k == 1) release();
+            if (!both || k == 0) stage_free();
             if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[c] = 0.f;
@@ -595,8 +598,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // slots they fill may lack copies, so each wait may run to its limit
     if (leader && threadIdx.x == 0) {
       const int last = mine > peer_issued ? mine : peer_issued;
-      for (int k = last - kSlots < 0 ? 0 : last - kSlots; k < last; ++k)
-        mbar_wait(full0 + 8 * (k % kSlots), (k / kSlots) & 1, kDrainLimitNs);
+      for (int k = last - P.slots < 0 ? 0 : last - P.slots; k < last; ++k)
+        mbar_wait(full0 + 8 * (k % P.slots), (k / P.slots) & 1, kDrainLimitNs);
     }
     __syncwarp();
     cluster_sync();
@@ -849,6 +852,18 @@ Schedule schedule(int64_t nx, int64_t cx, int64_t nw, int64_t cw, int pairs) {
   return s;
 }
 
+// Launches the product kernel on `pairs` pairs, with as many ring slots of the
+// operands' rows (256 bytes each) as there is room for.  (Three where there could
+// be six cost 33 x 1024 x 4000 1.5 of its 8 us: the way of a copy is longer than
+// the MMAs of two slots.)
+template <int MODE>
+cudaError_t launch_product(VocabKernel& P, int64_t pairs, cudaStream_t st) {
+  const int b_rows = MODE != kGrad ? P.tile_n / 2 : P.nx ? kHalf : P.box_rows;
+  P.slot_bytes = (P.box_rows + b_rows) * 2 * kRowBytes;
+  P.slots = std::min(kMaxSlots, kRingBytes / P.slot_bytes);
+  return launch(ts_vocab_kernel<MODE>, 2 * pairs, kThreads, kSmem, P, st);
+}
+
 // The forward pass's workspace for `rows` rows, its copy of w's rows aside: two
 // parts a tile, and tiles of half the width.
 int64_t forward_bytes(int64_t rows, int64_t cols, int64_t vocab, bool copy_x) {
@@ -948,7 +963,7 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
       P.part = const_cast<float2*>(J.part) + J.parts * rows;
       J.parts += 2 * P.tiles_v;
       const int64_t items = (int64_t)P.tiles_t * P.tiles_v;
-      e = launch(ts_vocab_kernel<kLoss>, 2 * std::min<int64_t>(pairs, items), kThreads, kSmem, P, st);
+      e = launch_product<kLoss>(P, std::min<int64_t>(pairs, items), st);
       if (e != cudaSuccess) return e;
     }
     e = launch(ts_loss_join_kernel, (rows + 31) / 32, kJoinWarps * 32, 0, J, st);
@@ -986,7 +1001,13 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
                   backward_bytes(a.rows, a.cols, n) + cost > h.ws_bytes))
       break;
     const Schedule s = schedule(tiles_t * tiles_c * n, (nkb + n - 1) / n, nw, dw_blocks(a.rows), pairs);
-    const int64_t t = s.blocks + (n > 1 ? 6 + one_dx * n / (int64_t(4) << 20) : 0);
+    // (dw of few rows is bound by memory, like dx: neither runs beside the other
+    // for free, so each kind's rounds count by themselves)
+    const int64_t nx = tiles_t * tiles_c * n;
+    const int64_t blocks = a.rows > kHalf ? s.blocks
+                                          : (nx + pairs - 1) / pairs * ((nkb + n - 1) / n + 1) +
+                                                (nw + pairs - 1) / pairs * (dw_blocks(a.rows) + 1);
+    const int64_t t = blocks + (n > 1 ? 6 + one_dx * n / (int64_t(4) << 20) : 0);
     if (t < least) {
       least = t;
       splits = n;
@@ -1072,7 +1093,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
       if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, P.tile_n / 2);
       if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
       if (e != cudaSuccess) return e;
-      e = launch(ts_vocab_kernel<kDlogits>, 2 * std::min<int64_t>(pairs, tiles_t * P.tiles_v), kThreads, kSmem, P, st);
+      e = launch_product<kDlogits>(P, std::min<int64_t>(pairs, tiles_t * P.tiles_v), st);
       P.copy.units = 0;
     }
     if (e == cudaSuccess && a.dw.p) {
@@ -1092,7 +1113,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
     P.dw_first = s.dw_first;
     P.late = s.late;
     P.extra = s.extra;
-    e = launch(ts_vocab_kernel<kGrad>, 2 * np, kThreads, kSmem, P, st);
+    e = launch_product<kGrad>(P, np, st);
   }
   if (direct) return e;
   if (e != cudaSuccess || !a.dx.p) return e;

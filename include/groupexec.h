@@ -657,9 +657,9 @@ fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* 
  * dy's rows with id v, and zeros where there are none; accumulate = 1 adds to
  * what dtable holds and leaves rows without tokens as they are.  Rows of dy
  * whose id is outside the table are not read.  The sum's order depends on the
- * ids and the sizes alone.  The workspace holds the tokens in sorted order: 8
- * bytes a token up to 8192 of them, about 17 for more (FG_EUNSUPPORTED
- * otherwise). */
+ * ids and the sizes alone.  Of more than 1024 tokens the workspace
+ * holds the sorted list: 8 bytes a token up to 16384 of them, about 18 for more
+ * (FG_EUNSUPPORTED otherwise). */
 fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, fg_dtype dy_dtype, int64_t lddy,
                                 int64_t rows, int64_t vocab, int64_t cols, float scale, void* dtable,
                                 fg_dtype d_dtype, int64_t ldd, int32_t accumulate, void* cuda_stream);
