@@ -81,12 +81,18 @@ struct SortKernel {
   int rows, passes, bits;
   uint2* out;            // (key, token) sorted by key, tokens of a key in order
   uint32_t* joins;       // set to 0; see EmbedBackKernel
+  uint8_t* present;      // [vocab], whether an id has tokens; null: not wanted
   // one pass over a longer list
   const uint2* in;       // null: the ids
   uint32_t* counts;      // [tiles][bins]
   int shift, tiles;
 };
 
+// Zeros, 16 bytes at a time, by thread `t` of `n`; the array's place is rounded up
+// to 256 bytes.
+__device__ __forceinline__ void clear_present(uint8_t* p, int64_t vocab, int64_t t, int64_t n) {
+  for (int64_t i = t * 16; p && i < vocab; i += n * 16) *reinterpret_cast<uint4*>(p + i) = make_uint4(0, 0, 0, 0);
+}
 // An id as a key: ids outside the table sort last.
 __device__ __forceinline__ uint32_t id_key(int64_t id, int64_t vocab) {
   return id >= 0 && id < vocab ? (uint32_t)id : (uint32_t)vocab;
@@ -190,6 +196,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_cluster_kernel(const 
     e[r] = make_uint2(i < n ? id_key(P.ids[part0 + i], P.vocab) : 0, part0 + i);
   }
   if (cta == 0 && threadIdx.x == 0) *P.joins = 0;
+  clear_present(P.present, P.vocab, cta * kSortThreads + threadIdx.x, kClusterCtas * kSortThreads);
   for (int pass = 0; pass < P.passes; ++pass) {
     uint32_t digit[PER], rank[PER];
 #pragma unroll
@@ -198,7 +205,13 @@ __global__ void __launch_bounds__(kSortThreads, 1) ts_sort_cluster_kernel(const 
     __syncthreads();
     const uint32_t mine = warp_offsets(hist, bins);
     if ((int)threadIdx.x < bins) totals[threadIdx.x] = mine;
-    cluster_sync();   // (every CTA has its tokens in registers now)
+    __threadfence();
+    cluster_sync();   // (every CTA has its tokens in registers now, and `present` is clear)
+    if (pass == 0 && P.present) {
+#pragma unroll
+      for (int r = 0; r < PER; ++r)
+        if (first + r * 32 + lane < n && e[r].x < (uint32_t)P.vocab) P.present[e[r].x] = 1;
+    }
     uint32_t before = 0, total = 0;
     if ((int)threadIdx.x < bins) {
       const uint32_t at = smem_u32(totals + threadIdx.x);
@@ -251,6 +264,7 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __gri
       atomicAdd(&hist[(P.in ? P.in[i].x : id_key(P.ids[i], P.vocab)) >> P.shift & (bins - 1)], 1u);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.joins = 0;
+  if (!P.in) clear_present(P.present, P.vocab, (int64_t)blockIdx.x * kSortThreads + threadIdx.x, (int64_t)gridDim.x * kSortThreads);
   __syncthreads();
   if ((int)threadIdx.x < bins) P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
 }
@@ -293,7 +307,10 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_pass_kernel(const __grid
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < PER; ++r) {
-    if (first + r * 32 + lane < n) P.out[base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r]] = e[r];
+    if (first + r * 32 + lane < n) {
+      P.out[base[digit[r]] + hist[warp * kMaxBins + digit[r]] + rank[r]] = e[r];
+      if (!P.in && P.present && e[r].x < (uint32_t)P.vocab) P.present[e[r].x] = 1;
+    }
   }
 }
 
@@ -305,12 +322,14 @@ struct EmbedBackKernel {
   void* d;
   float* part;           // [chunks][2][part_cols]: a chunk's first id's, its last id's
   uint32_t* joins;       // how many ids lie in more than one chunk, and the chunks where they begin
+  const uint8_t* present;
   int64_t lddy, ldd, part_cols, units, unit_blocks, vocab;
   int rows, cols, groups, chunk, chunks;
   float scale;
 };
 
 constexpr int kFillRows = 8;   // rows of the table a warp looks up at a time
+constexpr int kChunk = 64;     // tokens of a chunk, at most
 
 __device__ __forceinline__ float* part_at(const EmbedBackKernel& P, int chunk, int slot, int group, int lane) {
   return P.part + ((int64_t)chunk * 2 + slot) * P.part_cols + group * kGroupCols + lane * 8;
@@ -365,18 +384,8 @@ __global__ void __launch_bounds__(kThreads, 2) ts_embed_sum_kernel(const __grid_
   U* d = static_cast<U*>(P.d);
   if (blockIdx.x >= P.unit_blocks) {
     // rows that no token uses
-    const int64_t r0 = ((int64_t)(blockIdx.x - P.unit_blocks) * kWarps + warp) * kFillRows;
-    const int64_t v = r0 + lane;
-    bool absent = lane < kFillRows && v < P.vocab;
-    if (absent) {
-      int lo = 0, hi = P.rows;
-      while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if ((int64_t)P.list[mid].x < v) lo = mid + 1;
-        else hi = mid;
-      }
-      absent = !(lo < P.rows && (int64_t)P.list[lo].x == v);
-    }
+    const int64_t r0 = ((blockIdx.x - P.unit_blocks) * kWarps + warp) * kFillRows, v = r0 + lane;
+    const bool absent = lane < kFillRows && v < P.vocab && !P.present[v];
     const float zero[8] = {};
     for (uint32_t m = __ballot_sync(0xffffffffu, absent); m; m &= m - 1) {
       U* row = d + (r0 + __ffs(m) - 1) * P.ldd;
@@ -734,7 +743,7 @@ cudaError_t launch_embedding(const ts_ops& h, const EmbedArgs& a, cudaStream_t s
 namespace {
 struct SortPlan {
   int passes, bits, tiles;
-  int64_t counts_bytes, bytes;
+  int64_t counts_bytes, present_bytes, bytes;
 };
 SortPlan sort_plan(int64_t rows, int64_t vocab) {
   SortPlan s = {};
@@ -746,7 +755,8 @@ SortPlan sort_plan(int64_t rows, int64_t vocab) {
   s.tiles = (int)((rows + tile - 1) / tile);
   const bool alone = rows <= kClusterList;
   s.counts_bytes = alone ? 0 : ((int64_t)s.tiles << s.bits) * 4;
-  s.bytes = (rows * 8 + 255) / 256 * 256 * (alone ? 1 : 2) + (s.counts_bytes + 255) / 256 * 256;
+  s.present_bytes = (vocab + 255) / 256 * 256;
+  s.bytes = (rows * 8 + 255) / 256 * 256 * (alone ? 1 : 2) + (s.counts_bytes + 255) / 256 * 256 + s.present_bytes;
   return s;
 }
 template <int PER>
@@ -826,6 +836,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   S.tiles = s.tiles;
   S.out = at[0];
   S.joins = reinterpret_cast<uint32_t*>(h.ws + s.bytes);
+  S.present = a.accumulate ? nullptr : h.ws + s.bytes - s.present_bytes;
   cudaError_t e = cudaSuccess;
   if (a.rows <= kClusterList) {
     e = a.rows <= kClusterCtas * kSortThreads ? sort_cluster<1>(h, S, st) : sort_cluster<kClusterPer>(h, S, st);
@@ -842,6 +853,7 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   if (e != cudaSuccess) return e;
   P.list = at[0];
   P.joins = S.joins;
+  P.present = S.present;
   P.dy = a.dy.p;
   P.d = a.d.p;
   P.lddy = a.dy.ld;
@@ -853,13 +865,13 @@ cudaError_t launch_embedding_backward(const ts_ops& h, const EmbedArgs& a, cudaS
   P.groups = (a.cols + kGroupCols - 1) / kGroupCols;
   P.part_cols = (int64_t)P.groups * kGroupCols;
   // as many warps as are resident at once (two blocks an SM), or that many several
-  // times over, so that no SM idles at the end: 4 to 32 tokens a chunk; fewer,
+  // times over, so that no SM idles at the end: 4 to 64 tokens a chunk; fewer,
   // longer ones where the workspace has no room for so many partials
   const int64_t all = a.rows * P.groups, resident = (int64_t)h.nsm * 2 * kWarps;
-  const int64_t times = (all + resident * 32 - 1) / (resident * 32);
+  const int64_t times = (all + resident * kChunk - 1) / (resident * kChunk);
   const int64_t want = (all + resident * times - 1) / (resident * times);
   const int64_t room = (h.ws_bytes - s.bytes - 512) / (P.part_cols * 8 + 4);
-  P.chunk = (int)std::min<int64_t>(32, std::max<int64_t>(4, want));
+  P.chunk = (int)std::min<int64_t>(kChunk, std::max<int64_t>(4, want));
   if ((a.rows + P.chunk - 1) / P.chunk > std::max<int64_t>(room, 1))
     P.chunk = room < 2 ? (int)a.rows : (int)((a.rows + room - 1) / room);
   P.chunks = (int)((a.rows + P.chunk - 1) / P.chunk);

@@ -658,8 +658,8 @@ fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* 
  * what dtable holds and leaves rows without tokens as they are.  Rows of dy
  * whose id is outside the table are not read.  The sum's order depends on the
  * ids and the sizes alone.  Of more than 1024 tokens the workspace
- * holds the sorted list: 8 bytes a token up to 16384 of them, about 18 for more
- * (FG_EUNSUPPORTED otherwise). */
+ * holds the sorted list, 8 bytes a token up to 16384 of them and about 18 for
+ * more, and a byte a row of the table (FG_EUNSUPPORTED otherwise). */
 fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, fg_dtype dy_dtype, int64_t lddy,
                                 int64_t rows, int64_t vocab, int64_t cols, float scale, void* dtable,
                                 fg_dtype d_dtype, int64_t ldd, int32_t accumulate, void* cuda_stream);
