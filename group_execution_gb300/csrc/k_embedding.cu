@@ -335,26 +335,99 @@ __device__ __forceinline__ float* part_at(const EmbedBackKernel& P, int chunk, i
   return P.part + ((int64_t)chunk * 2 + slot) * P.part_cols + group * kGroupCols + lane * 8;
 }
 
+// A warp's 256 columns, eight to a lane: with VEC (all rows on 16 bytes) twice four
+// that lie together, 128 apart, so that each access of the warp covers whole lines
+// of either type (eight together, two accesses with gaps of 16 bytes for float32,
+// took 65536 x 1003 117 us in place of XX).
+template <bool VEC>
+__device__ __forceinline__ int quad_col(int lane, int j) {
+  return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane;
+}
+// Four values of a row as they lie in memory.
+template <class T>
+struct alignas(4 * sizeof(T)) Quad {
+  uint32_t w[sizeof(T)];
+  // the last ones of a row, zeros past its `n` (< 4) columns
+  __device__ __forceinline__ void edge(const T* p, int n) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      if constexpr (sizeof(T) == 4) {
+        w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+      } else {
+        w[i] = bf16x2(2 * i < n ? to_f32(p[2 * i]) : 0.f, 2 * i + 1 < n ? to_f32(p[2 * i + 1]) : 0.f);
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int j) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[j]);
+    else return __uint_as_float(j & 1 ? w[j >> 1] & 0xffff0000u : w[j >> 1] << 16);
+  }
+  __device__ __forceinline__ void set(const float* v) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(v[i]);
+      else w[i] = bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+  }
+};
+template <class T, bool VEC>
+struct RawQuads : RawGroup<T, false> {};
+template <class T>
+struct RawQuads<T, true> {
+  Quad<T> q[2];
+  __device__ __forceinline__ void load(const T* p, int c0, int cols, int lane) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int c = c0 + quad_col<true>(lane, 4 * k);
+      if (c + 4 <= cols) q[k] = *reinterpret_cast<const Quad<T>*>(p + c);
+      else q[k].edge(p + c, cols - c);
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = q[j >> 2].get(j & 3);
+  }
+};
+template <bool VEC, class T>
+__device__ __forceinline__ void store_quads(T* p, int c0, int cols, int lane, const float (&v)[8]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (VEC && c0 + quad_col<VEC>(lane, 4 * k) + 4 <= cols) {
+      Quad<T> q;
+      q.set(v + 4 * k);
+      *reinterpret_cast<Quad<T>*>(p + c0 + quad_col<VEC>(lane, 4 * k)) = q;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + quad_col<VEC>(lane, 4 * k + j);
+        if (c < cols) p[c] = from_f32<T>(v[4 * k + j]);
+      }
+    }
+  }
+}
+
 // Whether the sum is added in memory: float32 rows, each value by one reduction
 // of one launch, so that it does not matter when.  (Reading them first took
-// 65536 x 1003 into 50001 131 us in place of XX.)
+// 65536 x 1003 into 50001 131 us in place of 111.)
 template <class U, bool ACC>
 constexpr bool kAddInMemory = ACC && std::is_same<U, float>::value;
 
-// Adds the group's values to a float32 row.
+// Adds the values to a float32 row.
 template <bool VEC>
-__device__ __forceinline__ void add_group(float* p, int c0, int cols, int lane, const float (&v)[8]) {
-  if (VEC && c0 + lane * 8 + 8 <= cols) {
+__device__ __forceinline__ void add_quads(float* p, int c0, int cols, int lane, const float (&v)[8]) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 4)
-      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + c0 + lane * 8 + k), "f"(v[k]),
-                   "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3])
+  for (int k = 0; k < 2; ++k) {
+    float* q = p + c0 + quad_col<VEC>(lane, 4 * k);
+    if (VEC && c0 + quad_col<VEC>(lane, 4 * k) + 4 <= cols) {
+      asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(q), "f"(v[4 * k]), "f"(v[4 * k + 1]),
+                   "f"(v[4 * k + 2]), "f"(v[4 * k + 3])
                    : "memory");
-  } else {
+    } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = c0 + group_col<VEC>(lane, j);
-      if (c < cols) atomicAdd(p + c, v[j]);
+      for (int j = 0; j < 4; ++j) {
+        const int c = c0 + quad_col<VEC>(lane, 4 * k + j);
+        if (c < cols) atomicAdd(p + c, v[4 * k + j]);
+      }
     }
   }
 }
@@ -367,11 +440,11 @@ __device__ __forceinline__ void finish(U* row, float scale, const float (&acc)[8
   if constexpr (kAddInMemory<U, ACC>) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = scale * acc[j];
-    add_group<VEC>(row, c0, cols, lane, v);
+    add_quads<VEC>(row, c0, cols, lane, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = ACC ? fmaf(scale, acc[j], old[j]) : scale * acc[j];
-    store_group<VEC>(row, c0, cols, lane, v);
+    store_quads<VEC>(row, c0, cols, lane, v);
   }
 }
 
@@ -403,54 +476,61 @@ __global__ void __launch_bounds__(kThreads, 2) ts_embed_sum_kernel(const __grid_
   // rows of a batch; one is loaded while one is added
   constexpr int kU = kOld ? 2 : VEC && sizeof(T) == 2 ? 8 : 4;
   struct Batch {
-    RawGroup<T, VEC> raw[kU];
-    RawGroup<U, VEC> old[kOld ? kU : 1];
+    RawQuads<T, VEC> raw[kU];
+    RawQuads<U, VEC> old[kOld ? kU : 1];
   };
   bool open = false;
-  float acc[8] = {};
+  F2 acc[4] = {};
   for (int q = p0; q < p1; q += 32) {
-    const int at = q + lane, n = min(32, p1 - q);
+    // lane j: token j, and whether it is its id's last of the chunk (`cuts`) or of
+    // all (`ends`); padded places sort last and are left out
+    const int at = q + lane;
     const uint2 e = at < p1 ? P.list[at] : make_uint2(vocab, 0);
-    const uint32_t next = at + 1 < P.rows && at < p1 ? P.list[at + 1].x : 0xffffffffu;
+    const uint32_t next = at < p1 && at + 1 < P.rows ? P.list[at + 1].x : 0xffffffffu;
+    const int n = __popc(__ballot_sync(0xffffffffu, e.x < vocab));
+    if (n == 0) return;
+    const uint32_t ends = __ballot_sync(0xffffffffu, next != e.x);
+    const uint32_t cuts = ends | (p1 - q <= 32 ? 1u << (p1 - q - 1) : 0);
     // the first id may have tokens in the chunk before
     if (q == p0) open = p0 > 0 && P.list[p0 - 1].x == __shfl_sync(0xffffffffu, e.x, 0);
     auto load = [&](Batch& b, int j) {
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), xi = __shfl_sync(0xffffffffu, e.y, (j + i) & 31);
-        const bool in = j + i < n && ki < vocab;
-        b.raw[i].load(dy + (int64_t)(in ? xi : 0) * P.lddy, c0, in ? P.cols : 0, lane);
+        const int t = min(j + i, n - 1);   // (past the last one it is loaded again)
+        const uint32_t xi = __shfl_sync(0xffffffffu, e.y, t);
+        b.raw[i].load(dy + (int64_t)xi * P.lddy, c0, P.cols, lane);
         if constexpr (kOld) {
-          const uint32_t ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
-          const bool ends = in && ni != ki;
-          b.old[i].load(d + (int64_t)(ends ? ki : 0) * P.ldd, c0, ends ? P.cols : 0, lane);
+          const uint32_t ki = __shfl_sync(0xffffffffu, e.x, t);
+          b.old[i].load(d + (int64_t)ki * P.ldd, c0, ends >> t & 1 ? P.cols : 0, lane);
         }
       }
     };
     auto add = [&](const Batch& b, int j) {
 #pragma unroll
       for (int i = 0; i < kU; ++i) {
-        const uint32_t ki = __shfl_sync(0xffffffffu, e.x, (j + i) & 31), ni = __shfl_sync(0xffffffffu, next, (j + i) & 31);
-        if (j + i >= n || ki >= vocab) return;   // (padded places sort last)
+        if (j + i >= n) return;
         float v[8];
         b.raw[i].get(v);
 #pragma unroll
-        for (int m = 0; m < 8; ++m) acc[m] += v[m];
-        const bool ends = ni != ki;
-        if (!ends && q + j + i + 1 < p1) continue;
-        if (open || !ends) {
-          float* o = part_at(P, chunk, open ? 0 : 1, group, lane);
-          reinterpret_cast<float4*>(o)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-          reinterpret_cast<float4*>(o)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-          if (!open && group == 0 && lane == 0) P.joins[1 + atomicAdd(P.joins, 1u)] = chunk;
-        } else {
+        for (int m = 0; m < 4; ++m) acc[m] = add2(acc[m], pack2f(v[2 * m], v[2 * m + 1]));
+        if (!(cuts >> (j + i) & 1)) continue;
+        const bool whole = !open && (ends >> (j + i) & 1);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) unpack2f(acc[m], v[2 * m], v[2 * m + 1]);
+        if (whole) {
           float was[8] = {};
           if constexpr (kOld) b.old[i].get(was);
-          finish<VEC, ACC>(d + (int64_t)ki * P.ldd, P.scale, acc, was, c0, P.cols, lane);
+          const uint32_t ki = __shfl_sync(0xffffffffu, e.x, j + i);
+          finish<VEC, ACC>(d + (int64_t)ki * P.ldd, P.scale, v, was, c0, P.cols, lane);
+        } else {
+          float* o = part_at(P, chunk, open ? 0 : 1, group, lane);
+          reinterpret_cast<float4*>(o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4*>(o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          if (!open && group == 0 && lane == 0) P.joins[1 + atomicAdd(P.joins, 1u)] = chunk;
         }
         open = false;
 #pragma unroll
-        for (int m = 0; m < 8; ++m) acc[m] = 0.f;
+        for (int m = 0; m < 4; ++m) acc[m] = 0;
       }
     };
     Batch b0, b1;
@@ -510,7 +590,7 @@ __global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_co
     const float v[2] = {acc.x, acc.y};
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int c = piece * kJoinCols / kGroupCols * kGroupCols + group_col<VEC>((pos + i) / 8, (pos + i) % 8);
+      const int c = piece * kJoinCols / kGroupCols * kGroupCols + quad_col<VEC>((pos + i) / 8, (pos + i) % 8);
       if (c < P.cols) row[c] = from_f32<U>(ACC ? fmaf(P.scale, v[i], to_f32(row[c])) : P.scale * v[i]);
     }
   }

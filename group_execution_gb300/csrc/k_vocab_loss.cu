@@ -211,12 +211,17 @@ struct Stage {
       put(row, c, make_uint4(__float_as_uint(v[4 * c]), __float_as_uint(v[4 * c + 1]), __float_as_uint(v[4 * c + 2]),
                              __float_as_uint(v[4 * c + 3])));
   }
-  // 32 columns in bf16, the first or second half of the 128 bytes
-  __device__ __forceinline__ void put_bf16(int row, int half, const float (&v)[32]) const {
+  // 32 columns in bf16, the first or second half of the 128 bytes; signs flipped
+  // and values masked as asked
+  __device__ __forceinline__ void put_bf16(int row, int half, const float (&v)[32], uint32_t flip = 0,
+                                           uint32_t keep = 0xffffffffu) const {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      put(row, half * 4 + c, make_uint4(bf16x2(v[8 * c], v[8 * c + 1]), bf16x2(v[8 * c + 2], v[8 * c + 3]),
-                                        bf16x2(v[8 * c + 4], v[8 * c + 5]), bf16x2(v[8 * c + 6], v[8 * c + 7])));
+    for (int c = 0; c < 4; ++c) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = (bf16x2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]) ^ flip) & keep;
+      put(row, half * 4 + c, make_uint4(u[0], u[1], u[2], u[3]));
+    }
   }
 };
 
@@ -404,7 +409,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (w.kind < 0) break;
       const int r0 = w.m0 + h * kHalf + q * 32, row = r0 + lane;
       const int c0 = w.n0 + set * half_n;   // this warp's first column
-      float lse2 = 0.f, coef = 0.f, g = 0.f;
+      // d is |coef| p - (its sign) g at the target, as bf16 with coef's sign, or
+      // masked out; |coef| goes into the exponent
+      float shift = 0.f, g = 0.f;
+      uint32_t sign = 0, keep = 0;
       int target = -1;   // the target's column of the piece
       if constexpr (MODE != kGrad) {
         if (row < P.rows) {
@@ -413,10 +421,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if constexpr (MODE == kDlogits) {
             // (a row of -inf logits takes no gradient)
             const float l = P.lse[row];
-            const bool none = l == -INFINITY;
-            lse2 = none ? 0.f : l * kLog2e;
-            g = t >= 0 && t < P.total && !none ? P.g_loss[row] : 0.f;
-            coef = g + (P.g_lse && !none ? P.g_lse[row] : 0.f);
+            if (l != -INFINITY) {
+              g = t >= 0 && t < P.total ? P.g_loss[row] : 0.f;
+              const float coef = g + (P.g_lse ? P.g_lse[row] : 0.f);
+              shift = log2f(fabsf(coef)) - l * kLog2e;
+              if (coef < 0.f) {
+                sign = 0x80008000u;
+                g = -g;
+              }
+              // rows without a gradient have zeros whatever their logits
+              keep = coef == 0.f && g == 0.f ? 0 : 0xffffffffu;
+            }
           }
         }
       }
@@ -506,19 +521,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (j + 64 == half_n && k == 1) release();
             const int cc = c0 + j + 32 * k, left = P.vocab - cc, at = target - cc;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = coef * exp2_approx(fmaf(v[c], kLog2e, -lse2));
+            for (int c = 0; c < 32; ++c) v[c] = exp2_approx(fmaf(v[c], kLog2e, shift));
             if (at >= 0 && at < 32) {
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[c] -= c == at ? g : 0.f;
             }
-            if (left < 32 || coef == 0.f) {
-              // past the vocabulary, and in rows without a gradient whatever their logits
+            if (left < 32) {
 #pragma unroll
               for (int c = 0; c < 32; ++c)
-                if (c >= left || (coef == 0.f && g == 0.f)) v[c] = 0.f;
+                if (c >= left) v[c] = 0.f;
             }
             if (k == 0) stage_free();
-            stage.put_bf16(lane, k, v);
+            stage.put_bf16(lane, k, v, sign, keep);
           }
           stage_full();
           if (lane == 0) {
