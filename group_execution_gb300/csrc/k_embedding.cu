@@ -4,14 +4,18 @@
 // The lookup is bound by memory: a warp takes 256 columns of a token's row at
 // a time, four such pieces in flight where there are enough of them.
 //
-// The gradient sums in token order, so that it is the same every time: the tokens
-// are sorted by id (a stable radix sort, up to
-// 9 bits a pass), and the sorted list is cut into chunks of equal length,
-// however often a token occurs.  A warp sums one chunk's rows over 256 columns
-// in registers and writes each id's row once.  An id whose tokens lie in more
-// than one chunk leaves a float32 partial in the workspace for each, which a
-// second kernel adds in order.  Rows of the table that no token uses are zeroed
-// by other blocks of the same launch, which look them up in the sorted list.
+// The gradient sums in an order that the ids and the sizes fix, so that it is the
+// same every time: the tokens are sorted by id (a stable radix sort, up to 9 bits
+// a pass), and the sorted list is cut into chunks of equal length, however often a
+// token occurs.  A warp sums one chunk's rows over 256 columns in registers, a
+// batch of rows loaded while one is added, and writes each id's row once.  An id
+// whose tokens lie in more than one chunk leaves a float32 partial in the
+// workspace for each, which a second kernel adds in order.  Rows of the table that
+// no token uses are zeroed by later blocks of the same launch.
+//
+// At 8192 x 4096 bf16 into a float32 gradient of 50001 rows this takes 145 us (89 %
+// of the copy rate; 130 of it the sums and zeros, 9 the sort), added to what is
+// there 45 us (95 %); 65536 x 1003 float32 added to 50001 rows 99 us (87 %).
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -338,7 +342,7 @@ __device__ __forceinline__ float* part_at(const EmbedBackKernel& P, int chunk, i
 // A warp's 256 columns, eight to a lane: with VEC (all rows on 16 bytes) twice four
 // that lie together, 128 apart, so that each access of the warp covers whole lines
 // of either type (eight together, two accesses with gaps of 16 bytes for float32,
-// took 65536 x 1003 117 us in place of XX).
+// took 65536 x 1003 117 us in place of 99).
 template <bool VEC>
 __device__ __forceinline__ int quad_col(int lane, int j) {
   return VEC ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane;
@@ -601,8 +605,8 @@ __global__ void __launch_bounds__(kThreads) ts_embed_join_kernel(const __grid_co
 // Up to kFewTokens tokens in one launch.  Every block sorts the tokens for itself
 // (one a thread) and then takes 64 columns of all of them, its warps a part of the
 // sorted list each; the parts of an id meet in shared memory.  Later blocks zero
-// the rows that no token uses.  (512 tokens of 256 columns: XX us, by the kernels
-// below, one after the other, 11.7.)
+// the rows that no token uses.  (512 tokens of 256 columns: 8.1 us, by the three
+// kernels above, one after the other, 11.7.)
 constexpr int kFewTokens = kSortThreads;
 constexpr int kFewCols = 64;
 constexpr int kFewSmem =
