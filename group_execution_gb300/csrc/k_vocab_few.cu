@@ -9,6 +9,9 @@
 // serve two MMAs.  Where there are fewer tiles than warps, a tile's K is cut over
 // the warps of a block, and their sums meet in shared memory.
 //
+// 1 x 1024 x 4000 takes 7 us in a graph, where tiles on the tensor cores' own
+// memory take 11; a step of 16 x 1024 x 8000 or more is faster there.
+//
 // Forward, each block keeps a maximum and a sum of exponentials for every row;
 // the block that finishes last joins all of them in block order, so that the
 // whole pass is one launch.

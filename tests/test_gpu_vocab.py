@@ -447,10 +447,16 @@ def test_tied_step(ops):
     within(dw, want, 2.0 ** -24 * (len(ids) + 4) * size)
 
 
-def test_captured_and_replayed(ops):
-    a, b = tied(), tied()
+# every kernel that a call's size chooses: few rows of a small table, few tokens,
+# a cluster's sort, a sort of several launches
+SIZES = [(9, 264, 3001), (700, 264, 3001), (3000, 72, 3001), (20000, 40, 3001)]
+
+
+@pytest.mark.parametrize("rows, cols, vocab", SIZES)
+def test_captured_and_replayed(ops, rows, cols, vocab):
+    a, b = tied(rows, cols, vocab), tied(rows, cols, vocab)
     step(ops, *a)
-    mine = TrainingOps(workspace_bytes=64 << 20)
+    mine = TrainingOps(workspace_bytes=256 << 20)   # (as `ops`: sums are cut by what it holds)
     graph = torch.cuda.CUDAGraph()
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -476,8 +482,9 @@ def test_captured_and_replayed(ops):
         assert torch.equal(s, t)
 
 
-def test_two_handles_on_two_streams():
-    ref, runs = tied(), [tied(), tied()]
+@pytest.mark.parametrize("rows, cols, vocab", SIZES)
+def test_two_handles_on_two_streams(rows, cols, vocab):
+    ref, runs = tied(rows, cols, vocab), [tied(rows, cols, vocab), tied(rows, cols, vocab)]
     handles = [TrainingOps(workspace_bytes=64 << 20) for _ in range(3)]
     step(handles[2], *ref)
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
@@ -490,6 +497,56 @@ def test_two_handles_on_two_streams():
     for r in runs:
         for x, y in zip(ref, r):
             assert torch.equal(x, y)
+
+
+def test_calls_of_one_handle_in_any_order(ops):
+    """Calls of different sizes follow each other in one workspace, nothing
+    waited for: each finds what it needs as it was meant to be."""
+    want = [tied(*s) for s in SIZES]
+    fresh = TrainingOps(workspace_bytes=256 << 20)
+    for a in want:
+        step(fresh, *a)
+        fresh.sync()
+    got = [tied(*s) for s in SIZES]
+    for i in (0, 3, 1, 0, 2, 3, 0, 1, 2, 2, 0, 3):
+        step(ops, *got[i])
+    ops.sync()
+    for a, b in zip(want, got):
+        for x, y in zip(a, b):
+            assert torch.equal(x, y)
+
+
+def test_loss_gradient_is_the_differences(ops):
+    """Along a direction of x and of w, in steps that bf16 holds exactly."""
+    rows, cols, vocab = 40, 64, 500
+    x, w = torch.round(normal(1, rows, cols) * 8) / 8, torch.round(normal(2, vocab, cols) * 8) / 32
+    targets, g = tokens(3, rows, vocab).cuda(), (normal(4, rows).abs() + 0.5).cuda()
+
+    def total(x, w):
+        loss = torch.empty(rows, device="cuda")
+        ops.linear_cross_entropy(x.cuda().to(BF16), w.cuda().to(BF16), targets, loss, None)
+        return (loss.double() * g.double()).sum().item()
+
+    lse = torch.empty(rows, device="cuda")
+    xb, wb = x.cuda().to(BF16), w.cuda().to(BF16)
+    ops.linear_cross_entropy(xb, wb, targets, None, lse)
+    dx, dw = output(rows, cols), output(vocab, cols)
+    ops.linear_cross_entropy_backward(xb, wb, targets, lse, g, dx, dw)
+    # x, w and the steps are multiples of 2^-7 below 2: exact in bf16.  The second
+    # difference's term is bounded by the step's square times the logits' spread
+    step = 2.0 ** -7
+    for t, d, at in ((x, dx, 0), (w, dw, 1)):
+        u = torch.sign(normal(5 + at, *t.shape)) * (normal(7 + at, *t.shape).abs() > 1.5)
+        keep = ((t + step * u).to(BF16).float() == t + step * u) & ((t - step * u).to(BF16).float() == t - step * u)
+        u = u * keep
+        up, down = ((total(t + s * step * u, w) if at == 0 else total(x, t + s * step * u)) for s in (1, -1))
+        along = (d.cpu().double() * u.double()).sum().item()
+        # third derivatives of a log-sum-exp along a direction: the cube of the
+        # logits' change, and float32 losses of about 5 in both sums
+        delta = (step * (u @ w.t() if at == 0 else x @ u.t())).abs().amax(1).double()
+        bound = (delta ** 3 * g.cpu().double()).sum().item() / step + 2 * 2.0 ** -20 * 5 * g.sum().item() / step
+        bound += 2.0 ** -8 * (d.cpu().double().abs() * u.double().abs()).sum().item()
+        assert abs((up - down) / (2 * step) - along) <= bound, (up - down, along, bound)
 
 
 # ---- refusals -----------------------------------------------------------------------------
