@@ -898,6 +898,11 @@ int64_t forward_bytes(int64_t rows, int64_t cols, int64_t vocab, bool copy_x) {
 int64_t backward_bytes(int64_t rows, int64_t cols, int64_t splits) {
   return round_up(rows * pitch_of(cols) * 2, 256) + round_up(splits * rows * pitch_of(cols) * 4, 256);
 }
+// The parts that dx's K is cut in at most: some items a pair, where there are not
+// enough without.
+int64_t most_splits(int64_t rows, int64_t cols, int64_t vocab) {
+  return std::max<int64_t>(1, std::min<int64_t>(tiles(vocab) / 2, 256 / (tiles(rows) * tiles(cols))));
+}
 int64_t piece_bytes(int64_t rows, int64_t cols, bool copy_w) {
   return kTile * (rows + (copy_w ? pitch_of(cols) : 0)) * 2;
 }
@@ -907,7 +912,8 @@ int64_t piece_bytes(int64_t rows, int64_t cols, bool copy_w) {
 int64_t vocab_loss_workspace(int64_t rows, int64_t cols, int64_t vocab, bool copy_x, bool copy_w, bool backward,
                              bool whole) {
   if (backward)
-    return backward_bytes(rows, cols, 1) + (whole ? tiles(vocab) : 1) * piece_bytes(rows, cols, copy_w);
+    return backward_bytes(rows, cols, whole && rows > 0 ? most_splits(rows, cols, vocab) : 1) +
+           (whole ? tiles(vocab) : 1) * piece_bytes(rows, cols, copy_w);
   if (whole)
     return forward_bytes(rows, cols, vocab, copy_x) + (copy_w ? tiles(vocab) * kTile * pitch_of(cols) * 2 : 0);
   return forward_bytes(std::min<int64_t>(rows, kTile), cols, vocab, copy_x) +
@@ -1020,10 +1026,10 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   // (as if dw were wanted too: dx does not depend on whether it is)
   const int64_t nkb = (a.vocab + kKB - 1) / kKB, nw = tiles_v * tiles_c;
   int64_t splits = 1, least = INT64_MAX;
-  for (int64_t n = 1; n <= std::min<int64_t>(64, std::max<int64_t>(1, tiles_v / 2)); ++n) {
-    if (n > 1 && (round_up(a.rows * pitch * 2, 256) + n * one_dx > h.ws_bytes / 2 ||
-                  backward_bytes(a.rows, a.cols, n) + cost > h.ws_bytes))
-      break;
+  // (not at the price of more pieces)
+  const int64_t rest = (backward_bytes(a.rows, a.cols, 1) + tiles_v * cost <= h.ws_bytes ? tiles_v : 1) * cost;
+  for (int64_t n = 1; n <= most_splits(a.rows, a.cols, a.vocab); ++n) {
+    if (n > 1 && backward_bytes(a.rows, a.cols, n) + rest > h.ws_bytes) break;
     const Schedule s = schedule(tiles_t * tiles_c * n, (nkb + n - 1) / n, nw, dw_blocks(a.rows), pairs);
     // (dw of few rows is bound by memory, like dx: neither runs beside the other
     // for free, so each kind's rounds count by themselves)
