@@ -549,6 +549,42 @@ def test_loss_gradient_is_the_differences(ops):
         assert abs((up - down) / (2 * step) - along) <= bound, (up - down, along, bound)
 
 
+def test_offsets_past_32_bits():
+    """Tables of more than 2^31 elements, looked at near their ends."""
+    ops = TrainingOps(workspace_bytes=512 << 20)
+    vocab, cols, rows = 1 << 20, 2064, 40
+    g = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.empty((vocab, cols), dtype=BF16, device="cuda")
+    for part in w.split(1 << 17):
+        part.copy_(torch.randn(part.shape, generator=g, device="cuda") * 2.5 * cols ** -0.5)
+    ids = torch.cat([torch.arange(vocab - 30, vocab), torch.arange(10) * 100003]).cuda()
+    x = output(rows, cols, BF16)
+    ops.embedding(ids, w, x)
+    assert torch.equal(x, w[ids])
+    x.mul_(0.5)
+    loss, lse, grad = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.full((rows,), 0.1, device="cuda")
+    ops.linear_cross_entropy(x, w, ids, loss, lse)
+    logits = torch.cat([x.double() @ part.double().t() for part in w.split(1 << 17)], 1)
+    ref = torch.logsumexp(logits, 1)
+    tail = slice(vocab - 4096, vocab)
+    bound = 2.0 ** -23 * (cols + 8) * x.double().abs().sum(1) * w.abs().max().double() + 2.0 ** -20 + 2.0 ** -24 * 2000 + 2.0 ** -22 * ref
+    within(lse, ref, bound)
+    dx, dw = output(rows, cols), torch.full_like(w, 7.0)
+    ops.linear_cross_entropy_backward(x, w, ids, lse, grad, dx, dw)
+    ops.sync()
+    d = 0.1 * torch.exp(logits - lse.double()[:, None])
+    d.scatter_add_(1, ids[:, None], torch.full((rows, 1), -0.1, dtype=torch.float64, device="cuda"))
+    want = d[:, tail].t() @ x.double()
+    e = (dw[tail].double() - want).norm()
+    # d's roundings and dw's own: 2^-8 of each, at most
+    assert e <= 2 * 2.0 ** -8 * want.norm(), e
+    back = torch.full_like(w, 7.0)
+    ops.embedding_backward(ids, dx, back)
+    ops.sync()
+    assert torch.equal(back[ids], dx.to(BF16))   # (each id once)
+    assert (back[vocab - 5000:vocab - 30] == 0).all() and (back[:100000][1:] == 0).all()
+
+
 # ---- refusals -----------------------------------------------------------------------------
 
 
