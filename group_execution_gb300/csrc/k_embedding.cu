@@ -268,7 +268,9 @@ __global__ void __launch_bounds__(kSortThreads) ts_sort_count_kernel(const __gri
       atomicAdd(&hist[(P.in ? P.in[i].x : id_key(P.ids[i], P.vocab)) >> P.shift & (bins - 1)], 1u);
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) *P.joins = 0;
-  if (!P.in) clear_present(P.present, P.vocab, (int64_t)blockIdx.x * kSortThreads + threadIdx.x, (int64_t)gridDim.x * kSortThreads);
+  if (!P.in)
+    clear_present(P.present, P.vocab, (int64_t)blockIdx.x * kSortThreads + threadIdx.x,
+                  (int64_t)gridDim.x * kSortThreads);
   __syncthreads();
   if ((int)threadIdx.x < bins) P.counts[(int64_t)blockIdx.x * bins + threadIdx.x] = hist[threadIdx.x];
 }

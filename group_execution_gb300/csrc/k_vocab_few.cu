@@ -4,10 +4,11 @@
 // For so small a product the latency of a launch and of a chain of loads is what
 // counts.  So the weight's rows go from memory straight into the registers of
 // mma.sync.m16n8k16, 16 bytes a lane, and nothing is staged: a warp takes 16 rows
-// of w (two n8 tiles) against the 16 rows of x, whose pieces come from L1.  The k index of a fragment is permuted,
-// the same way for both operands, so that a lane's eight consecutive elements
-// serve two MMAs.  Where there are fewer tiles than warps, a tile's K is cut over
-// the warps of a block, and their sums meet in shared memory.
+// of w (two n8 tiles) against the 16 rows of x, whose pieces come from L1.  The k
+// index of a fragment is permuted, the same way for both operands, so that a
+// lane's eight consecutive elements serve two MMAs.  Where there are fewer tiles
+// than warps, a tile's K is cut over the warps of a block, and their sums meet in
+// shared memory.
 //
 // 1 x 1024 x 4000 takes 7 us in a graph, where tiles on the tensor cores' own
 // memory take 11; a step of 16 x 1024 x 8000 or more is faster there.
@@ -61,11 +62,24 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// (volatile: it stays behind the wait for the grid before)
 __device__ __forceinline__ uint4 stream16(const __nv_bfloat16* p) {
   uint4 v;
-  asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "l"(p));
+  return v;
+}
+
+// What other blocks have written in this launch.
+__device__ __forceinline__ float2 load_shared(const float2* p) {
+  float2 v;
+  asm volatile("ld.relaxed.gpu.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ float load_shared(const float* p) {
+  float v;
+  asm volatile("ld.relaxed.gpu.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
   return v;
 }
 
@@ -153,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
           for (int r = 0; r < 2; ++r) {
             xv[r] = make_uint4(0, 0, 0, 0);
             if (xin[r] && st + u < s1 && j < P.cols)
-              xv[r] = P.vec ? __ldg(reinterpret_cast<const uint4*>(xrow[r] + j)) : row_piece(xrow[r], j, P.cols);
+              xv[r] = P.vec ? *reinterpret_cast<const uint4*>(xrow[r] + j) : row_piece(xrow[r], j, P.cols);
           }
 #pragma unroll
           for (int n = 0; n < 2; ++n) {
@@ -271,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           v[k] = make_float2(-INFINITY, 0.f);
-          if (b0 + k * 32 < (int)gridDim.x) v[k] = __ldcg(P.part + (b0 + k * 32) * kFewRows + row);
+          if (b0 + k * 32 < (int)gridDim.x) v[k] = load_shared(P.part + (b0 + k * 32) * kFewRows + row);
         }
 #pragma unroll
         for (int k = 0; k < 8; ++k) join(bm, bs, v[k].x, v[k].y);
@@ -287,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
         if (P.lse) P.lse[row] = lse;
         if (P.loss) {
           const int64_t t = P.targets[row];
-          P.loss[row] = t < 0 || t >= P.vocab ? 0.f : lse == -INFINITY ? INFINITY : lse - __ldcg(P.tlogit + row);
+          P.loss[row] = t < 0 || t >= P.vocab ? 0.f : lse == -INFINITY ? INFINITY : lse - load_shared(P.tlogit + row);
         }
       }
     }

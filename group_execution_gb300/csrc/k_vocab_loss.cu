@@ -9,10 +9,11 @@
 // Everything large is a product on the 5th-generation tensor cores.  Forward:
 // one product whose epilogue reduces each row of a tile's 128 columns to a
 // maximum and a sum of exponentials (8 bytes for 128 logits), which a small
-// kernel joins (k_vocab_few.cu has few rows of small weights).  Backward, for each piece of the vocabulary: the logits again,
-// turned by the epilogue into d, rounded to bf16 (the tensor cores' operand) in
-// the workspace; then, in one launch, the piece's dw and its part of dx, which
-// float32 sums in the workspace collect.
+// kernel joins (k_vocab_few.cu has few rows of small weights).  Backward, for each
+// piece of the vocabulary: the logits again, turned by the epilogue into d,
+// rounded to bf16 (the tensor cores' operand) in the workspace; then, in one
+// launch, the piece's dw and its part of dx, which float32 sums in the workspace
+// collect (one piece that is not cut is dx itself).
 //
 // The product kernel is persistent: CTA pairs walk 256 x 256 tiles (2-SM
 // tcgen05.mma, cta_group::2), K 128 at a time; each CTA stages half of the
@@ -29,8 +30,8 @@
 //               accumulator; it overlaps the next tile's MMAs.
 // At 4096 x 1024 x 50001 the tensor pipe is active in 95 % of the cycles of the
 // loss (206 us, 2.04 PFLOP/s in a single run; 243 in a series of calls, at the
-// power limit), 82 % of the gradient's logits, 93 % of dx and dw (778 us together).
-// 8192 x 4096 x 50001 takes 1860 and 5870 us, 1.80 and 1.71 PFLOP/s.  Few rows are
+// power limit), 82 % of the gradient's logits, 93 % of dx and dw (770 us together).
+// 8192 x 4096 x 50001 takes 1840 and 5820 us, 1.82 and 1.73 PFLOP/s.  Few rows are
 // bound by the weight's bytes: 64 x 4096 x 32000 52 us forward (5.0 TB/s), 157
 // backward.  Models of 256 columns or fewer are bound by the epilogue.
 //

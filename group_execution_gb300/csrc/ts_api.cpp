@@ -149,7 +149,8 @@ fg_status ts_sync_status(ts_ops* h, void* stream) {
   if (flag == 0) return FG_OK;
   e = cudaMemset(h->err, 0, sizeof(int32_t));
   if (e != cudaSuccess) return cuda_err(e, "clearing the device error word");
-  if (flag == DEVERR_TIMEOUT) return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad or ts_linear_cross_entropy expired");
+  if (flag == DEVERR_TIMEOUT)
+    return err(FG_ETIMEOUT, "a device-side wait of ts_weight_grad or ts_linear_cross_entropy expired");
   return err(FG_EDEVICE, "device error word " + std::to_string(flag));
 }
 
