@@ -35,7 +35,7 @@ struct EmbedKernel {
   const int64_t* ids;
   const void* table;
   void* y;
-  int64_t rows, vocab, ldt, ldy, units;
+  int64_t vocab, ldt, ldy, units;
   int cols, packs;   // a unit is GROUPS groups of columns of one token, `packs` of them a token
   float scale;
 };
@@ -803,7 +803,6 @@ cudaError_t launch_embedding(const ts_ops& h, const EmbedArgs& a, cudaStream_t s
   P.ids = a.ids;
   P.table = a.table.p;
   P.y = a.y.p;
-  P.rows = a.rows;
   P.vocab = a.vocab;
   P.ldt = a.table.ld;
   P.ldy = a.y.ld;

@@ -822,7 +822,6 @@ CopyRows copy_of(const TsMat& m, int64_t rows, int cols, void* dst) {
   C.dst = static_cast<__nv_bfloat16*>(dst);
   C.ld = m.ld;
   C.pitch = pitch_of(cols);
-  C.rows = rows;
   C.cols = cols;
   C.units = rows * (C.pitch / 8);
   return C;

@@ -13,7 +13,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 struct CopyRows {
   const __nv_bfloat16* src;
   __nv_bfloat16* dst;
-  int64_t ld, pitch, rows, vocab, units;   // a unit: eight columns of a row
+  int64_t ld, pitch, vocab, units;   // a unit: eight columns of a row
   int cols;
   const int64_t* targets;
   const float* lse;

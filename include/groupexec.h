@@ -542,7 +542,9 @@ void tf_layout_destroy(tf_layout* l);
  * output may overlap an input except where stated (an output that starts where
  * an input does, but has another dtype or row pitch, is FG_EINVAL).  rows = 0 computes empty
  * sums; cols is at least 1; extents are at most 2^31 - 65536.  Results do not
- * depend on scheduling: no sum uses atomics.
+ * depend on scheduling: a sum's order is fixed by the sizes, the workspace's
+ * among them (and, for the embedding's gradient, by the ids), and a value that is
+ * added in memory is added once a launch.
  *
  * A ts_ops handle belongs to the device that is current in ts_create (calls
  * with another current device return FG_EINVAL) and owns a workspace and a
