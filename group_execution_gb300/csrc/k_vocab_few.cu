@@ -83,13 +83,6 @@ __device__ __forceinline__ float load_shared(const float* p) {
   return v;
 }
 
-// Adds (m, s) of a base-2 reference and a sum to another.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float next = fmaxf(m, m2), ref = next == -INFINITY ? 0.f : next;
-  s = s * exp2_approx(m - ref) + s2 * exp2_approx(m2 - ref);
-  m = next;
-}
-
 template <bool BACK>
 __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_constant__ FewKernel P) {
   __shared__ float sums[kWarps][2][32][4];   // K's parts
@@ -246,11 +239,11 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
             else if (v == target[r]) P.tlogit[row] = l[i];
             top = fmaxf(top, l[i]);
           }
-          const float next = fmaxf(m[r], top * kLog2e), ref = next == -INFINITY ? 0.f : next;
+          const float next = fmaxf(m[r], top), ref = next == -INFINITY ? 0.f : next;
           float s = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s += exp2_approx(fmaf(l[i], kLog2e, -ref));
-          sum[r] = sum[r] * exp2_approx(m[r] - ref) + s;
+          for (int i = 0; i < 4; ++i) s += exp2_approx((l[i] - ref) * kLog2e);
+          sum[r] = sum[r] * exp2_approx((m[r] - ref) * kLog2e) + s;
           m[r] = next;
         }
       }
@@ -261,14 +254,14 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
           const float om = __shfl_xor_sync(0xffffffffu, m[r], o), os = __shfl_xor_sync(0xffffffffu, sum[r], o);
-          join(m[r], sum[r], om, os);
+          join_sums(m[r], sum[r], om, os);
         }
         if (q == 0) rows_sm[warp][r * 8 + g] = make_float2(m[r], sum[r]);
       }
     __syncthreads();
     if ((int)threadIdx.x < P.rows) {
       float bm = -INFINITY, bs = 0.f;
-      for (int w = 0; w < kWarps; ++w) join(bm, bs, rows_sm[w][threadIdx.x].x, rows_sm[w][threadIdx.x].y);
+      for (int w = 0; w < kWarps; ++w) join_sums(bm, bs, rows_sm[w][threadIdx.x].x, rows_sm[w][threadIdx.x].y);
       P.part[blockIdx.x * kFewRows + threadIdx.x] = make_float2(bm, bs);
     }
     __threadfence();
@@ -288,20 +281,18 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
           if (b0 + k * 32 < (int)gridDim.x) v[k] = load_shared(P.part + (b0 + k * 32) * kFewRows + row);
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) join(bm, bs, v[k].x, v[k].y);
+        for (int k = 0; k < 8; ++k) join_sums(bm, bs, v[k].x, v[k].y);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) {
         const float om = __shfl_xor_sync(0xffffffffu, bm, o), os = __shfl_xor_sync(0xffffffffu, bs, o);
-        join(bm, bs, om, os);
+        join_sums(bm, bs, om, os);
       }
       if (lane == 0) {
-        // the reference is a rounded log2, the sum relative to it as rounded
-        const float lse = bs == 0.f ? -INFINITY : (bm + log2f(bs)) * kLn2;
-        if (P.lse) P.lse[row] = lse;
+        if (P.lse) P.lse[row] = lse_of(bm, bs);
         if (P.loss) {
           const int64_t t = P.targets[row];
-          P.loss[row] = t < 0 || t >= P.vocab ? 0.f : lse == -INFINITY ? INFINITY : lse - load_shared(P.tlogit + row);
+          P.loss[row] = t < 0 || t >= P.vocab ? 0.f : loss_of(bm, bs, load_shared(P.tlogit + row));
         }
       }
     }

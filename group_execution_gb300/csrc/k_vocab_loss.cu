@@ -85,7 +85,7 @@ struct VocabKernel {
   int slots, slot_bytes;     // of the ring
   int tiles_t, tiles_v, tiles_c;
   // forward
-  float2* part;              // [column parts][rows]: reference (log2) and sum
+  float2* part;              // [column parts][rows]: largest logit, and the sum of exp(l - it)
   float* tlogit;             // the target's logit
   const int64_t* targets;
   // backward
@@ -490,7 +490,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           s0 = chain_end<MODE>(s0, w.kb1);
         }
         if (!ok) break;
-        // the sum's reference is the largest logit, in log2
+        // the sum's reference is the largest logit itself: its term is exactly 1, and
+        // no finite logit overflows, as one in log2 would
         const int left = min(half_n, P.vocab - c0), at = target - c0;
         if (left < kHalf) {
 #pragma unroll
@@ -512,14 +513,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int c = 0; c < 32; ++c) top[c & 3] = fmaxf(top[c & 3], v[j][c]);
-        const float m2 = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * kLog2e;
-        const float ref = m2 == -INFINITY ? 0.f : m2;
+        const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx(fmaf(v[j][c], kLog2e, -ref));
+          for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx((v[j][c] - ref) * kLog2e);
         if (row < P.rows)
-          P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m2, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
 #pragma unroll 1
         for (int j = 0; j < half_n; j += 64) {
@@ -654,11 +655,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ts_loss_join_kernel(const __g
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
-  auto add = [&](float2 v) {
-    const float next = fmaxf(m, v.x), ref = next == -INFINITY ? 0.f : next;
-    s = s * exp2_approx(m - ref) + v.y * exp2_approx(v.x - ref);
-    m = next;
-  };
+  auto add = [&](float2 v) { join_sums(m, s, v.x, v.y); };
   if (row < P.rows) {
     const float2* p = P.part + row;
     for (int k0 = warp; k0 < P.parts; k0 += 8 * kJoinWarps) {
@@ -681,14 +678,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) ts_loss_join_kernel(const __g
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float ref = m == -INFINITY ? 0.f : m;
-  s = warp_sum(v.y * exp2_approx(v.x - ref));
+  s = warp_sum(v.y * exp2_approx((v.x - ref) * kLog2e));
   if (lane || row >= P.rows) return;
-  // the reference is a rounded log2, the sum relative to it as rounded
-  const float lse = s == 0.f ? -INFINITY : (m + log2f(s)) * kLn2;
-  if (P.lse) P.lse[row] = lse;
+  if (P.lse) P.lse[row] = lse_of(m, s);
   if (P.loss) {
     const int64_t t = P.targets[row];
-    P.loss[row] = t < 0 || t >= P.vocab ? 0.f : lse == -INFINITY ? INFINITY : lse - P.tlogit[row];
+    P.loss[row] = t < 0 || t >= P.vocab ? 0.f : loss_of(m, s, P.tlogit[row]);
   }
 }
 

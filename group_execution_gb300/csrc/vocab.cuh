@@ -5,7 +5,7 @@
 
 namespace fg {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // Rows of bf16 that are copied to a pitch that TMA can read.  Rows that take no
 // gradient (without a target, or of an lse of -inf) have d = 0 and may hold
@@ -23,6 +23,19 @@ __device__ __forceinline__ float exp2_approx(float v) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
   return r;
+}
+// A row's logits so far: the largest, m, and s = sum of exp(l - m).  Adds others'.
+__device__ __forceinline__ void join_sums(float& m, float& s, float m2, float s2) {
+  const float next = fmaxf(m, m2), ref = next == -INFINITY ? 0.f : next;
+  s = s * exp2_approx((m - ref) * kLog2e) + s2 * exp2_approx((m2 - ref) * kLog2e);
+  m = next;
+}
+// lse and the target's loss.  The loss is not lse - logit: lse is rounded at the
+// size of the logits, while m - logit is exact where they are close, and log s is
+// never negative (the largest logit's term is 1).
+__device__ __forceinline__ float lse_of(float m, float s) { return s == 0.f ? -INFINITY : m + logf(s); }
+__device__ __forceinline__ float loss_of(float m, float s, float logit) {
+  return s == 0.f ? INFINITY : (m - logit) + logf(s);
 }
 // Eight elements of a row from column j on, zeros past `cols`: out of the two
 // aligned pieces of 16 bytes that hold them, or one by one where those would

@@ -671,8 +671,9 @@ fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, f
  * token, like an embedding's table), both of type dtype, which must be FG_BF16.
  * lse = log sum exp of a row's logits, loss = lse - logits[targets[r]]; either
  * may be NULL (targets too without loss).  A target outside 0 .. vocab - 1
- * leaves its row unscored: loss 0.  The logits and all sums are float32.  A
- * -inf logit has probability 0; a row of nothing else has lse -inf and loss
+ * leaves its row unscored: loss 0.  The logits and all sums are float32, and
+ * loss is not taken from lse as it was rounded: it is as near to its value however
+ * large the logits are, and never negative.  A -inf logit has probability 0; a row of nothing else has lse -inf and loss
  * inf; a row with a NaN or +inf logit gives NaN.  rows, cols and vocab are at
  * most 2^20.
  *

@@ -1,0 +1,91 @@
+"""GPU tests of the vocabulary operators where 32 bits or the workspace end: logits
+near float32's largest value and rows that hold both ends, losses far smaller than
+their logits, sums longer than one accumulator takes, how a workspace cuts a call,
+and outputs in place of inputs."""
+import ctypes as C
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from group_execution_gb300 import FgError, TrainingOps, _lib, linear_cross_entropy_workspace
+from tests.test_gpu_vocab import matrix, normal, output, tied, tokens, within
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module")
+def ops():
+    return TrainingOps(workspace_bytes=256 << 20)
+
+
+# ---- logits at float32's ends --------------------------------------------------------
+
+# rows whose kernel takes K from registers, in one part and in many; tiles: a ragged
+# one, several of them, rows of more than one
+SIZES = [(7, 300), (14, 60001), (40, 300), (300, 1777)]
+
+
+def ends(rows, vocab, masked):
+    """x and w of one column: rows of logits 0.5 to 3; of NaN; of +inf; of values
+    near the largest float32, two of them or (masked) -inf beside them; and,
+    where no weight is -inf, of -inf alone."""
+    w = torch.where(torch.arange(vocab) % 3 == 0, 0.5, 1.0)[:, None]
+    if masked:
+        w[torch.arange(vocab) % 5 == 2] = -INF
+    values = [1.0, NAN, INF, 3e38, 3.0] + ([] if masked else [-INF, -3e38])
+    x = torch.tensor([values[i % len(values)] for i in range(rows)])[:, None]
+    return matrix(x, BF16, 7), matrix(w, BF16, 7)
+
+
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("rows, vocab", SIZES)
+def test_logits_at_the_ends_of_float32(ops, rows, vocab, masked):
+    x, w = ends(rows, vocab, masked)
+    targets = (torch.arange(rows) * 7 % vocab).cuda()
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ops.linear_cross_entropy(x, w, targets, loss, lse)
+    ops.sync()
+    logits = x.double() @ w.double().t()   # (one product each: exact)
+    ref = torch.logsumexp(logits, 1)
+    ref[(logits == INF).any(1)] = NAN
+    # the exponentials and their argument, about 60 + vocab / 1024 additions, the logarithm and lse's rounding
+    error = 2.0 ** -20 + 2.0 ** -24 * (60 + vocab / 1024)
+    within(lse, ref, error + 2.0 ** -23 * ref.abs())
+    at = logits.gather(1, targets[:, None])
+    want = torch.logsumexp(logits - at, 1)   # (lse - logit would lose a small loss in 64 bits too)
+    want[(at == -INF)[:, 0]] = INF
+    want[ref.isnan()] = NAN
+    within(loss, want, error + 2.0 ** -23 * want.abs())
+
+
+# ---- losses that are small beside their logits -----------------------------------------
+
+
+@pytest.mark.parametrize("far", [40.0, 8.0])
+@pytest.mark.parametrize("rows, vocab", [(1, 3000), (16, 40001), (60, 3000), (300, 20011)])
+def test_loss_of_confident_rows(ops, rows, vocab, far):
+    """The target's logit is a, the others' are far below: the loss is as near to
+    its value whatever a is, and never negative."""
+    a = torch.arange(rows) % 30 * 4.0 + 4.0
+    a[rows // 2:] *= 256.0                                   # up to 30720
+    c = -far + torch.arange(vocab) % 8 * 0.25                # (of eight bits, like a: exact in bf16, a + c in float32)
+    t = vocab // 3
+    c[t] = 0.0
+    x = matrix(torch.stack([a, torch.ones(rows)], 1), BF16, 6)
+    w = matrix(torch.stack([torch.ones(vocab), c], 1), BF16, 6)
+    targets = torch.full((rows,), t).cuda()
+    targets[rows // 4] = 0                                   # one that is not its row's largest
+    loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    ops.linear_cross_entropy(x, w, targets, loss, lse)
+    ops.sync()
+    rest = torch.exp(c.double().cuda()).sum() - 1.0          # beside the target's 1
+    want = torch.log1p(rest) - c.double().cuda()[targets]
+    # the others' exponentials and arguments, about 60 + vocab / 1024 additions, the logarithm's and the loss's roundings
+    error = 2.0 ** -20 * rest / (1 + rest) + 2.0 ** -24 * (60 + vocab / 1024) + 2.0 ** -22 * torch.log1p(rest)
+    within(loss, want, error + 2.0 ** -24 * want)
+    assert (loss >= 0).all()
+    within(lse, a.double().cuda() + torch.log1p(rest), error + 2.0 ** -24 * (a.double().cuda() + 1))
