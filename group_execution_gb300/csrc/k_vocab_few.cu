@@ -95,13 +95,13 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
   const int per_block = kWarps / P.ksplit, kp = warp % P.ksplit, group = warp / P.ksplit;
   const int steps = (P.cols + 31) / 32, s0 = steps * kp / P.ksplit, s1 = steps * (kp + 1) / P.ksplit;
   // this thread's rows: g and g + 8
-  float m[2], sum[2], lse2[2], coef[2], gl[2];
+  float m[2], sum[2], lse[2], coef[2], gl[2];
   int target[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int row = r * 8 + g;
       m[r] = -INFINITY;
-      sum[r] = lse2[r] = coef[r] = gl[r] = 0.f;
+      sum[r] = lse[r] = coef[r] = gl[r] = 0.f;
       target[r] = -1;
       if (row < P.rows && P.targets) {
         const int64_t i = P.targets[row];
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
           // (a row of -inf logits takes no gradient)
           const float l = P.lse_in[row];
           const bool none = l == -INFINITY;
-          lse2[r] = none ? 0.f : l * kLog2e;
+          lse[r] = none ? 0.f : l;
           gl[r] = target[r] >= 0 && !none ? P.g_loss[row] : 0.f;
           coef[r] = gl[r] + (P.g_lse && !none ? P.g_lse[row] : 0.f);
         }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int v = v0 + (i >> 1) * 8 + 2 * q + (i & 1);
-            l[i] = coef[r] * exp2_approx(fmaf(l[i], kLog2e, -lse2[r]));
+            l[i] = coef[r] * exp2_approx((l[i] - lse[r]) * kLog2e);
             if (v == target[r]) l[i] -= gl[r];
             if (none || v >= P.vocab) l[i] = 0.f;
           }

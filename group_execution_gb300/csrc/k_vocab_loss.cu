@@ -420,7 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int c0 = w.n0 + set * half_n;   // this warp's first column
       // d is |coef| p - (its sign) g at the target, as bf16 with coef's sign, or
       // masked out; |coef| goes into the exponent
-      float shift = 0.f, g = 0.f;
+      float lse = 0.f, shift = 0.f, g = 0.f;
       uint32_t sign = 0, keep = 0;
       int target = -1;   // the target's column of the piece
       if constexpr (MODE != kGrad) {
@@ -433,7 +433,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (l != -INFINITY) {
               g = t >= 0 && t < P.total ? P.g_loss[row] : 0.f;
               const float coef = g + (P.g_lse ? P.g_lse[row] : 0.f);
-              shift = log2f(fabsf(coef)) - l * kLog2e;
+              lse = l;   // (taken off before the change of base: in log2 a finite one may overflow)
+              shift = log2f(fabsf(coef));
               if (coef < 0.f) {
                 sign = 0x80008000u;
                 g = -g;
@@ -531,7 +532,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (j + 64 == half_n && k == 1) release();
             const int cc = c0 + j + 32 * k, left = P.vocab - cc, at = target - cc;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = exp2_approx(fmaf(v[c], kLog2e, shift));
+            for (int c = 0; c < 32; ++c) v[c] = exp2_approx(fmaf(v[c] - lse, kLog2e, shift));
             if (at >= 0 && at < 32) {
 #pragma unroll
               for (int c = 0; c < 32; ++c) v[c] -= c == at ? g : 0.f;

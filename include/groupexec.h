@@ -673,9 +673,9 @@ fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, f
  * may be NULL (targets too without loss).  A target outside 0 .. vocab - 1
  * leaves its row unscored: loss 0.  The logits and all sums are float32, and
  * loss is not taken from lse as it was rounded: it is as near to its value however
- * large the logits are, and never negative.  A -inf logit has probability 0; a row of nothing else has lse -inf and loss
- * inf; a row with a NaN or +inf logit gives NaN.  rows, cols and vocab are at
- * most 2^20.
+ * large the logits are, and never negative.  A -inf logit has probability 0; a
+ * row of nothing else has lse -inf and loss inf; a row with a NaN or +inf logit
+ * gives NaN.  rows, cols and vocab are at most 2^20.
  *
  * Its gradient: with d = (g_loss + g_lse) * exp(logits - lse) - g_loss *
  * onehot(target), from the lse it wrote, dx = d w and dw = d^T x, added to

@@ -62,6 +62,34 @@ def test_logits_at_the_ends_of_float32(ops, rows, vocab, masked):
     within(loss, want, error + 2.0 ** -23 * want.abs())
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("rows, vocab", SIZES)
+def test_gradient_of_logits_at_the_ends_of_float32(ops, rows, vocab, masked):
+    x, w = ends(rows, vocab, masked)
+    logits = x.double() @ w.double().t()
+    lse = torch.logsumexp(logits, 1).float()
+    g = ((0.25 + torch.arange(rows) % 3 * 0.5) / 1024).cuda()
+    targets = (torch.arange(rows) * 7 % vocab).cuda()
+    bad = logits.isnan().any(1) | (logits == INF).any(1)
+    targets[bad] = -1                                        # not scored: may hold anything
+    dx, dw = output(rows, 1), output(vocab, 1)
+    ops.linear_cross_entropy_backward(x, w, targets, lse, g, dx, dw)
+    ops.sync()
+    takes = ~bad & (lse != -INF)
+    d = torch.exp(logits - lse.double()[:, None]) * g.double()[:, None]
+    d[takes] = d[takes].scatter_add(1, targets[takes][:, None], -g[takes].double()[:, None])
+    d[~takes] = 0.0
+    # an exponential's 2^-20 and one rounding to bf16, the sums' additions
+    off = 2.0 ** -8 * d.abs() + 2.0 ** -19 * g.double()[:, None] + 1e-37
+    off[~takes] = 0.0
+    xd = torch.where(takes[:, None], x.double(), 0.0)
+    within(dw, d.t() @ xd, off.t() @ xd.abs() + 2.0 ** -23 * (rows + 8) * (d.abs().t() @ xd.abs()))
+    if not masked:   # (0 * -inf is NaN in dx)
+        wd = w.double()
+        within(dx, d @ wd, off @ wd.abs() + 2.0 ** -23 * (vocab + 8) * (d.abs() @ wd.abs()))
+        assert (dx[~takes] == 0).all()
+
+
 # ---- losses that are small beside their logits -----------------------------------------
 
 
