@@ -100,15 +100,20 @@ struct VocabKernel {
   int inject;
 };
 
-// A float32 accumulator of 4096 products is 2e-6 off, one of 1024 5e-7: the
-// tensor core truncates as it adds.  The loss is a float32 result, so its sums
-// run over at most kChain blocks of K; the epilogue's threads add what they came
-// to in registers, during the next one's MMAs.  (The gradients' sums are of
-// operands rounded to bf16.)
-constexpr int kChain = 8;
-template <int MODE>
+// The tensor core truncates as it adds, so that a float32 accumulator's error
+// grows with its products, to one side: 2e-6 of 4096, 1.4e-3 of 524288 of one
+// sign.  So a sum runs over a chain of at most 8 blocks of K for the loss (5e-7),
+// a float32 result, and 16 for the gradients, which sum over all rows or the whole
+// vocabulary (of operands in bf16); the epilogue's threads add what the chains
+// came to in registers, during the next one's MMAs.  (d is rounded to bf16, and its
+// logits' K is a model's width: one chain.  Gradients whose items are a chain at
+// most have a kernel without the registers that several take: 16 x 1024 x 4000
+// 16.8 us, with them 17.9.)
+constexpr int kLossChain = 8, kGradChain = 16;
+template <int MODE, bool CHAINS>
 __device__ __forceinline__ int chain_end(int kb0, int kb1) {
-  return MODE == kLoss && kb1 - kb0 > kChain ? kb0 + kChain : kb1;
+  constexpr int kChain = MODE == kLoss ? kLossChain : kGradChain;
+  return CHAINS && kb1 - kb0 > kChain ? kb0 + kChain : kb1;
 }
 
 // What a pair works on: a tile at (m0, n0) of a product, over blocks [kb0, kb1)
@@ -234,25 +239,38 @@ struct Stage {
   }
 };
 
-// A lane's column of the stage's first n rows, to rows `ld` apart.
-template <class T>
-__device__ __forceinline__ void to_rows(const Stage& stage, T* d, int64_t ld, int n, bool add) {
+// A lane's column of the stage's first n rows, to rows `ld` apart.  float32 rows are
+// added to in memory, as TMA does it; bf16 ones are read, four at a time.
+__device__ __forceinline__ void to_rows(const Stage& stage, float* d, int64_t ld, int n, bool add) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int r = 0; r < 32; r += 8, d += 8 * ld) {
-    float old[8] = {};
+  for (int r = 0; r < 32; r += 4, d += 4 * ld) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (r + i >= n) break;
+      if (add) atomicAdd(d + i * ld, stage.get(r + i, lane));
+      else d[i * ld] = stage.get(r + i, lane);
+    }
+  }
+}
+__device__ __forceinline__ void to_rows(const Stage& stage, __nv_bfloat16* d, int64_t ld, int n, bool add) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int r = 0; r < 32; r += 4, d += 4 * ld) {
+    float old[4] = {};
     if (add) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int i = 0; i < 4; ++i)
         if (r + i < n) old[i] = to_f32(d[i * ld]);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (r + i < n) d[i * ld] = from_f32<T>(old[i] + stage.get(r + i, lane));
+    for (int i = 0; i < 4; ++i)
+      if (r + i < n) d[i * ld] = from_f32<__nv_bfloat16>(old[i] + stage.get(r + i, lane));
   }
 }
 
-template <int MODE>
+// CHAINS: items may take more than one chain.
+template <int MODE, bool CHAINS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ts_vocab_kernel(const __grid_constant__ VocabKernel P) {
   extern __shared__ uint8_t smem_raw[];
@@ -362,7 +380,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t a_half = (a_mn ? 4 * 2048 : a_box) >> 4, b_half = (b_mn ? 4 * 2048 : b_box) >> 4;
         int s0 = w.kb0;
         do {
-          const int s1 = chain_end<MODE>(s0, w.kb1), b = i & 1;
+          const int s1 = chain_end<MODE, CHAINS>(s0, w.kb1), b = i & 1;
           if (i >= 2 && !wait_bar(tempty0 + 8 * b, ((i >> 1) & 1) ^ 1, P.wait_limit_ns, &abort_flag)) {
             ok = false;
             break;
@@ -459,22 +477,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive_cluster(cluster_addr(tempty0 + 8 * (i & 1), 0));
         ++i;
       };
-      if constexpr (MODE != kLoss) {
-        if (!next_acc()) break;
-      }
-      // before the stage is written again, its last store has read it
-      auto stage_free = [&]() {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-      };
-      auto stage_full = [&]() {
-        fence_proxy_async_smem();
-        __syncwarp();
-      };
-      if constexpr (MODE == kLoss) {
-        float v[4][32];
-        for (int s0 = w.kb0; s0 < w.kb1;) {
-          if (!next_acc()) break;
+      // a thread's half row, the chains added up
+      auto collect = [&](float (&v)[4][32]) {
+        int s0 = w.kb0;
+        do {
+          if (!next_acc()) return;
           if (s0 == w.kb0) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) tmem_ld32(acc + 32 * j, v[j]);
@@ -488,8 +495,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           release();
-          s0 = chain_end<MODE>(s0, w.kb1);
-        }
+          s0 = chain_end<MODE, CHAINS>(s0, w.kb1);
+        } while (s0 < w.kb1);
+      };
+      // before the stage is written again, its last store has read it
+      auto stage_free = [&]() {
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+      };
+      auto stage_full = [&]() {
+        fence_proxy_async_smem();
+        __syncwarp();
+      };
+      if constexpr (MODE == kLoss) {
+        float v[4][32];
+        collect(v);
         if (!ok) break;
         // the sum's reference is the largest logit itself: its term is exactly 1, and
         // no finite logit overflows, as one in log2 would
@@ -523,6 +543,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (row < P.rows)
           P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
+        if (!next_acc()) break;
 #pragma unroll 1
         for (int j = 0; j < half_n; j += 64) {
 #pragma unroll
@@ -564,25 +585,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else to_rows(stage, static_cast<float*>(out.p) + at, out.ld, n, out.add);
           __syncwarp();
         };
-#pragma unroll 1
+        float v[CHAINS ? 4 : 1][32];
+        bool one = true;
+        if constexpr (CHAINS) {
+          one = chain_end<MODE, CHAINS>(w.kb0, w.kb1) == w.kb1;
+          if (!one) collect(v);
+        }
+        if (one) next_acc();
+        if (!ok) break;
+#pragma unroll (CHAINS ? 2 : 1)
         for (int j = 0; j < kHalf; j += 64) {
           const bool tma = out.tma && (out.whole || c0 + j + 64 <= P.cols);
           const bool both = tma && out.bf16;   // both 32 columns in one store
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float v[32];
-            tmem_ld32(acc + j + 32 * k, v);
-            if (j + 64 == kHalf && k == 1) release();
+            float (&u)[32] = v[CHAINS ? j / 32 + k : 0];
+            if (one) {
+              tmem_ld32(acc + j + 32 * k, u);
+              if (j + 64 == kHalf && k == 1) release();
+            }
             if (!both || k == 0) stage_free();
             if (w.kb0 == w.kb1) {   // (a piece of fewer blocks than dx is cut in)
 #pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] = 0.f;
+              for (int c = 0; c < 32; ++c) u[c] = 0.f;
             }
             if (both) {
-              stage.put_bf16(lane, k, v);
+              stage.put_bf16(lane, k, u);
               if (k == 0) continue;
             } else {
-              stage.put_f32(lane, v);
+              stage.put_f32(lane, u);
               if (!tma) {
                 by_threads(j + 32 * k);
                 continue;
@@ -776,8 +807,8 @@ cudaError_t resident_pairs(int device, int* out) {
   static std::atomic<int> cached[64];
   int n = device < 64 ? cached[device].load(std::memory_order_acquire) : 0;
   if (!n) {
-    const void* kernels[3] = {(const void*)ts_vocab_kernel<kLoss>, (const void*)ts_vocab_kernel<kDlogits>,
-                              (const void*)ts_vocab_kernel<kGrad>};
+    const void* kernels[4] = {(const void*)ts_vocab_kernel<kLoss, true>, (const void*)ts_vocab_kernel<kDlogits, false>,
+                              (const void*)ts_vocab_kernel<kGrad, false>, (const void*)ts_vocab_kernel<kGrad, true>};
     for (const void* k : kernels) {
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
@@ -789,7 +820,7 @@ cudaError_t resident_pairs(int device, int* out) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, ts_vocab_kernel<kGrad>, &cfg);
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, ts_vocab_kernel<kGrad, true>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorLaunchOutOfResources;
     if (device < 64) cached[device].store(n, std::memory_order_release);
@@ -876,12 +907,12 @@ Schedule schedule(int64_t nx, int64_t cx, int64_t nw, int64_t cw, int pairs) {
 // operands' rows (256 bytes each) as there is room for.  (Three where there could
 // be six cost 33 x 1024 x 4000 1.5 of its 8 us: the way of a copy is longer than
 // the MMAs of two slots.)
-template <int MODE>
+template <int MODE, bool CHAINS>
 cudaError_t launch_product(VocabKernel& P, int64_t pairs, cudaStream_t st) {
   const int b_rows = MODE != kGrad ? P.tile_n / 2 : P.nx ? kHalf : P.box_rows;
   P.slot_bytes = (P.box_rows + b_rows) * 2 * kRowBytes;
   P.slots = std::min(kMaxSlots, kRingBytes / P.slot_bytes);
-  return launch(ts_vocab_kernel<MODE>, 2 * pairs, kThreads, kSmem, P, st);
+  return launch(ts_vocab_kernel<MODE, CHAINS>, 2 * pairs, kThreads, kSmem, P, st);
 }
 
 // The forward pass's workspace for `rows` rows, its copy of w's rows aside: two
@@ -989,7 +1020,7 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
       P.part = const_cast<float2*>(J.part) + J.parts * rows;
       J.parts += 2 * P.tiles_v;
       const int64_t items = (int64_t)P.tiles_t * P.tiles_v;
-      e = launch_product<kLoss>(P, std::min<int64_t>(pairs, items), st);
+      e = launch_product<kLoss, true>(P, std::min<int64_t>(pairs, items), st);
       if (e != cudaSuccess) return e;
     }
     e = launch(ts_loss_join_kernel, (rows + 31) / 32, kJoinWarps * 32, 0, J, st);
@@ -1119,7 +1150,7 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
       if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, P.tile_n / 2);
       if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
       if (e != cudaSuccess) return e;
-      e = launch_product<kDlogits>(P, std::min<int64_t>(pairs, tiles_t * P.tiles_v), st);
+      e = launch_product<kDlogits, false>(P, std::min<int64_t>(pairs, tiles_t * P.tiles_v), st);
       P.copy.units = 0;
     }
     if (e == cudaSuccess && a.dw.p) {
@@ -1139,7 +1170,9 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
     P.dw_first = s.dw_first;
     P.late = s.late;
     P.extra = s.extra;
-    e = launch_product<kGrad>(P, np, st);
+    const int64_t dx_blocks = P.nx ? ((nv + kKB - 1) / kKB + splits - 1) / splits : 0;
+    const int64_t most_blocks = std::max(dx_blocks, P.nw ? (a.rows + kKB - 1) / kKB : 0);
+    e = most_blocks > kGradChain ? launch_product<kGrad, true>(P, np, st) : launch_product<kGrad, false>(P, np, st);
   }
   if (direct) return e;
   if (e != cudaSuccess || !a.dx.p) return e;

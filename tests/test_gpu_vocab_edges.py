@@ -117,3 +117,50 @@ def test_loss_of_confident_rows(ops, rows, vocab, far):
     within(loss, want, error + 2.0 ** -24 * want)
     assert (loss >= 0).all()
     within(lse, a.double().cuda() + torch.log1p(rest), error + 2.0 ** -24 * (a.double().cuda() + 1))
+
+
+# ---- sums longer than one accumulator ----------------------------------------------------
+
+# An MMA adds 16 products to its accumulator, and each of the 17 may lose 2^-24 of
+# the sum (the tensor core truncates).  An accumulator takes 2048 products, whose
+# partial sums are half of the last on average; what accumulators come to is added in
+# float32, rounded to nearest.  All terms are of one sign and d is exact in bf16.
+
+
+def sum_bound(n):
+    return 17 * 2.0 ** -24 * (2048 / 16) / 2 + 2.0 ** -24 * (n / 2048 + 4)
+
+
+def test_weight_gradient_of_many_rows():
+    rows, cols, vocab = 1 << 19, 64, 128
+    ops = TrainingOps(workspace_bytes=640 << 20)
+    x = (1 + torch.rand((rows, cols), generator=torch.Generator(device="cuda").manual_seed(0), device="cuda")).to(BF16)
+    w = torch.zeros((vocab, cols), dtype=BF16, device="cuda")
+    targets = torch.full((rows,), -1, device="cuda")
+    lse = torch.full((rows,), vocab, device="cuda").log()
+    one = torch.ones(rows, device="cuda")
+    dw = output(vocab, cols)
+    ops.linear_cross_entropy_backward(x, w, targets, lse, one, None, dw, g_lse=one)
+    ops.sync()
+    ref = (x.sum(0, dtype=torch.float64) / vocab).expand(vocab, cols)
+    within(dw, ref, sum_bound(rows) * ref)
+
+
+def test_input_gradient_of_a_large_vocabulary():
+    # (as many tiles of dx as leave its sums uncut)
+    rows, cols, vocab = 4096, 4096, 1 << 19
+    ops = TrainingOps(workspace_bytes=5 << 30)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    w = torch.empty((vocab, cols), dtype=BF16, device="cuda")
+    for part in w.split(1 << 16):
+        part.copy_(1 + torch.rand(part.shape, generator=gen, device="cuda"))
+    x = torch.zeros((rows, cols), dtype=BF16, device="cuda")
+    targets = torch.full((rows,), -1, device="cuda")
+    lse = torch.full((rows,), vocab, device="cuda").log()
+    one = torch.ones(rows, device="cuda")
+    dx = output(rows, cols)
+    ops.linear_cross_entropy_backward(x, w, targets, lse, one, dx, None, g_lse=one)
+    ops.sync()
+    ref = torch.stack([part.sum(0, dtype=torch.float64) for part in w.split(1 << 16)]).sum(0) / vocab
+    ref = ref.expand(rows, cols)
+    within(dx, ref, sum_bound(vocab) * ref)
