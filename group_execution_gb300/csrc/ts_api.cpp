@@ -2,6 +2,7 @@
 // checks, the handle with its workspace and error word, and the launches.
 #include <cuda_runtime.h>
 
+#include <initializer_list>
 #include <memory>
 #include <new>
 #include <string>
@@ -68,6 +69,12 @@ fg_status check_in_place(const char* names, const void* out_p, int out_dtype, in
                          int in_dtype, int64_t in_ld, int64_t rows) {
   if (out_p && out_p == in_p && (out_dtype != in_dtype || (rows > 1 && out_ld != in_ld)))
     return err(FG_EINVAL, std::string(names) + " needs the same dtype and row pitch");
+  return FG_OK;
+}
+// An output that may not lie on any of these.
+fg_status check_apart(const char* name, const void* out_p, std::initializer_list<const void*> others) {
+  for (const void* p : others)
+    if (out_p && out_p == p) return err(FG_EINVAL, std::string(name) + " starts where another argument does");
   return FG_OK;
 }
 fg_status check_vocab(int64_t vocab) {
@@ -376,6 +383,7 @@ fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* 
   TS_TRY(check_matrix("table", table, table_dtype, ld_table, rows > 0 ? vocab : 0, cols));
   TS_TRY(check_matrix("y", y, y_dtype, ldy, rows, cols));
   if (rows == 0) return FG_OK;
+  TS_TRY(check_apart("y", y, {ids, table}));
   EmbedArgs a;
   a.ids = ids;
   a.rows = rows;
@@ -396,6 +404,7 @@ fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, f
   TS_TRY(check_array("ids", ids, rows > 0, 8));
   TS_TRY(check_matrix("dy", dy, dy_dtype, lddy, rows, cols));
   TS_TRY(check_matrix("dtable", dtable, d_dtype, ldd, vocab, cols));
+  if (rows > 0) TS_TRY(check_apart("dtable", dtable, {ids, dy}));
   TS_TRY(check_workspace(h, embedding_backward_workspace(rows, vocab)));
   EmbedArgs a;
   a.ids = ids;
@@ -433,6 +442,8 @@ fg_status ts_linear_cross_entropy(ts_ops* h, const void* x, int64_t ldx, const v
   TS_TRY(check_array("loss", loss, false));
   TS_TRY(check_array("lse", lse, false));
   if (rows == 0) return FG_OK;
+  TS_TRY(check_apart("loss", loss, {x, w, targets, lse}));
+  TS_TRY(check_apart("lse", lse, {x, w, targets}));
   VocabLossArgs a;
   a.x = mat(x, dtype, ldx);
   a.w = mat(w, dtype, ldw);
@@ -463,6 +474,11 @@ fg_status ts_linear_cross_entropy_backward(ts_ops* h, const void* x, int64_t ldx
   TS_TRY(check_array("g_lse", g_lse, false));
   if (dx) TS_TRY(check_matrix("dx", dx, dx_dtype, lddx, rows, cols));
   if (dw) TS_TRY(check_matrix("dw", dw, dw_dtype, lddw, vocab, cols));
+  if (rows > 0) {
+    TS_TRY(check_in_place("dx in place of x", dx, dx_dtype, lddx, x, dtype, ldx, rows));
+    TS_TRY(check_apart("dx", dx, {w, targets, lse, g_loss, g_lse, dw}));
+    TS_TRY(check_apart("dw", dw, {x, w, targets, lse, g_loss, g_lse}));
+  }
   VocabLossArgs a;
   a.x = mat(x, dtype, ldx);
   a.w = mat(w, dtype, ldw);

@@ -540,11 +540,13 @@ void tf_layout_destroy(tf_layout* l);
  * bytes run faster); vectors and row statistics are dense float32.  All
  * arithmetic and all sums are in float32; a bf16 output is rounded once.  No
  * output may overlap an input except where stated (an output that starts where
- * an input does, but has another dtype or row pitch, is FG_EINVAL).  rows = 0 computes empty
- * sums; cols is at least 1; extents are at most 2^31 - 65536.  Results do not
- * depend on scheduling: a sum's order is fixed by the sizes, the workspace's
- * among them (and, for the embedding's gradient, by the ids), and a value that is
- * added in memory is added once a launch.
+ * an input does, but has another dtype or row pitch, is FG_EINVAL; the embedding
+ * and the cross entropy refuse every output that starts where another argument
+ * does, but for dx on x).  rows = 0 computes empty sums; cols is at least 1;
+ * extents are at most 2^31 - 65536.  Results do not depend on scheduling: a sum's
+ * order is fixed by the sizes, the workspace's among them (and, for the
+ * embedding's gradient, by the ids), and a value that is added in memory is added
+ * once a launch.
  *
  * A ts_ops handle belongs to the device that is current in ts_create (calls
  * with another current device return FG_EINVAL) and owns a workspace and a
@@ -682,7 +684,8 @@ fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, f
  * what dw holds when accumulate = 1.  dx and dw are FG_F32 or FG_BF16, either
  * may be NULL; g_lse may be NULL.  d is rounded to bf16, as an operand of the
  * tensor cores; the sums are float32.  An unscored row takes only g_lse's part
- * (without g_lse it may hold anything), a row of -inf logits none.
+ * (without g_lse it may hold anything), a row of -inf logits none.  dx may be x
+ * when dtype and pitch agree.
  *
  * The workspace bounds how many rows (forward) or how much of the vocabulary
  * (backward) is taken at a time: ts_linear_cross_entropy_workspace gives the

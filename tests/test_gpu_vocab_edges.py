@@ -164,3 +164,64 @@ def test_input_gradient_of_a_large_vocabulary():
     ref = torch.stack([part.sum(0, dtype=torch.float64) for part in w.split(1 << 16)]).sum(0) / vocab
     ref = ref.expand(rows, cols)
     within(dx, ref, sum_bound(vocab) * ref)
+
+
+# ---- outputs in place of inputs --------------------------------------------------------------
+
+
+@pytest.mark.parametrize("size", [(9, 264, 3001), (700, 264, 3001), (33, 1003, 700)])
+def test_input_gradient_in_place(size):
+    """dx may be x: with room for the whole vocabulary, and for a piece at a time."""
+    rows, cols, vocab = size
+    for room in (0, 1):
+        ops = TrainingOps(workspace_bytes=max(1 << 20, linear_cross_entropy_workspace(*size)[1 - room]))
+        _, targets, w, _, loss, lse, g, _, dw = tied(*size)
+        x = normal(4, rows, cols).cuda().to(BF16)
+        ops.linear_cross_entropy(x, w, targets, loss, lse)
+        dx, dw2 = torch.empty_like(x), torch.empty_like(dw)
+        ops.linear_cross_entropy_backward(x, w, targets, lse, g, dx, dw)
+        ops.linear_cross_entropy_backward(x, w, targets, lse, g, x, dw2)
+        ops.sync()
+        assert torch.equal(dx, x) and torch.equal(dw, dw2)
+
+
+def test_outputs_in_place_of_inputs_are_refused(ops):
+    """An output that starts where an input does reaches no kernel, dx on an x of
+    its own dtype and pitch aside."""
+    buf = torch.zeros(8192, device="cuda")
+
+    def at(rows, cols, dtype, ld):
+        return torch.as_strided(buf.view(dtype), (rows, cols), (ld, 1))
+
+    x, w = torch.zeros((4, 64), dtype=BF16, device="cuda"), torch.zeros((9, 64), dtype=BF16, device="cuda")
+    ids, v, u = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    xs, ws, vs = at(4, 64, BF16, 64), at(9, 64, BF16, 64), buf[:4]
+    ls = buf[:8].view(torch.int64)
+    back = ops.linear_cross_entropy_backward
+    bad = [
+        lambda: ops.embedding(ids, ws, xs),
+        lambda: ops.embedding(ids, ws, at(4, 64, F32, 64)),
+        lambda: ops.embedding(ls, w, xs),
+        lambda: ops.embedding_backward(ids, xs, ws),
+        lambda: ops.embedding_backward(ids, xs, at(9, 64, F32, 64)),
+        lambda: ops.embedding_backward(ls, x, ws),
+        lambda: ops.linear_cross_entropy(xs, w, ids, vs, u),
+        lambda: ops.linear_cross_entropy(x, ws, ids, u, vs),
+        lambda: ops.linear_cross_entropy(x, w, ls, vs, u),
+        lambda: ops.linear_cross_entropy(x, w, ids, vs, vs),
+        lambda: back(xs, w, ids, v, v, at(4, 64, BF16, 72), None),
+        lambda: back(xs, w, ids, v, v, at(4, 64, F32, 64), None),
+        lambda: back(x, ws, ids, v, v, xs, None),
+        lambda: back(x, ws, ids, v, v, None, ws),
+        lambda: back(xs, w, ids, v, v, None, ws),
+        lambda: back(x, w, ids, v, v, xs, ws),
+        lambda: back(x, w, ids, vs, v, xs, None),
+        lambda: back(x, w, ids, v, vs, None, ws),
+        lambda: back(x, w, ids, v, v, None, ws, g_lse=vs),
+        lambda: back(x, w, ls, v, v, xs, None),
+    ]
+    for f in bad:
+        with pytest.raises(FgError) as e:
+            f()
+        assert e.value.status == _lib.FG_EINVAL
+    ops.sync()
