@@ -954,10 +954,13 @@ cudaError_t launch_vocab_loss(const ts_ops& h, const VocabLossArgs& a, cudaStrea
   if (e != cudaSuccess) return e;
   const bool copy_x = !rows_aligned(a.x), copy_w = !rows_aligned(a.w);
   const int64_t pitch = pitch_of(a.cols);
-  // w's rows are copied whole, or as many at a time as half of the workspace takes
+  // w's rows are copied whole where they fit beside all of x's, or as many at a time
+  // as half of the workspace takes
   int64_t piece = a.vocab, wbytes = 0;
   if (copy_w) {
-    piece = std::min<int64_t>(tiles(a.vocab), std::max<int64_t>(1, h.ws_bytes / 2 / (kTile * pitch * 2))) * kTile;
+    piece = tiles(a.vocab) * kTile;
+    if (forward_bytes(a.rows, a.cols, a.vocab, copy_x) + piece * pitch * 2 > h.ws_bytes)
+      piece = std::min<int64_t>(piece, std::max<int64_t>(1, h.ws_bytes / 2 / (kTile * pitch * 2)) * kTile);
     wbytes = piece * pitch * 2;
   }
   // all rows at once, or as many as leave w's room

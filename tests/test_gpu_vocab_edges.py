@@ -166,6 +166,42 @@ def test_input_gradient_of_a_large_vocabulary():
     within(dx, ref, sum_bound(vocab) * ref)
 
 
+# ---- how a workspace cuts a call -----------------------------------------------------------
+
+
+def launches(call):
+    """How many kernels a call launches: the nodes of its captured graph."""
+    cu = C.CDLL("libcuda.so.1")
+    stream, graph, n = torch.cuda.Stream(), C.c_void_p(), C.c_size_t()
+    at = C.c_void_p(stream.cuda_stream)
+    torch.cuda.synchronize()
+    assert cu.cuStreamBeginCapture_v2(at, 1) == 0
+    call(stream.cuda_stream)
+    assert cu.cuStreamEndCapture(at, C.byref(graph)) == 0
+    assert cu.cuGraphGetNodes(graph, None, C.byref(n)) == 0
+    assert cu.cuGraphDestroy(graph) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("rows, cols, vocab", [(64, 1001, 20000), (200, 1003, 50001), (1000, 65, 3001)])
+def test_loss_in_the_most_workspace(rows, cols, vocab):
+    """What the query calls the most takes all rows and the whole vocabulary at
+    once, copies of unaligned rows too: as any larger workspace does."""
+    x, w = matrix(normal(1, rows, cols), BF16, 0, 1), matrix(normal(2, vocab, cols, scale=cols ** -0.5), BF16, 0, 1)
+    targets = tokens(3, rows, vocab).cuda()
+    most = linear_cross_entropy_workspace(rows, cols, vocab)[1]
+    got = []
+    for size in (most, 8 * most):
+        ops = TrainingOps(workspace_bytes=size)
+        loss, lse = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+        ops.linear_cross_entropy(x, w, targets, loss, lse)
+        ops.sync()
+        # the copies of x and w, the products, the join
+        assert launches(lambda s: ops.linear_cross_entropy(x, w, targets, loss, lse, stream=s)) == 4
+        got.append((loss, lse))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
 # ---- outputs in place of inputs --------------------------------------------------------------
 
 
