@@ -25,7 +25,7 @@
 //   warp 1      allocates TMEM (two accumulators) and, in the even CTA, issues
 //               the MMAs from one thread,
 //   warp 2      TMA producer of the B half,
-//   warp 3      copies x for dw beside the first piece's logits,
+//   warp 3      copies x for dw beside the first piece's logits, where that hides it,
 //   warps 4-11  epilogue: a thread owns half of one row of the CTA's 128 x 256
 //               accumulator; it overlaps the next tile's MMAs.
 // At 4096 x 1024 x 50001 the tensor pipe is active in 95 % of the cycles of the
@@ -873,6 +873,18 @@ int logits_width(int64_t tiles_t, int64_t vocab, int pairs) {
 // which takes as long as reading.
 int box_rows(int64_t rows) { return (int)std::min<int64_t>(kHalf, round_up(rows, 16)); }
 
+// Whether dw's copy of x (`units` of 16 bytes) fits beside the first piece's logits:
+// a warp of each CTA takes 1 to 2 us for every 128 units, the pair 0.5 us for each
+// block of K of its items; before them it is a launch, 3 us, and bound by memory.
+// (Backward, us, beside and before: 300 x 256 x 1000 15.3 and 16.1, 2048 x 256 x
+// 32000 95 and 98, 4096 x 1024 x 8000 137 and 132, 8192 x 4096 x 8000 1000 and 892,
+// 16384 x 2048 x 4000 756 and 456, 256 x 4096 x 100 491 and 27.)
+bool copy_beside(int64_t units, int64_t items, int64_t cols, int pairs) {
+  const int64_t ctas = 2 * std::min<int64_t>(items, pairs);
+  const int64_t blocks = (items + pairs - 1) / pairs * ((cols + kKB - 1) / kKB);
+  return units / (ctas * 128) <= blocks / 4 + 3;
+}
+
 // An item of dw takes at least about three blocks of K for its epilogue.
 int64_t dw_blocks(int64_t rows) { return std::max<int64_t>(3, (rows + kKB - 1) / kKB); }
 
@@ -1097,8 +1109,8 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
   P.err = h.err;
   P.wait_limit_ns = h.wait_limit_ns;
   P.inject = h.inject;
-  // dw's copy of x: beside the first piece's logits, or before them where TMA
-  // cannot read x itself
+  // dw's copy of x: beside the first piece's logits, or before them where they are
+  // too short to hide it, or TMA cannot read x itself
   TsMat x = a.x;
   CopyRows C = copy_of(a.x, a.rows, a.cols, xcopy);
   C.targets = a.g_lse ? nullptr : a.targets;
@@ -1114,7 +1126,13 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
     x.p = xcopy;
     x.ld = pitch;
   } else if (a.dw.p) {
-    P.copy = C;
+    const int64_t first = std::min(piece, a.vocab), width = logits_width(tiles_t, first, pairs);
+    if (copy_beside(C.units, tiles_t * ((first + width - 1) / width), a.cols, pairs)) {
+      P.copy = C;
+    } else {
+      e = launch_copy(C, st);
+      if (e != cudaSuccess) return e;
+    }
   }
   auto describe = [](Out& o, const TsOut& m, int64_t rows, int cols, bool add) {
     o.p = m.p;

@@ -9,7 +9,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from group_execution_gb300 import FgError, TrainingOps, _lib, linear_cross_entropy_workspace
-from tests.test_gpu_vocab import matrix, normal, output, tied, tokens, within
+from tests.test_gpu_vocab import check_backward, matrix, normal, output, run_backward, tied, tokens, within
 
 pytestmark = pytest.mark.gpu
 
@@ -200,6 +200,23 @@ def test_loss_in_the_most_workspace(rows, cols, vocab):
         assert launches(lambda s: ops.linear_cross_entropy(x, w, targets, loss, lse, stream=s)) == 4
         got.append((loss, lse))
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("rows, cols, vocab, before", [(256, 4096, 100, 1), (1000, 1024, 777, 1), (3000, 264, 300, 1),
+                                                      (300, 256, 1000, 0)])
+def test_copy_of_x_is_no_longer_than_the_logits(ops, rows, cols, vocab, before):
+    """dw's copy of x has a launch of its own where the logits are too few to hide it."""
+    x, w = matrix(normal(1, rows, cols), BF16), matrix(normal(2, vocab, cols, scale=2.5 * cols ** -0.5), BF16)
+    targets = tokens(3, rows, vocab).cuda()
+    lse = torch.logsumexp(x.double() @ w.double().t(), 1).float()
+    g = (normal(4, rows) / rows).cuda()
+    x[(targets < 0) | (targets >= vocab)] = NAN              # unscored rows may hold anything
+    dx, dw = run_backward(ops, x, w, targets, lse, g, None, BF16, F32, 0, 0)
+    check_backward(x, w, targets, lse, g, None, dx, dw)
+
+    def count(dx, dw):
+        return launches(lambda s: ops.linear_cross_entropy_backward(x, w, targets, lse, g, dx, dw, stream=s))
+    assert count(dx, dw) == count(dx, None) + before
 
 
 # ---- outputs in place of inputs --------------------------------------------------------------
