@@ -229,7 +229,8 @@ class TrainingOps:
 
     def embedding_backward(self, ids, dy, dtable, scale=1.0, accumulate=False, stream=None):
         """The table's gradient: row v is scale times the sum of dy over the
-        tokens of id v, in their order."""
+        tokens of id v (in an order that the ids, the sizes and the workspace
+        fix).  accumulate adds to what dtable holds."""
         dev = self.device
         rows, cols = dy.shape
         vocab = dtable.shape[0]

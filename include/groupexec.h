@@ -546,7 +546,8 @@ void tf_layout_destroy(tf_layout* l);
  * extents are at most 2^31 - 65536.  Results do not depend on scheduling: a sum's
  * order is fixed by the sizes, the workspace's among them (and, for the
  * embedding's gradient, by the ids), and a value that is added in memory is added
- * once a launch.
+ * once a launch.  (What memory adds, it may flush: with accumulate = 1, float32
+ * values below the smallest normal one, 2^-126, may count as zero.)
  *
  * A ts_ops handle belongs to the device that is current in ts_create (calls
  * with another current device return FG_EINVAL) and owns a workspace and a
@@ -660,10 +661,12 @@ fg_status ts_embedding(ts_ops* h, const int64_t* ids, int64_t rows, const void* 
 /* Its gradient: row v of dtable [vocab, cols] is scale times the float32 sum of
  * dy's rows with id v, and zeros where there are none; accumulate = 1 adds to
  * what dtable holds and leaves rows without tokens as they are.  Rows of dy
- * whose id is outside the table are not read.  The sum's order depends on the
- * ids and the sizes alone.  Of more than 1024 tokens the workspace
- * holds the sorted list, 8 bytes a token up to 16384 of them and about 18 for
- * more, and a byte a row of the table (FG_EUNSUPPORTED otherwise). */
+ * whose id is outside the table are not read.  A row's tokens are summed by pieces
+ * of the list sorted by id, each in the tokens' order, the pieces in theirs; the
+ * pieces' length depends on the sizes, the workspace's and the number of SMs among
+ * them, and on nothing else.  Of more than 1024 tokens the workspace holds the
+ * sorted list, 8 bytes a token up to 16384 of them and about 18 for more, and a
+ * byte a row of the table (FG_EUNSUPPORTED otherwise). */
 fg_status ts_embedding_backward(ts_ops* h, const int64_t* ids, const void* dy, fg_dtype dy_dtype, int64_t lddy,
                                 int64_t rows, int64_t vocab, int64_t cols, float scale, void* dtable,
                                 fg_dtype d_dtype, int64_t ldd, int32_t accumulate, void* cuda_stream);

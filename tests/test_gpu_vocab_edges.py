@@ -278,3 +278,26 @@ def test_outputs_in_place_of_inputs_are_refused(ops):
             f()
         assert e.value.status == _lib.FG_EINVAL
     ops.sync()
+
+
+# ---- values below the smallest normal float32 ---------------------------------------------------
+
+
+@pytest.mark.parametrize("rows", [40, 3000, 20000])
+def test_embedding_gradient_added_to_small_values(ops, rows):
+    """A sum that is added in memory may be taken as zero, and left as zero, where
+    it is below the smallest normal float32; rows without tokens are kept."""
+    cols, vocab, tiny = 40, 5000, 2.0 ** -126
+    ids = tokens(1, rows, vocab // 2).cuda()
+    dy, old = normal(2, rows, cols).cuda() * tiny, normal(3, vocab, cols).cuda() * tiny
+    d = old.clone()
+    ops.embedding_backward(ids, dy, d, scale=0.5, accumulate=True)
+    ops.sync()
+    inside = (ids >= 0) & (ids < vocab)
+    at, src = ids[inside], dy[inside].double() * 0.5
+    ref = old.double().index_add(0, at, src)
+    n = torch.zeros(vocab, dtype=torch.float64, device="cuda").index_add_(0, at, torch.ones_like(at, dtype=torch.float64))
+    size = old.double().abs().index_add(0, at, src.abs())
+    # three values of an addition in memory, 2^-126 each; additions among subnormals are exact or round by 2^-150
+    within(d, ref, 3 * tiny + (n[:, None] + 4) * 2.0 ** -24 * (size + tiny))
+    assert torch.equal(d[n == 0], old[n == 0])
