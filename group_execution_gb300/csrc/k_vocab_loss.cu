@@ -102,17 +102,18 @@ struct VocabKernel {
 
 // The tensor core truncates as it adds, so that a float32 accumulator's error
 // grows with its products, to one side: 2e-6 of 4096, 1.4e-3 of 524288 of one
-// sign.  So a sum runs over a chain of at most 8 blocks of K for the loss (5e-7),
-// a float32 result, and 16 for the gradients, which sum over all rows or the whole
-// vocabulary (of operands in bf16); the epilogue's threads add what the chains
-// came to in registers, during the next one's MMAs.  (d is rounded to bf16, and its
-// logits' K is a model's width: one chain.  Gradients whose items are a chain at
-// most have a kernel without the registers that several take: 16 x 1024 x 4000
-// 16.8 us, with them 17.9.)
+// sign.  So a sum runs over a chain of at most 8 blocks of K for the logits (5e-7)
+// and 16 for the gradients, which sum over all rows or the whole vocabulary (of
+// operands in bf16); the epilogue's threads add what the chains came to in
+// registers, during the next one's MMAs.  The loss and the gradient cut alike, so
+// that their logits are the same to the bit: a confident row's exp(l - lse) - 1 is
+// as small as it should be, whatever the sums have lost.  (Where all items are a
+// chain at most, the gradient's kernels do without the registers that several
+// take: 16 x 1024 x 4000 16.8 us, with them 17.9.)
 constexpr int kLossChain = 8, kGradChain = 16;
 template <int MODE, bool CHAINS>
 __device__ __forceinline__ int chain_end(int kb0, int kb1) {
-  constexpr int kChain = MODE == kLoss ? kLossChain : kGradChain;
+  constexpr int kChain = MODE == kGrad ? kGradChain : kLossChain;
   return CHAINS && kb1 - kb0 > kChain ? kb0 + kChain : kb1;
 }
 
@@ -543,33 +544,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (row < P.rows)
           P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
       } else if constexpr (MODE == kDlogits) {
-        if (!next_acc()) break;
-#pragma unroll 1
-        for (int j = 0; j < half_n; j += 64) {
+        // 32 columns, from j on, into the stage; 64 of it leave
+        auto turn = [&](float (&u)[32], int j) {
+          const int cc = c0 + j, left = P.vocab - cc, at = target - cc;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float v[32];
-            tmem_ld32(acc + j + 32 * k, v);
-            if (j + 64 == half_n && k == 1) release();
-            const int cc = c0 + j + 32 * k, left = P.vocab - cc, at = target - cc;
+          for (int c = 0; c < 32; ++c) u[c] = exp2_approx(fmaf(u[c] - lse, kLog2e, shift));
+          if (at >= 0 && at < 32) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = exp2_approx(fmaf(v[c] - lse, kLog2e, shift));
-            if (at >= 0 && at < 32) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) v[c] -= c == at ? g : 0.f;
-            }
-            if (left < 32) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c >= left) v[c] = 0.f;
-            }
-            if (k == 0) stage_free();
-            stage.put_bf16(lane, k, v, sign, keep);
+            for (int c = 0; c < 32; ++c) u[c] -= c == at ? g : 0.f;
           }
+          if (left < 32) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c >= left) u[c] = 0.f;
+          }
+          if (j % 64 == 0) stage_free();
+          stage.put_bf16(lane, j / 32 & 1, u, sign, keep);
+        };
+        auto send = [&](int j) {
           stage_full();
           if (lane == 0) {
             if (r0 < P.rows) tma_store_2d(&P.store_d, c0 + j, r0, stage_u32);
             bulk_commit();
+          }
+        };
+        if constexpr (CHAINS) {
+          float v[4][32];
+          collect(v);
+          if (!ok) break;
+          turn(v[0], 0);
+          turn(v[1], 32);
+          send(0);
+          if (half_n > 64) {
+            turn(v[2], 64);
+            turn(v[3], 96);
+            send(64);
+          }
+        } else {
+          if (!next_acc()) break;
+#pragma unroll 1
+          for (int j = 0; j < half_n; j += 64) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float u[32];
+              tmem_ld32(acc + j + 32 * k, u);
+              if (j + 64 == half_n && k == 1) release();
+              turn(u, j + 32 * k);
+            }
+            send(j);
           }
         }
       } else {
@@ -807,8 +829,9 @@ cudaError_t resident_pairs(int device, int* out) {
   static std::atomic<int> cached[64];
   int n = device < 64 ? cached[device].load(std::memory_order_acquire) : 0;
   if (!n) {
-    const void* kernels[4] = {(const void*)ts_vocab_kernel<kLoss, true>, (const void*)ts_vocab_kernel<kDlogits, false>,
-                              (const void*)ts_vocab_kernel<kGrad, false>, (const void*)ts_vocab_kernel<kGrad, true>};
+    const void* kernels[5] = {(const void*)ts_vocab_kernel<kLoss, true>, (const void*)ts_vocab_kernel<kDlogits, false>,
+                              (const void*)ts_vocab_kernel<kDlogits, true>, (const void*)ts_vocab_kernel<kGrad, false>,
+                              (const void*)ts_vocab_kernel<kGrad, true>};
     for (const void* k : kernels) {
       const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
       if (e != cudaSuccess) return e;
@@ -1173,7 +1196,9 @@ cudaError_t launch_vocab_loss_backward(const ts_ops& h, const VocabLossArgs& a, 
       if (e == cudaSuccess) e = make_map(&P.w, w.p, 1, a.cols, nv, w.ld, 64, P.tile_n / 2);
       if (e == cudaSuccess) e = make_map(&P.store_d, d, 1, dpitch, a.rows, dpitch, 64, 32);
       if (e != cudaSuccess) return e;
-      e = launch_product<kDlogits, false>(P, std::min<int64_t>(pairs, tiles_t * P.tiles_v), st);
+      const int64_t np = std::min<int64_t>(pairs, tiles_t * P.tiles_v);
+      e = a.cols > kLossChain * kKB ? launch_product<kDlogits, true>(P, np, st)
+                                    : launch_product<kDlogits, false>(P, np, st);
       P.copy.units = 0;
     }
     if (e == cudaSuccess && a.dw.p) {

@@ -119,6 +119,31 @@ def test_loss_of_confident_rows(ops, rows, vocab, far):
     within(lse, a.double().cuda() + torch.log1p(rest), error + 2.0 ** -24 * (a.double().cuda() + 1))
 
 
+@pytest.mark.parametrize("rows, cols, vocab", [(40, 8192, 300), (300, 2056, 5003), (9, 8192, 300)])
+def test_gradient_of_confident_rows(ops, rows, cols, vocab):
+    """The target's logit is a sum of one sign, far above the others: whatever the
+    tensor core loses of it, the gradient is that of the loss, here nothing."""
+    gen = torch.Generator().manual_seed(0)
+    x = matrix(1 + torch.rand((rows, cols), generator=gen), BF16, -cols % 8)
+    w = torch.zeros((vocab, cols))
+    w[vocab // 3] = (1 + torch.rand(cols, generator=gen)) * (40 / 2.25 / cols)
+    w = matrix(w, BF16, -cols % 8)
+    targets = torch.full((rows,), vocab // 3).cuda()
+    loss, lse, g = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda"), torch.ones(rows, device="cuda")
+    ops.linear_cross_entropy(x, w, targets, loss, lse)
+    dx, dw = output(rows, cols), output(vocab, cols)
+    ops.linear_cross_entropy_backward(x, w, targets, lse, g, dx, dw)
+    ops.sync()
+    xd, wd = x.double(), w.double()
+    d = torch.softmax(xd @ wd.t(), 1)
+    d[:, vocab // 3] -= 1.0
+    # of d: lse's rounding at its size and an exponential's 2^-21, and one rounding to bf16
+    off = 2.0 ** -8 * d.abs() + 2.0 ** -21 + 2.0 ** -23 * lse.double()[:, None].abs()
+    off[:, torch.arange(vocab) != vocab // 3] = 1e-12        # (e^-38 of the others)
+    within(dx, d @ wd, off @ wd.abs())
+    within(dw, d.t() @ xd, off.t() @ xd.abs())
+
+
 # ---- sums longer than one accumulator ----------------------------------------------------
 
 # An MMA adds 16 products to its accumulator, and each of the 17 may lose 2^-24 of
