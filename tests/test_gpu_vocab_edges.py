@@ -326,3 +326,29 @@ def test_embedding_gradient_added_to_small_values(ops, rows):
     # three values of an addition in memory, 2^-126 each; additions among subnormals are exact or round by 2^-150
     within(d, ref, 3 * tiny + (n[:, None] + 4) * 2.0 ** -24 * (size + tiny))
     assert torch.equal(d[n == 0], old[n == 0])
+
+
+# ---- waits --------------------------------------------------------------------------------------
+
+
+def test_waits_that_run_out_between_chains():
+    """Without its copies every wait of a product over several chains expires, the
+    call reports it and the next one is right."""
+    ops = TrainingOps(wait_limit_ns=1_000_000, flags=_lib.FG_FLAG_INJECT_NO_LOADS)
+    rows, cols, vocab = 2500, 1100, 5000
+    x, w = matrix(normal(1, rows, cols), BF16, 4), matrix(normal(2, vocab, cols, scale=0.05), BF16, 4)
+    targets = tokens(3, rows, vocab).cuda()
+    lse = torch.logsumexp(x.double() @ w.double().t(), 1).float()
+    g = (normal(4, rows) / rows).cuda()
+    got, loss = torch.empty(rows, device="cuda"), torch.empty(rows, device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    for call in (lambda: ops.linear_cross_entropy(x, w, targets, loss, got),
+                 lambda: ops.linear_cross_entropy_backward(x, w, targets, lse, g, dx, dw)):
+        call()
+        with pytest.raises(FgError) as e:
+            ops.sync()
+        assert e.value.status == _lib.FG_ETIMEOUT
+    _lib.check(ops.lib.ts_set_wait_limit(ops.h, 2_000_000_000, 0))
+    x[(targets < 0) | (targets >= vocab)] = 0.0
+    dx, dw = run_backward(ops, x, w, targets, lse, g, None, BF16, F32, 4, 0)
+    check_backward(x, w, targets, lse, g, None, dx, dw)
