@@ -530,7 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 32; ++c) l = 32 * j + c == at ? v[j][c] : l;
           P.tlogit[row] = l;
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {};
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        F2 sum[2] = {};
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -540,15 +541,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < 32; ++c) sum[c & 3] += exp2_approx((v[j][c] - ref) * kLog2e);
+          for (int c = 0; c < 32; c += 2) {
+            const F2 e = mul2(add2(pack2f(v[j][c], v[j][c + 1]), pack2f(-ref, -ref)), pack2f(kLog2e, kLog2e));
+            float a, b;
+            unpack2f(e, a, b);
+            sum[c / 2 & 1] = add2(sum[c / 2 & 1], pack2f(exp2_approx(a), exp2_approx(b)));
+          }
         if (row < P.rows)
-          P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+          P.part[(int64_t)(c0 / half_n) * P.rows + row] = make_float2(m, sum2(sum[0]) + sum2(sum[1]));
       } else if constexpr (MODE == kDlogits) {
         // 32 columns, from j on, into the stage; 64 of it leave
         auto turn = [&](float (&u)[32], int j) {
           const int cc = c0 + j, left = P.vocab - cc, at = target - cc;
 #pragma unroll
-          for (int c = 0; c < 32; ++c) u[c] = exp2_approx(fmaf(u[c] - lse, kLog2e, shift));
+          for (int c = 0; c < 32; c += 2) {
+            const F2 e = fma2(add2(pack2f(u[c], u[c + 1]), pack2f(-lse, -lse)), pack2f(kLog2e, kLog2e),
+                              pack2f(shift, shift));
+            float a, b;
+            unpack2f(e, a, b);
+            u[c] = exp2_approx(a);
+            u[c + 1] = exp2_approx(b);
+          }
           if (at >= 0 && at < 32) {
 #pragma unroll
             for (int c = 0; c < 32; ++c) u[c] -= c == at ? g : 0.f;
