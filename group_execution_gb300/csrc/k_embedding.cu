@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) ts_embed_sum_kernel(const __grid_
 // The ids whose tokens lie in more than one chunk, as the kernel before has
 // noted them (in any order: each is summed by itself, its chunks in order).  A
 // warp takes 64 columns, so that an id of many chunks has many warps: at 65536
-// tokens the most frequent id has 190 chunks.
+// tokens the most frequent id has about 75 chunks.
 constexpr int kJoinCols = 64;
 
 template <class U, bool VEC, bool ACC>

@@ -98,26 +98,26 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
   float m[2], sum[2], lse[2], coef[2], gl[2];
   int target[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int row = r * 8 + g;
-      m[r] = -INFINITY;
-      sum[r] = lse[r] = coef[r] = gl[r] = 0.f;
-      target[r] = -1;
-      if (row < P.rows && P.targets) {
-        const int64_t i = P.targets[row];
-        if (i >= 0 && i < P.vocab) target[r] = (int)i;
-      }
-      if constexpr (BACK) {
-        if (row < P.rows) {
-          // (a row of -inf logits takes no gradient)
-          const float l = P.lse_in[row];
-          const bool none = l == -INFINITY;
-          lse[r] = none ? 0.f : l;
-          gl[r] = target[r] >= 0 && !none ? P.g_loss[row] : 0.f;
-          coef[r] = gl[r] + (P.g_lse && !none ? P.g_lse[row] : 0.f);
-        }
+  for (int r = 0; r < 2; ++r) {
+    const int row = r * 8 + g;
+    m[r] = -INFINITY;
+    sum[r] = lse[r] = coef[r] = gl[r] = 0.f;
+    target[r] = -1;
+    if (row < P.rows && P.targets) {
+      const int64_t i = P.targets[row];
+      if (i >= 0 && i < P.vocab) target[r] = (int)i;
+    }
+    if constexpr (BACK) {
+      if (row < P.rows) {
+        // (a row of -inf logits takes no gradient)
+        const float l = P.lse_in[row];
+        const bool none = l == -INFINITY;
+        lse[r] = none ? 0.f : l;
+        gl[r] = target[r] >= 0 && !none ? P.g_loss[row] : 0.f;
+        coef[r] = gl[r] + (P.g_lse && !none ? P.g_lse[row] : 0.f);
       }
     }
+  }
   for (int tile0 = blockIdx.x * per_block; tile0 < P.tiles; tile0 += gridDim.x * per_block) {   // (uniform)
     const int tile = tile0 + group, v0 = tile * kTileV;
     float tot[2][4] = {};
@@ -131,11 +131,11 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
         wrow[n] = P.w + (int64_t)(win[n] ? v0 + n * 8 + g : 0) * P.ldw;
       }
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = r * 8 + g;
-          xin[r] = row < P.rows;
-          xrow[r] = P.x + (int64_t)(xin[r] ? row : 0) * P.ldx;
-        }
+      for (int r = 0; r < 2; ++r) {
+        const int row = r * 8 + g;
+        xin[r] = row < P.rows;
+        xrow[r] = P.x + (int64_t)(xin[r] ? row : 0) * P.ldx;
+      }
       struct Batch {
         uint4 w[kBatch][2];
       };
@@ -171,12 +171,12 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
       };
       auto flush = [&]() {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              tot[n][i] += acc[n][i];
-              acc[n][i] = 0.f;
-            }
+          for (int i = 0; i < 4; ++i) {
+            tot[n][i] += acc[n][i];
+            acc[n][i] = 0.f;
+          }
       };
       Batch b0, b1;
       load(b0, s0);
@@ -196,68 +196,68 @@ __global__ void __launch_bounds__(kThreads, 2) ts_few_kernel(const __grid_consta
     if (P.ksplit > 1) {
       if (kp) {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sums[warp][n][lane][i] = tot[n][i];
+          for (int i = 0; i < 4; ++i) sums[warp][n][lane][i] = tot[n][i];
       }
       __syncthreads();
       if (kp == 0) {
         for (int k = 1; k < P.ksplit; ++k)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < 2; ++n)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) tot[n][i] += sums[warp + k][n][lane][i];
+            for (int i = 0; i < 4; ++i) tot[n][i] += sums[warp + k][n][lane][i];
       }
       __syncthreads();
     }
     if (kp || tile >= P.tiles) continue;
     // a thread holds columns v0 + n * 8 + 2 q, + 1 of its rows
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = r * 8 + g;
-        float l[4] = {tot[0][2 * r], tot[0][2 * r + 1], tot[1][2 * r], tot[1][2 * r + 1]};
-        if constexpr (BACK) {
-          const bool none = coef[r] == 0.f && gl[r] == 0.f;
+    for (int r = 0; r < 2; ++r) {
+      const int row = r * 8 + g;
+      float l[4] = {tot[0][2 * r], tot[0][2 * r + 1], tot[1][2 * r], tot[1][2 * r + 1]};
+      if constexpr (BACK) {
+        const bool none = coef[r] == 0.f && gl[r] == 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int v = v0 + (i >> 1) * 8 + 2 * q + (i & 1);
-            l[i] = coef[r] * exp2_approx((l[i] - lse[r]) * kLog2e);
-            if (v == target[r]) l[i] -= gl[r];
-            if (none || v >= P.vocab) l[i] = 0.f;
-          }
-          if (row < P.rows) {
-            __nv_bfloat16* d = P.d + row * P.dpitch + v0 + 2 * q;
-            *reinterpret_cast<uint32_t*>(d) = bf16x2(l[0], l[1]);
-            *reinterpret_cast<uint32_t*>(d + 8) = bf16x2(l[2], l[3]);
-          }
-        } else {
-          float top = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int v = v0 + (i >> 1) * 8 + 2 * q + (i & 1);
-            if (v >= P.vocab) l[i] = -INFINITY;
-            else if (v == target[r]) P.tlogit[row] = l[i];
-            top = fmaxf(top, l[i]);
-          }
-          const float next = fmaxf(m[r], top), ref = next == -INFINITY ? 0.f : next;
-          float s = 0.f;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s += exp2_approx((l[i] - ref) * kLog2e);
-          sum[r] = sum[r] * exp2_approx((m[r] - ref) * kLog2e) + s;
-          m[r] = next;
+        for (int i = 0; i < 4; ++i) {
+          const int v = v0 + (i >> 1) * 8 + 2 * q + (i & 1);
+          l[i] = coef[r] * exp2_approx((l[i] - lse[r]) * kLog2e);
+          if (v == target[r]) l[i] -= gl[r];
+          if (none || v >= P.vocab) l[i] = 0.f;
         }
+        if (row < P.rows) {
+          __nv_bfloat16* d = P.d + row * P.dpitch + v0 + 2 * q;
+          *reinterpret_cast<uint32_t*>(d) = bf16x2(l[0], l[1]);
+          *reinterpret_cast<uint32_t*>(d + 8) = bf16x2(l[2], l[3]);
+        }
+      } else {
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int v = v0 + (i >> 1) * 8 + 2 * q + (i & 1);
+          if (v >= P.vocab) l[i] = -INFINITY;
+          else if (v == target[r]) P.tlogit[row] = l[i];
+          top = fmaxf(top, l[i]);
+        }
+        const float next = fmaxf(m[r], top), ref = next == -INFINITY ? 0.f : next;
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += exp2_approx((l[i] - ref) * kLog2e);
+        sum[r] = sum[r] * exp2_approx((m[r] - ref) * kLog2e) + s;
+        m[r] = next;
       }
+    }
   }
   if constexpr (!BACK) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
+    for (int r = 0; r < 2; ++r) {
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-          const float om = __shfl_xor_sync(0xffffffffu, m[r], o), os = __shfl_xor_sync(0xffffffffu, sum[r], o);
-          join_sums(m[r], sum[r], om, os);
-        }
-        if (q == 0) rows_sm[warp][r * 8 + g] = make_float2(m[r], sum[r]);
+      for (int o = 1; o < 4; o <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m[r], o), os = __shfl_xor_sync(0xffffffffu, sum[r], o);
+        join_sums(m[r], sum[r], om, os);
       }
+      if (q == 0) rows_sm[warp][r * 8 + g] = make_float2(m[r], sum[r]);
+    }
     __syncthreads();
     if ((int)threadIdx.x < P.rows) {
       float bm = -INFINITY, bs = 0.f;

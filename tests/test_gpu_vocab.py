@@ -188,8 +188,8 @@ def loss_bounds(x, w, lse):
 
 # one of each; less than a tile, ragged tiles, more than one slot of K; rows
 # of more than a group of tiles; every pair with more than two tiles
-# (rows up to 32 have kernels of their own: one and two tiles of rows, K cut over
-# warps or not, more tiles than warps)
+# (up to 16 rows of small weights have a kernel of their own: K cut over warps or
+# not, more tiles than warps)
 LOSS = [(1, 1, 1), (1, 64, 100), (3, 16, 257), (16, 1024, 3000), (17, 1003, 700), (32, 2056, 50), (8, 40, 60001),
         (31, 264, 45000), (33, 130, 5003), (100, 1024, 3000), (256, 128, 256), (257, 64, 511),
         (512, 256, 4000), (1000, 1003, 777), (4500, 96, 2500), (700, 520, 20011)]
