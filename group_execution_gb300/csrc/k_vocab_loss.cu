@@ -1,6 +1,6 @@
 // Softmax cross entropy of a linear layer over a vocabulary, l = x w^T, and its
-// gradients, in pieces of the vocabulary: the logits [rows, vocab] are never
-// kept.
+// gradients.  The logits [rows, vocab] are never kept; the gradient keeps d, in
+// bf16, of as much of the vocabulary as the workspace holds.
 //
 //   lse_t = log sum_v exp l_tv, loss_t = lse_t - l_t,target
 //   d_tv = (g_t + h_t) exp(l_tv - lse_t) - g_t [v = target_t]
@@ -28,11 +28,12 @@
 //   warp 3      copies x for dw beside the first piece's logits, where that hides it,
 //   warps 4-11  epilogue: a thread owns half of one row of the CTA's 128 x 256
 //               accumulator; it overlaps the next tile's MMAs.
-// At 4096 x 1024 x 50001 the tensor pipe is active in 95 % of the cycles of the
-// loss (206 us, 2.04 PFLOP/s in a single run; 243 in a series of calls, at the
-// power limit), 82 % of the gradient's logits, 93 % of dx and dw (770 us together).
-// 8192 x 4096 x 50001 takes 1840 and 5820 us, 1.82 and 1.73 PFLOP/s.  Few rows are
-// bound by the weight's bytes: 64 x 4096 x 32000 52 us forward (5.0 TB/s), 157
+// At 4096 x 1024 x 50001 the tensor pipe is active in 96 % of the cycles of the
+// loss (213 us, 1.97 PFLOP/s in a single run; 245 to 253 in a series of calls, at the
+// power limit), 83 % of the gradient's logits, 91 % of dx and dw (790 us together).
+// 8192 x 4096 x 50001 takes 1850 to 1905 and 5900 to 6005 us, 1.76 to 1.81 and 1.68
+// to 1.71 PFLOP/s, d of the whole vocabulary (822 MB) in the workspace.  Few rows are
+// bound by the weight's bytes: 64 x 4096 x 32000 50 us forward (5.3 TB/s), 161
 // backward.  Models of 256 columns or fewer are bound by the epilogue.
 //
 // Every wait is bounded; on expiry the CTA records the error, the pair waits
