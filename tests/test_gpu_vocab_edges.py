@@ -99,7 +99,7 @@ def test_loss_of_confident_rows(ops, rows, vocab, far):
     """The target's logit is a, the others' are far below: the loss is as near to
     its value whatever a is, and never negative."""
     a = torch.arange(rows) % 30 * 4.0 + 4.0
-    a[rows // 2:] *= 256.0                                   # up to 30720
+    a[rows // 2:] *= 256.0
     c = -far + torch.arange(vocab) % 8 * 0.25                # (of eight bits, like a: exact in bf16, a + c in float32)
     t = vocab // 3
     c[t] = 0.0
@@ -112,7 +112,8 @@ def test_loss_of_confident_rows(ops, rows, vocab, far):
     ops.sync()
     rest = torch.exp(c.double().cuda()).sum() - 1.0          # beside the target's 1
     want = torch.log1p(rest) - c.double().cuda()[targets]
-    # the others' exponentials and arguments, about 60 + vocab / 1024 additions, the logarithm's and the loss's roundings
+    # the others' exponentials and arguments, about 60 + vocab / 1024 additions, the
+    # logarithm's and the loss's roundings
     error = 2.0 ** -20 * rest / (1 + rest) + 2.0 ** -24 * (60 + vocab / 1024) + 2.0 ** -22 * torch.log1p(rest)
     within(loss, want, error + 2.0 ** -24 * want)
     assert (loss >= 0).all()
@@ -272,7 +273,7 @@ def test_outputs_in_place_of_inputs_are_refused(ops):
         return torch.as_strided(buf.view(dtype), (rows, cols), (ld, 1))
 
     x, w = torch.zeros((4, 64), dtype=BF16, device="cuda"), torch.zeros((9, 64), dtype=BF16, device="cuda")
-    ids, v, u = torch.zeros(4, dtype=torch.int64, device="cuda"), torch.zeros(4, device="cuda"), torch.zeros(4, device="cuda")
+    ids, v, u = torch.zeros(4, dtype=torch.int64, device="cuda"), *torch.zeros((2, 4), device="cuda")
     xs, ws, vs = at(4, 64, BF16, 64), at(9, 64, BF16, 64), buf[:4]
     ls = buf[:8].view(torch.int64)
     back = ops.linear_cross_entropy_backward

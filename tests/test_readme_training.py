@@ -42,12 +42,14 @@ def test_the_sequence_runs():
     names = dict(
         vocab=VOCAB, width=WIDTH, x=torch.randn((ROWS, WIDTH), device="cuda").to(torch.bfloat16),
         gamma=torch.ones(WIDTH, **f32), beta=torch.zeros(WIDTH, **f32), y=torch.empty((ROWS, WIDTH), **bf16),
-        mean=torch.empty(ROWS, **f32), rstd=torch.empty(ROWS, **f32), dy=torch.randn((ROWS, WIDTH), device="cuda").to(torch.bfloat16),
+        mean=torch.empty(ROWS, **f32), rstd=torch.empty(ROWS, **f32),
+        dy=torch.randn((ROWS, WIDTH), device="cuda").to(torch.bfloat16),
         dw=torch.empty((WIDTH, WIDTH), **f32), db=torch.empty(WIDTH, **f32), logits=torch.randn((ROWS, VOCAB), **f32),
         tokens=ids, logprob=torch.empty(ROWS, **f32), entropy=torch.empty(ROWS, **f32), lse=torch.empty(ROWS, **f32),
         top_logprob=torch.empty((ROWS, 20), **f32), top_id=torch.empty((ROWS, 20), device="cuda", dtype=torch.int32),
         ids=ids, table=(torch.randn((VOCAB, WIDTH), device="cuda") / WIDTH ** 0.5).to(torch.bfloat16), targets=targets,
-        loss=torch.empty(ROWS, **f32), g_loss=torch.full((ROWS,), 1.0 / ROWS, **f32), dx=torch.empty((ROWS, WIDTH), **bf16),
+        loss=torch.empty(ROWS, **f32), g_loss=torch.full((ROWS,), 1.0 / ROWS, **f32),
+        dx=torch.empty((ROWS, WIDTH), **bf16),
         dtable=torch.empty((VOCAB, WIDTH), **f32))
     exec(printed(), names)
     for out in ("y", "dw", "db", "logprob", "loss", "dx", "dtable"):
